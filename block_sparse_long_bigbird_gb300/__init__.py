@@ -21,6 +21,18 @@ from ._lib import (  # noqa: F401
     SA_OPT_WAIT_LIMIT,
     SparseAttnError,
 )
+from .paged import (  # noqa: F401
+    cache_append,
+    cache_compact,
+    cache_copy_pages,
+    cache_fork,
+    cache_free,
+    cache_reserve,
+    cache_trim,
+    cache_workspace_bytes,
+    longformer_attn_paged_fwd,
+    paged_workspace_bytes,
+)
 
 _DTYPE = {torch.bfloat16: SA_BF16, torch.float32: SA_FP32}
 

@@ -18,9 +18,10 @@ SA_ERR_UNSUPPORTED = 2
 SA_ERR_CUDA = 3
 SA_ERR_TIMEOUT = 4
 SA_ERR_BAD_INDEX = 5
+SA_ERR_NO_PAGES = 6
 STATUS_NAMES = {
     0: "SA_OK", 1: "SA_ERR_INVALID_ARG", 2: "SA_ERR_UNSUPPORTED", 3: "SA_ERR_CUDA",
-    4: "SA_ERR_TIMEOUT", 5: "SA_ERR_BAD_INDEX",
+    4: "SA_ERR_TIMEOUT", 5: "SA_ERR_BAD_INDEX", 6: "SA_ERR_NO_PAGES",
 }
 
 SA_BF16 = 0
@@ -35,6 +36,7 @@ SA_OPT_CHUNK_KEYS = 5
 # Exported symbol -> (restype, argtypes).
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
+_SZ = ctypes.c_size_t
 SIGNATURES = {
     "build_bigbird_pattern": (_I, [ctypes.c_uint64, _I, _I, _I, _I, _I, _I, _VP]),
     "bigbird_attn_fwd": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _I, _VP, _VP, _I, _VP]),
@@ -59,6 +61,16 @@ SIGNATURES = {
     "sa_last_launch_count": (_I, []),
     "bigbird_attn_fwd_noalloc": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _I, _VP, _VP, _VP]),
     "sa_check_wait_expiry": (_I, [ctypes.c_int64, _VP]),
+    "longformer_attn_paged_fwd": (_I, [_VP] * 4 + [_I] * 8 + [_VP] * 3 + [_I, _VP, _VP, _I, _VP, _SZ, _I, _VP]),
+    "sa_longformer_paged_workspace_bytes": (_SZ, [_I] * 8),
+    "sa_cache_append": (_I, [_VP] * 4 + [_I] * 7 + [_VP] * 3 + [_I, _VP]),
+    "sa_cache_workspace_bytes": (_SZ, [_I, _I]),
+    "sa_cache_copy_pages": (_I, [_VP, _VP, _I, _I, _SZ, _VP, _VP, _I, _VP]),
+    "sa_cache_fork": (_I, [_VP, _VP, _I, _I, _SZ, _I, _I, _I, _VP, _VP, _I] + [_VP] * 7 + [_SZ, _VP]),
+    "sa_cache_free": (_I, [_I, _I, _I, _VP, _I] + [_VP] * 7),
+    "sa_cache_trim": (_I, [_I] * 5 + [_VP, _I] + [_VP] * 6),
+    "sa_cache_reserve": (_I, [_I] * 4 + [_VP] * 7 + [_SZ, _VP]),
+    "sa_cache_compact": (_I, [_VP, _VP, _I, _I, _SZ, _I, _I] + [_VP] * 5 + [_SZ, _VP]),
 }
 NOALLOC_SCRATCH_BYTES = 16 << 20
 

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "paged.h"
 #include "tc_sync.cuh"
 
 namespace {
@@ -397,6 +398,27 @@ sa_status run_host(const sa::Problem &hp, sa_dtype dtype, cudaStream_t s) {
 
 }  // namespace
 
+namespace sa {
+
+sa_status api_device(unsigned **status, int *num_sms) {
+    int dev = 0;
+    DeviceState *st = nullptr;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    const sa_status s = current_device(&dev, &st);
+    if (s != SA_OK) return s;
+    if (st->cc_major != 10 || st->cc_minor != 3) return SA_ERR_UNSUPPORTED;
+    *status = st->status;
+    *num_sms = st->num_sms;
+    return SA_OK;
+}
+
+void api_set_launches(int n) { g_last_launches = n; }
+bool api_force_simt() { return g_force_simt.load() != 0; }
+unsigned long long api_wait_ns() { return (unsigned long long)g_wait_limit.load() * 1000ull; }
+int api_grid_ctas() { return g_grid_ctas.load(); }
+
+}  // namespace sa
+
 extern "C" {
 
 sa_status bigbird_attn_fwd(const void *Q, const void *K, const void *V, void *O, int B, int H, int n, int d,
@@ -655,6 +677,7 @@ sa_status sa_get_last_device_status(sa_stream_t stream) {
         return SA_ERR_TIMEOUT;
     }
     if (word & sa::kDevBadIndex) return SA_ERR_BAD_INDEX;
+    if (word & sa::kDevNoPages) return SA_ERR_NO_PAGES;
     return SA_OK;
 }
 
@@ -666,6 +689,7 @@ const char *sa_status_string(sa_status status) {
         case SA_ERR_CUDA: return "SA_ERR_CUDA";
         case SA_ERR_TIMEOUT: return "SA_ERR_TIMEOUT";
         case SA_ERR_BAD_INDEX: return "SA_ERR_BAD_INDEX";
+        case SA_ERR_NO_PAGES: return "SA_ERR_NO_PAGES";
     }
     return "SA_ERR_UNKNOWN";
 }

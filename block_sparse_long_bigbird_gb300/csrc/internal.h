@@ -17,6 +17,7 @@ constexpr int kMaxDilation = 63;
 enum DeviceStatusBits : unsigned int {
     kDevTimeout = 1u << 0,
     kDevBadIndex = 1u << 1,
+    kDevNoPages = 1u << 2,
 };
 
 // One attention call, as validated by the host API.

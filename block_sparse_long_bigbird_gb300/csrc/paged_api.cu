@@ -1,0 +1,312 @@
+// Host side of the paged cache's entry points: argument checks, the choice of
+// kernel, scratch sizes and launches. Nothing is kept between calls.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "internal.h"
+#include "paged.h"
+
+namespace sa {
+
+// At most this many query rows of a key head go to the kernel that streams the
+// cache with the ordinary units.
+static int rows_limit(sa_dtype dtype) { return dtype == SA_FP32 ? 8 : 4; }
+
+PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, int num_sms) {
+    p.group = p.Hq / p.Hkv;
+    p.log_page = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
+    p.scale_log2 = 1.4426950408889634f / sqrtf((float)p.d);
+    const long long rows = (long long)p.m * p.group;
+    if (rows <= rows_limit(dtype)) {
+        p.tpt = p.tpt_half = p.m;
+        p.rows = (int)rows;
+        p.target = 4 * num_sms;
+        p.min_split = 4;
+        return kPagedRows;
+    }
+    const int most = 64 / p.group;
+    p.tpt = p.tpt_half = p.m < most ? p.m : most;
+    p.rows = p.tpt * p.group;
+    p.target = 4 * num_sms;
+    p.min_split = 4;
+    return kPagedTile;
+}
+
+// The plan (paged_common.cuh) cuts a sweep of e blocks into ceil(e / len)
+// pieces only if e > len, with len >= (sum of e) / target: the pieces of cut
+// sweeps are fewer than 2 * target. No sweep is longer than its table row.
+static bool may_split(const PagedProblem &p) {
+    return ((long long)p.max_pages << p.log_page) > 64ll * p.min_split;
+}
+
+size_t paged_workspace_bytes(const PagedProblem &p) {
+    if (!may_split(p)) return 0;
+    return 2 * (size_t)p.target * p.rows * (p.d + 2) * sizeof(float);
+}
+
+}  // namespace sa
+
+namespace {
+
+bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+// Sizes of the attention and the append; the limits come after the contract.
+sa_status sizes_ok(int B, int Hkv, int m, int d, int page, int num_pages, int max_pages) {
+    if (B < 1 || Hkv < 1 || m < 1 || num_pages < 1 || max_pages < 1) return SA_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || !page_ok(page)) return SA_ERR_INVALID_ARG;
+    if (B > sa::kPagedMaxBatch || (long long)max_pages * page > sa::kPagedMaxLen) return SA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * Hkv > 0x7fffffffll || (long long)B * Hkv * m > 0x3fffffffll) return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+sa_status finish(cudaError_t e, int launches) {
+    if (e == cudaErrorNotSupported) return SA_ERR_UNSUPPORTED;
+    if (e != cudaSuccess) return SA_ERR_CUDA;
+    sa::api_set_launches(launches);
+    return SA_OK;
+}
+
+// Sizes and pointers that the bookkeeping calls share.
+sa_status pool_ok(const void *K, const void *V, int layers, int num_pages, size_t page_bytes) {
+    if (!K || !V || K == V || !al16(K) || !al16(V)) return SA_ERR_INVALID_ARG;
+    if (layers < 1 || num_pages < 1 || page_bytes == 0 || (page_bytes & 15u)) return SA_ERR_INVALID_ARG;
+    if (page_bytes > (1ull << 40) / (size_t)num_pages || layers > (1 << 16)) return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+sa_status tables_ok(int B, int max_pages, int num_pages, const void *a, const void *b, const void *c, const void *d) {
+    if (B < 1 || max_pages < 1 || num_pages < 1) return SA_ERR_INVALID_ARG;
+    if (!a || !b || !c || !d || !al4(a) || !al4(b) || !al4(c) || !al4(d)) return SA_ERR_INVALID_ARG;
+    if (B > sa::kPagedMaxBatch) return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+sa_status ws_ok(const void *ws, size_t bytes, size_t need) {
+    return ws && al16(ws) && bytes >= need ? SA_OK : SA_ERR_INVALID_ARG;
+}
+
+int log2_page(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+}  // namespace
+
+extern "C" {
+
+sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const void *V_pages, void *O, int B, int Hq,
+                                    int Hkv, int m, int d, int page, int num_pages, int max_pages,
+                                    const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                                    int window, const int32_t *dilation, const int32_t *global_idx, int n_global,
+                                    void *workspace, size_t workspace_bytes, sa_dtype dtype, sa_stream_t stream) {
+    if (dtype != SA_BF16 && dtype != SA_FP32) return SA_ERR_INVALID_ARG;
+    if (!Q || !K_pages || !V_pages || !O || !al16(Q) || !al16(K_pages) || !al16(V_pages) || !al16(O))
+        return SA_ERR_INVALID_ARG;
+    if (O == Q || O == K_pages || O == V_pages) return SA_ERR_INVALID_ARG;
+    if (!block_table || !seq_lens || !al4(block_table) || !al4(seq_lens) || !al4(q_lens) || !al4(dilation) ||
+        !al4(global_idx))
+        return SA_ERR_INVALID_ARG;
+    if (window < 0 || (window & 1) || n_global < 0 || (n_global > 0 && !global_idx)) return SA_ERR_INVALID_ARG;
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return SA_ERR_INVALID_ARG;
+    sa_status s = sizes_ok(B, Hkv, m, d, page, num_pages, max_pages);
+    if (s != SA_OK) return s;
+    if (Hq / Hkv > sa::kPagedMaxGroup || n_global > sa::kPagedMaxGlobal || (long long)B * Hq > (1ll << 30))
+        return SA_ERR_UNSUPPORTED;
+    sa::PagedProblem p = {};
+    int sms = 0;
+    s = sa::api_device(&p.status, &sms);
+    if (s != SA_OK) return s;
+    p.Q = Q; p.K = K_pages; p.V = V_pages; p.O = O;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.m = m; p.d = d;
+    p.page = page; p.num_pages = num_pages; p.max_pages = max_pages;
+    p.table = block_table; p.lens = seq_lens; p.qlens = q_lens;
+    p.half = window / 2;
+    p.dilation = dilation;
+    p.gidx = n_global > 0 ? global_idx : nullptr;
+    p.ng = n_global;
+    p.wait_ns = sa::api_wait_ns();
+    const sa::PagedKernel kind = sa::paged_shape(p, dtype, sms);
+    const size_t need = sa::paged_workspace_bytes(p);
+    if (need) {
+        if (ws_ok(workspace, workspace_bytes, need) != SA_OK) return SA_ERR_INVALID_ARG;
+        p.part_o = static_cast<float *>(workspace);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + 2 * (size_t)p.target * p.rows * p.d);
+    }
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = kind == sa::kPagedRows ? sa::launch_paged_rows(p, dtype, sms, cs)
+                                           : sa::launch_paged_tile(p, dtype, sms, cs);
+    if (e == cudaSuccess && need) e = sa::launch_paged_merge(p, dtype, sms, cs);
+    return finish(e, need ? 2 : 1);
+}
+
+size_t sa_longformer_paged_workspace_bytes(int B, int Hq, int Hkv, int m, int d, int page, int max_pages,
+                                           sa_dtype dtype) {
+    if ((dtype != SA_BF16 && dtype != SA_FP32) || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
+        Hq / Hkv > sa::kPagedMaxGroup || sizes_ok(B, Hkv, m, d, page, 1, max_pages) != SA_OK)
+        return 0;
+    unsigned *status = nullptr;
+    int sms = 0;
+    if (sa::api_device(&status, &sms) != SA_OK) return 0;
+    sa::PagedProblem p = {};
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.m = m; p.d = d; p.page = page; p.max_pages = max_pages;
+    sa::paged_shape(p, dtype, sms);
+    return sa::paged_workspace_bytes(p);
+}
+
+sa_status sa_cache_append(const void *K_new, const void *V_new, void *K_pages, void *V_pages, int B, int Hkv, int m,
+                          int d, int page, int num_pages, int max_pages, const int32_t *block_table,
+                          const int32_t *seq_lens, const int32_t *q_lens, sa_dtype dtype, sa_stream_t stream) {
+    if (dtype != SA_BF16 && dtype != SA_FP32) return SA_ERR_INVALID_ARG;
+    const void *t[4] = {K_new, V_new, K_pages, V_pages};
+    for (int i = 0; i < 4; ++i) {
+        if (!t[i] || !al16(t[i])) return SA_ERR_INVALID_ARG;
+        for (int j = 2; j < i; ++j)
+            if (t[i] == t[j]) return SA_ERR_INVALID_ARG;
+    }
+    if (K_new == K_pages || K_new == V_pages || V_new == K_pages || V_new == V_pages) return SA_ERR_INVALID_ARG;
+    if (!block_table || !seq_lens || !al4(block_table) || !al4(seq_lens) || !al4(q_lens)) return SA_ERR_INVALID_ARG;
+    sa_status s = sizes_ok(B, Hkv, m, d, page, num_pages, max_pages);
+    if (s != SA_OK) return s;
+    sa::AppendProblem p = {};
+    int sms = 0;
+    s = sa::api_device(&p.status, &sms);
+    if (s != SA_OK) return s;
+    p.Kn = K_new; p.Vn = V_new; p.K = K_pages; p.V = V_pages;
+    p.B = B; p.Hkv = Hkv; p.m = m;
+    p.row_bytes = d * (dtype == SA_FP32 ? 4 : 2);
+    p.page = page; p.log_page = log2_page(page); p.num_pages = num_pages; p.max_pages = max_pages;
+    p.table = block_table; p.lens = seq_lens; p.qlens = q_lens;
+    return finish(sa::launch_cache_append(p, sms, reinterpret_cast<cudaStream_t>(stream)), 1);
+}
+
+size_t sa_cache_workspace_bytes(int num_pages, int B) {
+    if (num_pages < 1 || B < 1 || B > sa::kPagedMaxBatch) return 0;
+    return 4 * sa::cache_workspace_words(num_pages, B);
+}
+
+sa_status sa_cache_copy_pages(void *K_pages, void *V_pages, int layers, int num_pages, size_t page_bytes,
+                              const int32_t *src, const int32_t *dst, int count, sa_stream_t stream) {
+    sa_status s = pool_ok(K_pages, V_pages, layers, num_pages, page_bytes);
+    if (s != SA_OK) return s;
+    if (count < 0 || (count > 0 && (!src || !dst || !al4(src) || !al4(dst)))) return SA_ERR_INVALID_ARG;
+    sa::PoolProblem p = {};
+    int sms = 0, launches = 0;
+    s = sa::api_device(&p.status, &sms);
+    if (s != SA_OK) return s;
+    p.K = static_cast<uint8_t *>(K_pages);
+    p.V = static_cast<uint8_t *>(V_pages);
+    p.layers = layers; p.num_pages = num_pages; p.page_bytes = page_bytes;
+    p.src = src; p.dst = dst; p.n = count;
+    const cudaError_t e = sa::launch_cache_copy(p, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+sa_status sa_cache_fork(void *K_pages, void *V_pages, int layers, int num_pages, size_t page_bytes, int page, int B,
+                        int max_pages, const int32_t *src, const int32_t *dst, int count, const int32_t *table_in,
+                        const int32_t *lens_in, const int32_t *ref_in, int32_t *table_out, int32_t *lens_out,
+                        int32_t *ref_out, void *workspace, size_t workspace_bytes, sa_stream_t stream) {
+    sa_status s = pool_ok(K_pages, V_pages, layers, num_pages, page_bytes);
+    if (s != SA_OK) return s;
+    if (!page_ok(page) || count < 0 || (count > 0 && (!src || !dst || !al4(src) || !al4(dst)))) return SA_ERR_INVALID_ARG;
+    if ((s = tables_ok(B, max_pages, num_pages, table_in, ref_in, table_out, ref_out)) != SA_OK) return s;
+    if (!lens_in || !lens_out || !al4(lens_in) || !al4(lens_out)) return SA_ERR_INVALID_ARG;
+    if ((long long)max_pages * page > sa::kPagedMaxLen) return SA_ERR_UNSUPPORTED;
+    if ((s = ws_ok(workspace, workspace_bytes, sa_cache_workspace_bytes(num_pages, B))) != SA_OK) return s;
+    sa::PoolProblem p = {};
+    int sms = 0, launches = 0;
+    s = sa::api_device(&p.status, &sms);
+    if (s != SA_OK) return s;
+    p.K = static_cast<uint8_t *>(K_pages);
+    p.V = static_cast<uint8_t *>(V_pages);
+    p.layers = layers; p.num_pages = num_pages; p.page_bytes = page_bytes;
+    p.page = page; p.log_page = log2_page(page); p.B = B; p.max_pages = max_pages;
+    p.src = src; p.dst = dst; p.n = count;
+    p.table_in = table_in; p.lens_in = lens_in; p.refs_in = ref_in;
+    p.table_out = table_out; p.lens_out = lens_out; p.refs_out = ref_out;
+    p.ws = static_cast<int32_t *>(workspace);
+    const cudaError_t e = sa::launch_cache_fork(p, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+sa_status sa_cache_free(int num_pages, int B, int max_pages, const int32_t *rows, int count, const int32_t *table_in,
+                        const int32_t *lens_in, const int32_t *ref_in, int32_t *table_out, int32_t *lens_out,
+                        int32_t *ref_out, sa_stream_t stream) {
+    sa_status s = tables_ok(B, max_pages, num_pages, table_in, ref_in, table_out, ref_out);
+    if (s != SA_OK) return s;
+    if (!lens_in || !lens_out || !al4(lens_in) || !al4(lens_out)) return SA_ERR_INVALID_ARG;
+    if (count < 0 || (count > 0 && (!rows || !al4(rows)))) return SA_ERR_INVALID_ARG;
+    sa::PoolProblem p = {};
+    int sms = 0, launches = 0;
+    s = sa::api_device(&p.status, &sms);
+    if (s != SA_OK) return s;
+    p.num_pages = num_pages; p.B = B; p.max_pages = max_pages;
+    p.src = rows; p.n = count;
+    p.table_in = table_in; p.lens_in = lens_in; p.refs_in = ref_in;
+    p.table_out = table_out; p.lens_out = lens_out; p.refs_out = ref_out;
+    const cudaError_t e = sa::launch_cache_free(p, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+sa_status sa_cache_trim(int num_pages, int page, int B, int max_pages, int reach, const int32_t *global_idx,
+                        int n_global, const int32_t *table_in, const int32_t *seq_lens, const int32_t *ref_in,
+                        int32_t *table_out, int32_t *ref_out, sa_stream_t stream) {
+    sa_status s = tables_ok(B, max_pages, num_pages, table_in, ref_in, table_out, ref_out);
+    if (s != SA_OK) return s;
+    if (!page_ok(page) || reach < 0 || !seq_lens || !al4(seq_lens)) return SA_ERR_INVALID_ARG;
+    if (n_global < 0 || (n_global > 0 && (!global_idx || !al4(global_idx)))) return SA_ERR_INVALID_ARG;
+    sa::PoolProblem p = {};
+    int sms = 0, launches = 0;
+    s = sa::api_device(&p.status, &sms);
+    if (s != SA_OK) return s;
+    p.num_pages = num_pages; p.page = page; p.log_page = log2_page(page); p.B = B; p.max_pages = max_pages;
+    p.reach = reach;
+    p.gidx = global_idx; p.ng = n_global;
+    p.table_in = table_in; p.lens_in = seq_lens; p.refs_in = ref_in;
+    p.table_out = table_out; p.refs_out = ref_out;
+    const cudaError_t e = sa::launch_cache_trim(p, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+sa_status sa_cache_reserve(int num_pages, int page, int B, int max_pages, const int32_t *seq_lens,
+                           const int32_t *q_lens, const int32_t *table_in, const int32_t *ref_in, int32_t *table_out,
+                           int32_t *ref_out, void *workspace, size_t workspace_bytes, sa_stream_t stream) {
+    sa_status s = tables_ok(B, max_pages, num_pages, table_in, ref_in, table_out, ref_out);
+    if (s != SA_OK) return s;
+    if (!page_ok(page) || !seq_lens || !q_lens || !al4(seq_lens) || !al4(q_lens)) return SA_ERR_INVALID_ARG;
+    if ((long long)max_pages * page > sa::kPagedMaxLen) return SA_ERR_UNSUPPORTED;
+    if ((s = ws_ok(workspace, workspace_bytes, sa_cache_workspace_bytes(num_pages, B))) != SA_OK) return s;
+    sa::PoolProblem p = {};
+    int sms = 0, launches = 0;
+    s = sa::api_device(&p.status, &sms);
+    if (s != SA_OK) return s;
+    p.num_pages = num_pages; p.page = page; p.log_page = log2_page(page); p.B = B; p.max_pages = max_pages;
+    p.qlens = q_lens;
+    p.table_in = table_in; p.lens_in = seq_lens; p.refs_in = ref_in;
+    p.table_out = table_out; p.refs_out = ref_out;
+    p.ws = static_cast<int32_t *>(workspace);
+    const cudaError_t e = sa::launch_cache_reserve(p, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+sa_status sa_cache_compact(void *K_pages, void *V_pages, int layers, int num_pages, size_t page_bytes, int B,
+                           int max_pages, const int32_t *table_in, const int32_t *ref_in, int32_t *table_out,
+                           int32_t *ref_out, void *workspace, size_t workspace_bytes, sa_stream_t stream) {
+    sa_status s = pool_ok(K_pages, V_pages, layers, num_pages, page_bytes);
+    if (s != SA_OK) return s;
+    if ((s = tables_ok(B, max_pages, num_pages, table_in, ref_in, table_out, ref_out)) != SA_OK) return s;
+    if ((s = ws_ok(workspace, workspace_bytes, sa_cache_workspace_bytes(num_pages, B))) != SA_OK) return s;
+    sa::PoolProblem p = {};
+    int sms = 0, launches = 0;
+    s = sa::api_device(&p.status, &sms);
+    if (s != SA_OK) return s;
+    p.K = static_cast<uint8_t *>(K_pages);
+    p.V = static_cast<uint8_t *>(V_pages);
+    p.layers = layers; p.num_pages = num_pages; p.page_bytes = page_bytes;
+    p.B = B; p.max_pages = max_pages;
+    p.table_in = table_in; p.refs_in = ref_in; p.table_out = table_out; p.refs_out = ref_out;
+    p.ws = static_cast<int32_t *>(workspace);
+    const cudaError_t e = sa::launch_cache_compact(p, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
+    return finish(e, launches);
+}
+
+}  // extern "C"

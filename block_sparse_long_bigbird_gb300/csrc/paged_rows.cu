@@ -1,0 +1,380 @@
+// Attention of a few new tokens per sequence over a paged cache (single-token
+// steps, short drafts), bf16 and fp32, on the ordinary units.
+//
+//     O_r = sum_j w_rj V_j / sum_j w_rj,   w_rj = 2^(s_rj - max_j s_rj),   s = q . k log2(e) / sqrt(d)
+//
+// A call reads each visible key and value row once per key head and does a few
+// flops per byte: the memory bounds it as long as a key head has at most R = 8
+// rows (rows = tokens x query heads of the key head). One warp takes 16 keys
+// at a time (one page, one table entry): each key's row is spread over
+// D / 8 (bf16) or D / 4 (fp32) lanes, 16 bytes each, so all loads are full
+// lines; K and V of the 16 keys are requested together before either is used.
+// Every group of lanes keeps a running maximum, sum and D-sum of its own keys
+// in registers and in fp32; groups, then warps, are joined once at the end of
+// the unit. Masked keys are not loaded: dilated heads read only their own
+// keys, and unwritten memory is never touched. Long sweeps are cut into units
+// by the plan; their partial results are joined by paged_merge in a fixed
+// order, so results do not depend on timing.
+#include "paged_common.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kRowsWarps = 8;
+constexpr int kItem = 16;  // keys a warp takes at a time
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) paged_rows(const PagedProblem p) {
+    constexpr int VE = 16 / sizeof(T);  // elements of a 16-byte load
+    constexpr int LPK = D / VE;         // lanes per key
+    constexpr int KPL = 32 / LPK;       // keys per warp-wide load
+    constexpr int NIT = kItem / KPL;    // loads per item
+    constexpr int MOST = R >= 4 || (sizeof(T) == 2 && D == 128) ? 4 : 8;
+    constexpr int CH = NIT < MOST ? NIT : MOST;  // of which this many are in flight together
+    extern __shared__ __align__(16) uint8_t smem[];
+    // joining the warps' results: [warp][R] maxima and sums, [warp][R][D] sums
+    float *jm = reinterpret_cast<float *>(smem);
+    float *jl = jm + kRowsWarps * R;
+    float *ja = jl + kRowsWarps * R;
+    Plan P = plan_at(ja + kRowsWarps * R * D, p.B, p.ng);
+    make_plan(p, P);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int grp = lane / LPK, sub = lane % LPK;
+    const T *Kp = static_cast<const T *>(p.K), *Vp = static_cast<const T *>(p.V);
+
+    const int total = P.ubase[p.B];
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        const Unit U = decode_unit(p, P, u);
+        float q[R][VE], acc[R][VE], m[R], l[R];
+        // lane r masks for row r; the warp reads the masks from there
+        Row mine;
+        {
+            int t, head;
+            row_token(p, U, lane < p.rows ? lane : 0, p.tpt, t, head);
+            mine = make_row(p, P, U, head, t);
+            mine.valid = mine.valid && lane < p.rows;
+        }
+        const uint32_t rows_in = __ballot_sync(kAllLanes, mine.valid);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            int t, head;
+            row_token(p, U, r < p.rows ? r : 0, p.tpt, t, head);
+            m[r] = -CUDART_INF_F;
+            l[r] = 0.f;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) acc[r][i] = q[r][i] = 0.f;
+            if ((rows_in >> r) & 1u) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(
+                    static_cast<const T *>(p.Q) + (((size_t)U.b * p.Hq + head) * p.m + t) * D + sub * VE);
+                const T *x = reinterpret_cast<const T *>(&w);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) q[r][i] = to_float<T>(x[i]) * p.scale_log2;
+            }
+        }
+        // items of this unit: four per 64-key block, dealt to the warps in turn
+        const int i_end = 4 * U.e1;
+        int item = 4 * U.e0 + warp;
+        int blk = 0, pg = -1;
+        if (item < i_end) {
+            blk = entry_block(P, U, item >> 2);
+            pg = page_of(p, U.b, (blk << 6) + (item & 3) * kItem);
+        }
+        while (item < i_end) {
+            const int next = item + kRowsWarps;
+            int nblk = 0, npg = -1;
+            if (next < i_end) {  // the next table entry is on its way while this item is worked on
+                nblk = entry_block(P, U, next >> 2);
+                npg = page_of(p, U.b, (nblk << 6) + (next & 3) * kItem);
+            }
+            const int j0 = (blk << 6) + (item & 3) * kItem;
+            uint32_t mask[R], any = 0u, all = 0xffffu;
+            if (pg >= 0) {
+                const uint32_t w =
+                    (uint32_t)(row_mask(mine, blk, global_bits(P, p, blk), ~0ull) >> ((item & 3) * kItem)) & 0xffffu;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    mask[r] = __shfl_sync(kAllLanes, w, r);
+                    any |= mask[r];
+                    if ((rows_in >> r) & 1u) all &= mask[r];
+                }
+            }
+            if (any) {
+                const size_t at = ((((size_t)pg * p.Hkv + U.hk) << p.log_page) + (j0 & (p.page - 1))) * D + sub * VE;
+                const bool same = all == any;  // every row sees the same keys
+#pragma unroll
+                for (int c = 0; c < NIT / CH; ++c) {
+                    uint4 kw[CH], vw[CH];
+                    if (KPL > 1 || any >> (c * CH)) {
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            const int kk = (c * CH + i) * KPL + grp;
+                            kw[i] = vw[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if ((any >> kk) & 1u) kw[i] = __ldg(reinterpret_cast<const uint4 *>(Kp + at + (size_t)kk * D));
+                        }
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            const int kk = (c * CH + i) * KPL + grp;
+                            if ((any >> kk) & 1u) vw[i] = __ldg(reinterpret_cast<const uint4 *>(Vp + at + (size_t)kk * D));
+                        }
+                        float s[R][CH];
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            const T *k = reinterpret_cast<const T *>(&kw[i]);
+#pragma unroll
+                            for (int r = 0; r < R; ++r) s[r][i] = 0.f;
+#pragma unroll
+                            for (int x = 0; x < VE; ++x) {
+                                const float kx = to_float<T>(k[x]);
+#pragma unroll
+                                for (int r = 0; r < R; ++r) s[r][i] = fmaf(q[r][x], kx, s[r][i]);
+                            }
+                        }
+#pragma unroll
+                        for (int o = LPK / 2; o; o >>= 1)
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+#pragma unroll
+                                for (int i = 0; i < CH; ++i) s[r][i] += __shfl_xor_sync(kAllLanes, s[r][i], o);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            float mn = m[r];
+#pragma unroll
+                            for (int i = 0; i < CH; ++i) {
+                                if (!((mask[r] >> ((c * CH + i) * KPL + grp)) & 1u)) s[r][i] = -CUDART_INF_F;
+                                mn = fmaxf(mn, s[r][i]);
+                            }
+                            const float ref = mn == -CUDART_INF_F ? 0.f : mn;
+                            const float f = ptx::ex2(m[r] - ref);  // 0 from the initial -inf
+                            m[r] = mn;
+                            l[r] *= f;
+#pragma unroll
+                            for (int i = 0; i < CH; ++i) {
+                                s[r][i] = ptx::ex2(s[r][i] - ref);
+                                l[r] += s[r][i];
+                            }
+#pragma unroll
+                            for (int x = 0; x < VE; ++x) acc[r][x] *= f;
+                        }
+                        if (same) {
+#pragma unroll
+                            for (int i = 0; i < CH; ++i) {
+                                const T *v = reinterpret_cast<const T *>(&vw[i]);
+#pragma unroll
+                                for (int x = 0; x < VE; ++x) {
+                                    const float vx = to_float<T>(v[x]);
+#pragma unroll
+                                    for (int r = 0; r < R; ++r) acc[r][x] = fmaf(s[r][i], vx, acc[r][x]);
+                                }
+                            }
+                        } else {  // a value that some row does not see may be anything: keep 0 x NaN out of that row
+#pragma unroll
+                            for (int i = 0; i < CH; ++i) {
+                                const T *v = reinterpret_cast<const T *>(&vw[i]);
+#pragma unroll
+                                for (int r = 0; r < R; ++r) {
+                                    const bool sees = (mask[r] >> ((c * CH + i) * KPL + grp)) & 1u;
+#pragma unroll
+                                    for (int x = 0; x < VE; ++x)
+                                        acc[r][x] = sees ? fmaf(s[r][i], to_float<T>(v[x]), acc[r][x]) : acc[r][x];
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            item = next;
+            blk = nblk;
+            pg = npg;
+        }
+        // join the groups of lanes of a warp
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int o = LPK; o < 32; o <<= 1) {
+                const float m2 = __shfl_xor_sync(kAllLanes, m[r], o), l2 = __shfl_xor_sync(kAllLanes, l[r], o);
+                const float mn = fmaxf(m[r], m2), ref = mn == -CUDART_INF_F ? 0.f : mn;
+                const float f = ptx::ex2(m[r] - ref), f2 = ptx::ex2(m2 - ref);
+                l[r] = l[r] * f + l2 * f2;
+#pragma unroll
+                for (int x = 0; x < VE; ++x) {
+                    const float a2 = __shfl_xor_sync(kAllLanes, acc[r][x], o);
+                    acc[r][x] = acc[r][x] * f + a2 * f2;
+                }
+                m[r] = mn;
+            }
+            if (grp == 0) {
+#pragma unroll
+                for (int x = 0; x < VE; ++x) ja[(warp * R + r) * D + sub * VE + x] = acc[r][x];
+            }
+            if (lane == 0) {
+                jm[warp * R + r] = m[r];
+                jl[warp * R + r] = l[r];
+            }
+        }
+        __syncthreads();
+        // and the warps, in order
+        for (int idx = tid; idx < p.rows * D; idx += kRowsWarps * 32) {
+            const int r = idx / D, x = idx % D;
+            float mx = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kRowsWarps; ++w) mx = fmaxf(mx, jm[w * R + r]);
+            const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+            float ls = 0.f, a = 0.f;
+#pragma unroll
+            for (int w = 0; w < kRowsWarps; ++w) {
+                const float f = ptx::ex2(jm[w * R + r] - ref);
+                ls = fmaf(jl[w * R + r], f, ls);
+                a = fmaf(ja[(w * R + r) * D + x], f, a);
+            }
+            int t, head;
+            row_token(p, U, r, p.tpt, t, head);
+            if (U.ns > 1) {
+                const size_t slot = (size_t)U.slot * p.rows + r;
+                p.part_o[slot * D + x] = a;
+                if (x == 0) p.part_ml[slot] = make_float2(mx, ls);
+            } else if (t < p.m) {
+                static_cast<T *>(p.O)[(((size_t)U.b * p.Hq + head) * p.m + t) * D + x] =
+                    from_float<T>(ls == 0.f ? 0.f : a / ls);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Joins the partial results of split sweeps, split by split in order: four
+// warps take a row, each a stretch of its splits. Launched so that its plan is
+// computed while the sweeps still run.
+constexpr int kMergeWarps = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge(const PagedProblem p) {
+    constexpr int E = D / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *jm = reinterpret_cast<float *>(smem);  // [warp]
+    float *jl = jm + kMergeWarps;
+    float *ja = jl + kMergeWarps;  // [warp][D]
+    Plan P = plan_at(ja + kMergeWarps * D, p.B, p.ng);
+    make_plan(p, P);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the sweeps' results are visible from here on
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slots = P.sbase[p.B];
+    // work items: (slot of a sweep's first split, row)
+    const long long n_items = (long long)slots * p.rows;
+    for (long long w = blockIdx.x; w < n_items; w += gridDim.x) {
+        const int row = (int)(w % p.rows), slot = (int)(w / p.rows);
+        int b = 0, hi = p.B;  // last sequence with sbase <= slot (its range is not empty)
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (P.sbase[mid] <= slot) b = mid; else hi = mid;
+        }
+        const int ns = P.ns[b];
+        int r = slot - P.sbase[b];
+        if (r % ns) continue;
+        r /= ns;
+        const int tiles = (P.q[b] + p.tpt - 1) / p.tpt;
+        Unit U;
+        U.hk = r / tiles;
+        U.t0 = (tiles - 1 - r % tiles) * p.tpt;
+        // tiled kernels put the tokens of a unit's two halves apart: a row's
+        // token and head come from the half it is in
+        const int half_rows = p.rows > p.group * p.tpt_half ? p.rows / 2 : p.rows;
+        const int x = row / half_rows;
+        U.t0 += x * p.tpt_half;
+        int t, head;
+        row_token(p, U, row - x * half_rows, p.tpt_half, t, head);
+        const float2 *ml = p.part_ml + (size_t)slot * p.rows + row;
+        const float *po = p.part_o + ((size_t)slot * p.rows + row) * D + lane * E;
+        float mx = -CUDART_INF_F;
+        for (int c = lane; c < ns; c += 32) mx = fmaxf(mx, ml[(size_t)c * p.rows].x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, o));
+        const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+        float l = 0.f, acc[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0.f;
+        const int c0 = ns * warp / kMergeWarps, c1 = ns * (warp + 1) / kMergeWarps;
+#pragma unroll 4
+        for (int c = c0; c < c1; ++c) {
+            const float2 y = ml[(size_t)c * p.rows];
+            const float f = ptx::ex2(y.x - ref);
+            l = fmaf(y.y, f, l);
+            const float *src = po + (size_t)c * p.rows * D;
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = fmaf(src[i], f, acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) ja[warp * D + lane * E + i] = acc[i];
+        if (lane == 0) jl[warp] = l;
+        __syncthreads();
+        if (t < p.m) {
+            for (int d = tid; d < D; d += kMergeWarps * 32) {
+                float a = 0.f, ls = 0.f;
+#pragma unroll
+                for (int k = 0; k < kMergeWarps; ++k) {
+                    a += ja[k * D + d];
+                    ls += jl[k];
+                }
+                const bool valid = t < P.q[b];
+                static_cast<T *>(p.O)[(((size_t)b * p.Hq + head) * p.m + t) * D + d] =
+                    from_float<T>(!valid || ls == 0.f ? 0.f : a / ls);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int D, int R>
+cudaError_t launch_rows(const PagedProblem &p, int num_sms, cudaStream_t stream) {
+    const size_t smem = (size_t)kRowsWarps * R * (D + 2) * 4 + plan_bytes(p.B, p.ng);
+    auto kern = paged_rows<T, D, R>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    int per_sm = 1;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kRowsWarps * 32, smem)) != cudaSuccess) return e;
+    const long long units = (long long)p.B * p.Hkv + 2ll * p.target;
+    const long long grid = (long long)num_sms * (per_sm < 1 ? 1 : per_sm);
+    kern<<<(int)(units < grid ? units : grid), kRowsWarps * 32, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_rows_r(const PagedProblem &p, int num_sms, cudaStream_t stream) {
+    if (p.rows <= 1) return launch_rows<T, D, 1>(p, num_sms, stream);
+    if (p.rows <= 2) return launch_rows<T, D, 2>(p, num_sms, stream);
+    if constexpr (sizeof(T) == 4) {
+        if (p.rows > 4) return launch_rows<T, D, 8>(p, num_sms, stream);
+    }
+    return launch_rows<T, D, 4>(p, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream) {
+    if (dtype == SA_FP32)
+        return p.d == 64 ? launch_rows_r<float, 64>(p, num_sms, stream) : launch_rows_r<float, 128>(p, num_sms, stream);
+    return p.d == 64 ? launch_rows_r<__nv_bfloat16, 64>(p, num_sms, stream)
+                     : launch_rows_r<__nv_bfloat16, 128>(p, num_sms, stream);
+}
+
+cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream) {
+    const size_t smem = (size_t)kMergeWarps * (p.d + 2) * 4 + plan_bytes(p.B, p.ng);
+    void (*kern)(const PagedProblem) =
+        dtype == SA_FP32 ? (p.d == 64 ? paged_merge<float, 64> : paged_merge<float, 128>)
+                         : (p.d == 64 ? paged_merge<__nv_bfloat16, 64> : paged_merge<__nv_bfloat16, 128>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long items = 2ll * p.target * p.rows, grid = 8ll * num_sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items < grid ? items : grid));
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace sa

@@ -1,0 +1,254 @@
+// Attention of many new tokens over a paged cache on the ordinary units: the
+// fp32 path, and bf16 where SA_OPT_FORCE_SIMT asks for a cross-check.
+//
+// A unit's 64 query rows (tokens x the query heads of one key head) walk the
+// 64-key blocks that any of them sees. Scores and output are 8 x 4 register
+// tiles of fp32 multiply-adds per thread: 32 multiply-adds for three 16-byte
+// shared loads, so the multiply-add rate bounds it. Q and K are held
+// transposed (the inner loop runs over d and reads four keys and eight rows at
+// a time); V takes K's buffer once the scores are done, which leaves room for
+// several CTAs per SM to hide one another's loads and barriers.
+#include "paged_common.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kTR = 64;        // rows and keys of a tile
+constexpr int kTT = 128;       // threads
+constexpr int kPad = kTR + 4;  // row stride of the transposed arrays (16-byte aligned, off the banks' period)
+
+template <typename T, int D>
+struct TileSmem {
+    static constexpr int Q = 0;
+    static constexpr int KV = Q + D * kTR * 4;
+    static constexpr int S = KV + (D * kPad > kTR * D ? D * kPad : kTR * D) * 4;
+    static constexpr int MASK = S + kTR * kPad * 4;
+    static constexpr int FLAG = MASK + kTR * 8;
+    static constexpr int PLAN = FLAG + kTR * 4;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
+    using L = TileSmem<T, D>;
+    constexpr int VE = 16 / sizeof(T);
+    constexpr int ND = D / 64;  // 4-wide output columns per thread
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *Qs = reinterpret_cast<float *>(smem + L::Q);    // [D][64]
+    float *KV = reinterpret_cast<float *>(smem + L::KV);   // K: [D][kPad], then V: [64][D]
+    float *Ps = reinterpret_cast<float *>(smem + L::S);    // [key][kPad rows]
+    uint64_t *masks = reinterpret_cast<uint64_t *>(smem + L::MASK);
+    int *flags = reinterpret_cast<int *>(smem + L::FLAG);
+    Plan P = plan_at(smem + L::PLAN, p.B, p.ng);
+    make_plan(p, P);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ty = tid >> 4, tx = tid & 15;  // rows ty * 8 ..., keys and columns tx * 4 ...
+    const T *Kp = static_cast<const T *>(p.K), *Vp = static_cast<const T *>(p.V);
+
+    const int total = P.ubase[p.B];
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        const Unit U = decode_unit(p, P, u);
+        // threads 0..63: one row each, for the masks
+        Row row = {};
+        if (tid < kTR) {
+            int t = 0, head = 0;
+            if (tid < p.rows) {
+                row_token(p, U, tid, p.tpt_half, t, head);
+                row = make_row(p, P, U, head, t);
+            }
+        }
+        // queries, transposed and scaled; a lane per row
+        for (int i = tid; i < kTR * (D / VE); i += kTT) {
+            const int r = i % kTR, c = i / kTR;
+            int t, head;
+            row_token(p, U, r < p.rows ? r : 0, p.tpt_half, t, head);
+            const bool ok = U.live && r < p.rows && t < U.q;
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (ok)
+                w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.Q) +
+                                                          (((size_t)U.b * p.Hq + head) * p.m + t) * D + c * VE));
+            const T *x = reinterpret_cast<const T *>(&w);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) Qs[(c * VE + k) * kTR + r] = to_float<T>(x[k]) * p.scale_log2;
+        }
+        float acc[8][4 * ND], m[8], l[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            m[r] = -CUDART_INF_F;
+            l[r] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4 * ND; ++x) acc[r][x] = 0.f;
+        }
+        for (int e = U.e0; e < U.e1; ++e) {
+            const int blk = entry_block(P, U, e), j0 = blk << 6;
+            __syncthreads();  // the previous step is done with KV, Ps and masks
+            if (tid < kTR) masks[tid] = row_mask(row, blk, global_bits(P, p, blk), ~0ull);
+            // one key per lane: keys past the sequence or without a page count as
+            // zeros and are masked below
+            const int key = tid & 63, pos = j0 + key;
+            const int pg = pos < U.s ? page_of(p, U.b, pos) : -1;
+            const size_t at = ((((size_t)(pg < 0 ? 0 : pg) * p.Hkv + U.hk) << p.log_page) + (pos & (p.page - 1))) * D;
+#pragma unroll 4
+            for (int c = tid >> 6; c < D / VE; c += kTT / 64) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (pg >= 0) w = __ldg(reinterpret_cast<const uint4 *>(Kp + at + c * VE));
+                const T *x = reinterpret_cast<const T *>(&w);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) KV[(c * VE + k) * kPad + key] = to_float<T>(x[k]);
+            }
+            const unsigned there = __ballot_sync(kAllLanes, pg >= 0);  // of keys 32 (warp & 1) ...
+            if (warp < 2 && lane == 0) flags[kTR - 2 + warp] = (int)there;
+            __syncthreads();
+            const uint64_t present = (uint32_t)flags[kTR - 2] | ((uint64_t)(uint32_t)flags[kTR - 1] << 32);
+            float s[8][4];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[r][x] = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < D; ++k) {
+                const float4 a0 = *reinterpret_cast<const float4 *>(Qs + k * kTR + ty * 8);
+                const float4 a1 = *reinterpret_cast<const float4 *>(Qs + k * kTR + ty * 8 + 4);
+                const float4 b = *reinterpret_cast<const float4 *>(KV + k * kPad + tx * 4);
+                const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    s[r][0] = fmaf(a[r], b.x, s[r][0]);
+                    s[r][1] = fmaf(a[r], b.y, s[r][1]);
+                    s[r][2] = fmaf(a[r], b.z, s[r][2]);
+                    s[r][3] = fmaf(a[r], b.w, s[r][3]);
+                }
+            }
+            __syncthreads();  // K is done with
+            {
+                // V rows as they are: a warp per key row piece
+                for (int i = tid; i < kTR * (D / VE); i += kTT) {
+                    const int vk = i / (D / VE), c = i % (D / VE), vpos = j0 + vk;
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if ((present >> vk) & 1ull) {
+                        const int vpg = page_of(p, U.b, vpos);
+                        w = __ldg(reinterpret_cast<const uint4 *>(
+                            Vp + ((((size_t)vpg * p.Hkv + U.hk) << p.log_page) + (vpos & (p.page - 1))) * D + c * VE));
+                    }
+                    const T *x = reinterpret_cast<const T *>(&w);
+#pragma unroll
+                    for (int k = 0; k < VE; ++k) KV[vk * D + c * VE + k] = to_float<T>(x[k]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const uint32_t w = (uint32_t)((masks[ty * 8 + r] & present) >> (tx * 4)) & 15u;
+                float mn = m[r];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (!((w >> x) & 1u)) s[r][x] = -CUDART_INF_F;
+                    mn = fmaxf(mn, s[r][x]);
+                }
+#pragma unroll
+                for (int o = 8; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kAllLanes, mn, o));
+                const float ref = mn == -CUDART_INF_F ? 0.f : mn;
+                const float f = ptx::ex2(m[r] - ref);
+                m[r] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    s[r][x] = ptx::ex2(s[r][x] - ref);
+                    sum += s[r][x];
+                }
+                l[r] = l[r] * f + sum;  // this thread's keys; joined at the end
+#pragma unroll
+                for (int x = 0; x < 4 * ND; ++x) acc[r][x] *= f;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float *dst = Ps + (tx * 4 + x) * kPad + ty * 8;
+                *reinterpret_cast<float4 *>(dst) = make_float4(s[0][x], s[1][x], s[2][x], s[3][x]);
+                *reinterpret_cast<float4 *>(dst + 4) = make_float4(s[4][x], s[5][x], s[6][x], s[7][x]);
+            }
+            __syncthreads();
+#pragma unroll 4
+            for (int k = 0; k < kTR; ++k) {
+                const float4 a0 = *reinterpret_cast<const float4 *>(Ps + k * kPad + ty * 8);
+                const float4 a1 = *reinterpret_cast<const float4 *>(Ps + k * kPad + ty * 8 + 4);
+                const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+                for (int h = 0; h < ND; ++h) {
+                    const float4 b = *reinterpret_cast<const float4 *>(KV + k * D + h * 64 + tx * 4);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        acc[r][h * 4 + 0] = fmaf(a[r], b.x, acc[r][h * 4 + 0]);
+                        acc[r][h * 4 + 1] = fmaf(a[r], b.y, acc[r][h * 4 + 1]);
+                        acc[r][h * 4 + 2] = fmaf(a[r], b.z, acc[r][h * 4 + 2]);
+                        acc[r][h * 4 + 3] = fmaf(a[r], b.w, acc[r][h * 4 + 3]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (tid < kTR) flags[tid] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+#pragma unroll
+            for (int o = 8; o; o >>= 1) l[r] += __shfl_xor_sync(kAllLanes, l[r], o);
+            const int rr = ty * 8 + r;
+            if (rr >= p.rows) continue;
+            int t, head;
+            row_token(p, U, rr, p.tpt_half, t, head);
+            const bool valid = U.live && t < U.q;
+            bool bad = not_finite(l[r]);
+#pragma unroll
+            for (int x = 0; x < 4 * ND; ++x) bad |= not_finite(acc[r][x]);
+            if (bad && valid) flags[rr] = 1;
+            if (U.ns > 1) {
+                const size_t slot = (size_t)U.slot * p.rows + rr;
+#pragma unroll
+                for (int h = 0; h < ND; ++h)
+                    *reinterpret_cast<float4 *>(p.part_o + slot * D + h * 64 + tx * 4) =
+                        make_float4(acc[r][h * 4], acc[r][h * 4 + 1], acc[r][h * 4 + 2], acc[r][h * 4 + 3]);
+                if (tx == 0) p.part_ml[slot] = make_float2(m[r], l[r]);
+            } else if (t < p.m) {
+                T *o = static_cast<T *>(p.O) + (((size_t)U.b * p.Hq + head) * p.m + t) * D;
+                const float inv = valid && l[r] != 0.f ? 1.f / l[r] : 0.f;
+#pragma unroll
+                for (int h = 0; h < ND; ++h)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        o[h * 64 + tx * 4 + x] = from_float<T>(valid ? acc[r][h * 4 + x] * inv : 0.f);
+            }
+        }
+        __syncthreads();
+        for (int rr = warp; rr < p.rows; rr += kTT / 32)
+            if (flags[rr]) {
+                int t, head;
+                row_token(p, U, rr, p.tpt_half, t, head);
+                float a[D / 32];
+                const float2 ml = exact_row<T, D>(p, P, U, t, head, a);
+                store_exact_row<T, D>(p, U, t, head, rr, ml, a);
+            }
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_tile(const PagedProblem &p, int num_sms, cudaStream_t stream) {
+    const size_t smem = TileSmem<T, D>::PLAN + plan_bytes(p.B, p.ng);
+    auto kern = paged_tile<T, D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    int per_sm = 1;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kTT, smem)) != cudaSuccess) return e;
+    const long long units = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt) + 2ll * p.target;
+    const long long grid = (long long)num_sms * (per_sm < 1 ? 1 : per_sm);
+    kern<<<(int)(units < grid ? units : grid), kTT, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tile(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream) {
+    if (dtype == SA_FP32)
+        return p.d == 64 ? launch_tile<float, 64>(p, num_sms, stream) : launch_tile<float, 128>(p, num_sms, stream);
+    return p.d == 64 ? launch_tile<__nv_bfloat16, 64>(p, num_sms, stream)
+                     : launch_tile<__nv_bfloat16, 128>(p, num_sms, stream);
+}
+
+}  // namespace sa

@@ -1,0 +1,263 @@
+"""Paged key/value cache of an autoregressive Longformer: attention of new tokens over it, and its pages.
+
+Thin wrappers of the ``longformer_attn_paged_fwd`` and ``sa_cache_*`` entry
+points (include/sparse_attn.h says what each computes). A pool of one layer is
+a ``[num_pages, Hkv, page, d]`` tensor; the calls that move pages take either
+one layer or all of them, ``[layers, num_pages, Hkv, page, d]``.
+
+The bookkeeping calls return new tables, lengths and counts; with ``out`` they
+write into the tensors given there, which may be the inputs themselves. Pools
+are always changed in place. Nothing here waits for the device: what a kernel
+finds wrong in a table or a list is reported by ``get_last_device_status``.
+"""
+
+import ctypes
+
+import torch
+
+from . import _lib
+
+_DTYPE = {torch.bfloat16: _lib.SA_BF16, torch.float32: _lib.SA_FP32}
+_INT = torch.int32
+
+
+def _call(name, device, stream, *args):
+    """Run a C entry point on `device` and `stream` (default: its current one)."""
+    fn = getattr(_lib.lib(), name)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream.cuda_stream)
+    if st != _lib.SA_OK:
+        raise _lib.SparseAttnError(st, name)
+
+
+def _scratch(n_bytes, device, stream):
+    """Workspace of one call, from torch's allocator; kept from reuse until `stream` is done with it."""
+    if n_bytes == 0:
+        return None
+    ws = torch.empty(n_bytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _fresh(like, stream):
+    t = torch.empty_like(like)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ints(name, t, device, shape):
+    """`t` must be a contiguous int32 tensor on `device` of `shape` (None: any size there)."""
+    if t is None:
+        return
+    if t.dtype is not _INT or t.device != device or not t.is_contiguous() or t.dim() != len(shape) \
+            or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device} (None: any size)")
+
+
+def _pools(K_pages, V_pages, dims):
+    if K_pages.dtype not in _DTYPE:
+        raise TypeError(f"unsupported dtype {K_pages.dtype}; use bfloat16 or float32")
+    if not K_pages.is_cuda or K_pages.dim() not in dims or V_pages.shape != K_pages.shape \
+            or V_pages.dtype is not K_pages.dtype or V_pages.device != K_pages.device \
+            or not K_pages.is_contiguous() or not V_pages.is_contiguous():
+        raise ValueError("K_pages and V_pages must be contiguous CUDA tensors [num_pages, Hkv, page, d]"
+                         + (" or [layers, num_pages, Hkv, page, d]" if 5 in dims else "")
+                         + " of one shape, dtype and device")
+
+
+def _new_rows(name, t, K_pages, heads):
+    if t.dtype is not K_pages.dtype or t.device != K_pages.device or t.dim() != 4 or not t.is_contiguous() \
+            or t.shape[3] != K_pages.shape[3] or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be a contiguous [B, heads, m, d] tensor matching the pools in dtype, device "
+                         "and head size")
+
+
+def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window, global_idx=None, dilation=None,
+                              q_lens=None, out=None, stream=None, workspace=None):
+    """Autoregressive Longformer attention of new tokens over a paged cache; returns O shaped like Q.
+
+    Q: [B, Hq, m, d], the new tokens' queries (Hq a multiple of the pools' heads; m = 1 for a single-token step).
+    block_table: int32 [B, max_pages], page of each stretch of tokens or -1; seq_lens: int32 [B], tokens in the
+    cache with the new ones (already appended); q_lens: int32 [B], new tokens of each sequence, or None (m each).
+    window, global_idx, dilation: as for longformer_attn_fwd (causal); 2 * (longest sequence) sees every token.
+    workspace: uint8 CUDA tensor of paged_workspace_bytes(...), or None to allocate it here.
+    Rows past q_lens and rows that see no key are zeros.
+    """
+    _pools(K_pages, V_pages, (4,))
+    num_pages, Hkv, page, d = K_pages.shape
+    _new_rows("Q", Q, K_pages, None)
+    B, Hq, m, _ = Q.shape
+    dev = Q.device
+    _ints("block_table", block_table, dev, (B, None))
+    _ints("seq_lens", seq_lens, dev, (B,))
+    _ints("q_lens", q_lens, dev, (B,))
+    _ints("dilation", dilation, dev, (Hq,))
+    _ints("global_idx", global_idx, dev, (None,))
+    n_global = 0 if global_idx is None else global_idx.numel()
+    max_pages = block_table.shape[1]
+    dt = _DTYPE[Q.dtype]
+    if workspace is None:
+        workspace = _scratch(paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, Q.dtype, dev), dev, stream)
+    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on Q's device")
+    if out is None:
+        out = _fresh(Q, stream)
+    elif out.shape != Q.shape or out.dtype is not Q.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous CUDA tensor shaped and typed like Q")
+    _call("longformer_attn_paged_fwd", dev, stream, Q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
+          out.data_ptr(), B, Hq, Hkv, m, d, page, num_pages, max_pages, block_table.data_ptr(), seq_lens.data_ptr(),
+          _ptr(q_lens), window, _ptr(dilation), global_idx.data_ptr() if n_global else None, n_global,
+          _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), dt)
+    return out
+
+
+def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None):
+    """Scratch bytes of a longformer_attn_paged_fwd call of these sizes."""
+    fn = _lib.lib().sa_longformer_paged_workspace_bytes
+    if device is not None and device.index is not None and torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return fn(B, Hq, Hkv, m, d, page, max_pages, _DTYPE[dtype])
+    return fn(B, Hq, Hkv, m, d, page, max_pages, _DTYPE[dtype])
+
+
+def cache_append(K_new, V_new, K_pages, V_pages, block_table, seq_lens, q_lens=None, stream=None):
+    """Write the new tokens' keys and values [B, Hkv, m, d] into their pages; returns (K_pages, V_pages)."""
+    _pools(K_pages, V_pages, (4,))
+    num_pages, Hkv, page, d = K_pages.shape
+    _new_rows("K_new", K_new, K_pages, Hkv)
+    _new_rows("V_new", V_new, K_pages, Hkv)
+    B, _, m, _ = K_new.shape
+    if V_new.shape != K_new.shape:
+        raise ValueError("K_new and V_new must share shape")
+    dev = K_pages.device
+    _ints("block_table", block_table, dev, (B, None))
+    _ints("seq_lens", seq_lens, dev, (B,))
+    _ints("q_lens", q_lens, dev, (B,))
+    _call("sa_cache_append", dev, stream, K_new.data_ptr(), V_new.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
+          B, Hkv, m, d, page, num_pages, block_table.shape[1], block_table.data_ptr(), seq_lens.data_ptr(),
+          _ptr(q_lens), _DTYPE[K_pages.dtype])
+    return K_pages, V_pages
+
+
+def _pool_args(K_pages, V_pages):
+    """(layers, num_pages, bytes of a page of one layer, page) of pools of one layer or several."""
+    _pools(K_pages, V_pages, (4, 5))
+    num_pages, Hkv, page, d = K_pages.shape[-4:]
+    layers = K_pages.shape[0] if K_pages.dim() == 5 else 1
+    return layers, num_pages, Hkv * page * d * K_pages.element_size(), page
+
+
+def _outputs(out, ins, stream):
+    if out is None:
+        return [_fresh(t, stream) for t in ins]
+    if len(out) != len(ins):
+        raise ValueError(f"out must hold {len(ins)} tensors")
+    for o, t in zip(out, ins):
+        if o.dtype is not t.dtype or o.shape != t.shape or o.device != t.device or not o.is_contiguous():
+            raise ValueError("out tensors must be contiguous and match the inputs in shape, dtype and device")
+    return list(out)
+
+
+def _book(block_table, ref_count, num_pages=None, device=None):
+    dev = block_table.device
+    if not block_table.is_cuda or (device is not None and dev != device):
+        raise ValueError("block_table must be a CUDA tensor on the pools' device")
+    _ints("block_table", block_table, dev, (None, None))
+    _ints("ref_count", ref_count, dev, (num_pages,))
+    return dev, block_table.shape[0], block_table.shape[1], ref_count.numel()
+
+
+def cache_workspace_bytes(num_pages, B):
+    """Scratch bytes of cache_fork, cache_reserve and cache_compact."""
+    return _lib.lib().sa_cache_workspace_bytes(num_pages, B)
+
+
+def cache_copy_pages(K_pages, V_pages, src, dst, stream=None):
+    """Copy page src[i] to page dst[i] in every layer; returns (K_pages, V_pages). No page twice in dst, or in both."""
+    layers, num_pages, page_bytes, _ = _pool_args(K_pages, V_pages)
+    dev = K_pages.device
+    _ints("src", src, dev, (None,))
+    _ints("dst", dst, dev, (src.numel(),))
+    _call("sa_cache_copy_pages", dev, stream, K_pages.data_ptr(), V_pages.data_ptr(), layers, num_pages, page_bytes,
+          src.data_ptr(), dst.data_ptr(), src.numel())
+    return K_pages, V_pages
+
+
+def cache_fork(K_pages, V_pages, block_table, seq_lens, ref_count, src, dst, out=None, stream=None):
+    """Rows dst[i] become copies of rows src[i]: whole pages shared, a partial last page copied.
+
+    Returns (block_table, seq_lens, ref_count).
+    """
+    layers, num_pages, page_bytes, page = _pool_args(K_pages, V_pages)
+    dev, B, max_pages, _ = _book(block_table, ref_count, num_pages, K_pages.device)
+    _ints("seq_lens", seq_lens, dev, (B,))
+    _ints("src", src, dev, (None,))
+    _ints("dst", dst, dev, (src.numel(),))
+    table, lens, refs = _outputs(out, (block_table, seq_lens, ref_count), stream)
+    n_bytes = cache_workspace_bytes(num_pages, B)
+    ws = _scratch(n_bytes, dev, stream)
+    _call("sa_cache_fork", dev, stream, K_pages.data_ptr(), V_pages.data_ptr(), layers, num_pages, page_bytes, page, B,
+          max_pages, src.data_ptr(), dst.data_ptr(), src.numel(), block_table.data_ptr(), seq_lens.data_ptr(),
+          ref_count.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(), _ptr(ws), n_bytes)
+    return table, lens, refs
+
+
+def cache_free(block_table, seq_lens, ref_count, rows, out=None, stream=None):
+    """The rows give up their pages; returns (block_table, seq_lens, ref_count)."""
+    dev, B, max_pages, num_pages = _book(block_table, ref_count)
+    _ints("seq_lens", seq_lens, dev, (B,))
+    _ints("rows", rows, dev, (None,))
+    table, lens, refs = _outputs(out, (block_table, seq_lens, ref_count), stream)
+    _call("sa_cache_free", dev, stream, num_pages, B, max_pages, rows.data_ptr(), rows.numel(), block_table.data_ptr(),
+          seq_lens.data_ptr(), ref_count.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
+    return table, lens, refs
+
+
+def cache_trim(block_table, seq_lens, ref_count, page, reach, global_idx=None, out=None, stream=None):
+    """Rows give up the pages that the window (reach tokens back) has left; returns (block_table, ref_count)."""
+    dev, B, max_pages, num_pages = _book(block_table, ref_count)
+    _ints("seq_lens", seq_lens, dev, (B,))
+    _ints("global_idx", global_idx, dev, (None,))
+    n_global = 0 if global_idx is None else global_idx.numel()
+    table, refs = _outputs(out, (block_table, ref_count), stream)
+    _call("sa_cache_trim", dev, stream, num_pages, page, B, max_pages, reach,
+          global_idx.data_ptr() if n_global else None, n_global, block_table.data_ptr(), seq_lens.data_ptr(),
+          ref_count.data_ptr(), table.data_ptr(), refs.data_ptr())
+    return table, refs
+
+
+def cache_reserve(block_table, seq_lens, q_lens, ref_count, page, out=None, stream=None):
+    """Pages for the new tokens [seq_lens - q_lens, seq_lens) of every row; returns (block_table, ref_count)."""
+    dev, B, max_pages, num_pages = _book(block_table, ref_count)
+    _ints("seq_lens", seq_lens, dev, (B,))
+    _ints("q_lens", q_lens, dev, (B,))
+    table, refs = _outputs(out, (block_table, ref_count), stream)
+    n_bytes = cache_workspace_bytes(num_pages, B)
+    ws = _scratch(n_bytes, dev, stream)
+    _call("sa_cache_reserve", dev, stream, num_pages, page, B, max_pages, seq_lens.data_ptr(), q_lens.data_ptr(),
+          block_table.data_ptr(), ref_count.data_ptr(), table.data_ptr(), refs.data_ptr(), _ptr(ws), n_bytes)
+    return table, refs
+
+
+def cache_compact(K_pages, V_pages, block_table, ref_count, out=None, stream=None):
+    """Leave the L pages in use at [0, L), in every layer; returns (block_table, ref_count)."""
+    layers, num_pages, page_bytes, _ = _pool_args(K_pages, V_pages)
+    dev, B, max_pages, _ = _book(block_table, ref_count, num_pages, K_pages.device)
+    table, refs = _outputs(out, (block_table, ref_count), stream)
+    n_bytes = cache_workspace_bytes(num_pages, B)
+    ws = _scratch(n_bytes, dev, stream)
+    _call("sa_cache_compact", dev, stream, K_pages.data_ptr(), V_pages.data_ptr(), layers, num_pages, page_bytes, B,
+          max_pages, block_table.data_ptr(), ref_count.data_ptr(), table.data_ptr(), refs.data_ptr(), _ptr(ws),
+          n_bytes)
+    return table, refs

@@ -58,7 +58,8 @@ typedef enum {
     SA_ERR_UNSUPPORTED = 2, /* valid arguments this build does not run (e.g. no sm_103a device) */
     SA_ERR_CUDA = 3,        /* a CUDA runtime/driver call or a kernel launch failed */
     SA_ERR_TIMEOUT = 4,     /* device: a bounded pipeline wait expired; the kernel exited cleanly */
-    SA_ERR_BAD_INDEX = 5    /* device: rand_idx / global_idx held an out-of-range or unsorted entry */
+    SA_ERR_BAD_INDEX = 5,   /* device: a table, a list or a length held an out-of-range or unsorted entry */
+    SA_ERR_NO_PAGES = 6     /* device: a page cache had fewer free pages than a call needed */
 } sa_status;
 
 typedef enum {
@@ -357,8 +358,8 @@ sa_status sa_set_workspace(void *dev_ptr, size_t bytes);
 
 /*
  * sa_get_last_device_status - synchronise `stream`, then read and clear the
- * current device's latched device status (SA_OK, SA_ERR_TIMEOUT or
- * SA_ERR_BAD_INDEX). Returns SA_ERR_CUDA if the synchronisation fails.
+ * current device's latched device status (SA_OK, SA_ERR_TIMEOUT,
+ * SA_ERR_BAD_INDEX or SA_ERR_NO_PAGES; the first of these that was latched). Returns SA_ERR_CUDA if the synchronisation fails.
  */
 sa_status sa_get_last_device_status(sa_stream_t stream);
 
@@ -450,6 +451,169 @@ sa_status bigbird_attn_fwd_noalloc(const void *Q, const void *K, const void *V, 
                                    int B, int H, int n, int d, int b, int g, int w, int r,
                                    const int32_t *rand_idx, const uint8_t *key_mask,
                                    sa_stream_t stream);
+
+/*
+ * The paged key/value cache: Longformer's autoregressive attention for callers
+ * that generate token by token. ("Longformer", App. B, trains and evaluates the
+ * autoregressive mode on whole sequences; the pages print no cache, so its
+ * layout is fixed here.)
+ *
+ * A pool holds `num_pages` pages of `page` tokens: K_pages and V_pages are
+ * DEVICE [num_pages][Hkv][page][d] arrays, contiguous, 16-byte aligned, page in
+ * {16, 32, 64, 128}, d in {64, 128}. A model keeps one pool of `layers` such
+ * slices, [layers][num_pages][Hkv][page][d]: page numbers mean the same page
+ * in every layer; the attention and the append take one layer's slice.
+ *
+ * block_table: DEVICE int32 [B][max_pages]. Entry c of row b is the page that
+ *   holds tokens [c * page, (c + 1) * page) of sequence b, or -1 for none.
+ * seq_lens: DEVICE int32 [B], tokens in the cache, the call's new ones included.
+ * q_lens: DEVICE int32 [B], how many of them are new, 0 <= q_lens[b] <= m, or
+ *   NULL (m each). New token t of sequence b sits at position
+ *   p = seq_lens[b] - q_lens[b] + t.
+ * ref_count: DEVICE int32 [num_pages], how many table entries name the page;
+ *   0 means free.
+ *
+ * Unlike the entry points above, these calls share nothing between them: no
+ * scratch of the library's, no counters. Scratch is an argument, so calls on
+ * different streams, and captured graphs, may overlap as long as each has its
+ * own workspace (16-byte aligned; it need not be cleared) and they do not
+ * write what another reads. Values on the device that break the contract
+ * latch SA_ERR_BAD_INDEX; nothing outside the arrays is ever touched.
+ * Limits: B <= 1024, max_pages * page <= 2^30, num_pages * Hkv < 2^31.
+ */
+
+/*
+ * longformer_attn_paged_fwd - longformer_attn_fwd_ex(causal = 1) for new tokens
+ * against the cache: a single token per sequence (m = 1), a few drafted ones,
+ * or a chunk of a prompt.
+ *
+ * New token t of sequence b, at position p, sees token j <= p iff j or p is
+ * global, or p - j = k (dilation[h] + 1) for some 0 <= k <= window / 2; and
+ * token j's page is there (block_table entry >= 0). The keys and values of the
+ * new tokens must be in the cache already (sa_cache_append). window =
+ * 2 * (max_pages * page) sees every earlier token.
+ *
+ * Q, O: DEVICE [B][Hq][m][d], contiguous, 16-byte aligned, O not aliasing Q.
+ * Hq: a multiple of Hkv, at most 64 query heads per key head; head h reads key
+ *   head h / (Hq / Hkv).
+ * Rows t >= q_lens[b], and rows that see no key, are written as zeros. What
+ * memory holds where no token was written, or at keys a row does not see, does
+ * not reach that row, infinities and NaN included.
+ * A sequence whose seq_lens or q_lens break the contract (or do not fit its
+ *   table row) gets zeros and latches SA_ERR_BAD_INDEX; a table entry outside
+ *   [-1, num_pages) counts as -1 and latches it.
+ * window: even, >= 0. dilation: DEVICE int32 [Hq] or NULL, as for
+ *   longformer_attn_fwd_ex. global_idx: DEVICE int32 [n_global], strictly
+ *   increasing positions, the same for every sequence; positions past a
+ *   sequence's end do not matter. n_global <= 512.
+ * Numerics: bf16 inputs: fp32 scores, softmax and sums; with more than 4 query
+ *   rows per key head (m * Hq / Hkv) the weights are rounded to bf16 for the
+ *   tensor cores, as in the calls above. fp32: fp32 throughout.
+ *   Deterministic: no atomics on values; splits are joined in a fixed order.
+ * workspace: sa_longformer_paged_workspace_bytes bytes (0: none needed), for
+ *   the partial results of long sweeps cut into pieces.
+ * Errors: SA_ERR_INVALID_ARG for any size or pointer outside the contract or a
+ *   workspace too small; SA_ERR_UNSUPPORTED without an sm_103 device, or past
+ *   the limits (B, group, n_global, lengths); SA_ERR_CUDA if a launch fails.
+ */
+sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const void *V_pages, void *O,
+                                    int B, int Hq, int Hkv, int m, int d,
+                                    int page, int num_pages, int max_pages,
+                                    const int32_t *block_table, const int32_t *seq_lens,
+                                    const int32_t *q_lens, int window, const int32_t *dilation,
+                                    const int32_t *global_idx, int n_global,
+                                    void *workspace, size_t workspace_bytes,
+                                    sa_dtype dtype, sa_stream_t stream);
+/* Scratch bytes of such a call on the current device (0 also for invalid
+ * sizes). The option SA_OPT_FORCE_SIMT must be the same for both calls. */
+size_t sa_longformer_paged_workspace_bytes(int B, int Hq, int Hkv, int m, int d, int page, int max_pages,
+                                           sa_dtype dtype);
+
+/*
+ * sa_cache_append - write the new tokens' keys and values into their pages.
+ *
+ * K_new, V_new: DEVICE [B][Hkv][m][d]; token t < q_lens[b] of sequence b goes
+ *   to position seq_lens[b] - q_lens[b] + t. Other pool contents are left as
+ *   they are. Tokens whose table entry names no page are dropped and latch
+ *   SA_ERR_BAD_INDEX, as does a sequence whose lengths break the contract
+ *   (nothing of it is written).
+ * Errors: as for longformer_attn_paged_fwd.
+ */
+sa_status sa_cache_append(const void *K_new, const void *V_new, void *K_pages, void *V_pages,
+                          int B, int Hkv, int m, int d, int page, int num_pages, int max_pages,
+                          const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_lens,
+                          sa_dtype dtype, sa_stream_t stream);
+
+/*
+ * Moving pages. K_pages, V_pages: DEVICE [layers][num_pages][page_bytes], with
+ * page_bytes = Hkv * page * d * element size (a multiple of 16). The
+ * bookkeeping arrays are read from *_in and written whole to *_out; the two may
+ * be the same array, and must not overlap otherwise. Page numbers are chosen
+ * by the inputs alone: the lowest free pages, in order.
+ * workspace: sa_cache_workspace_bytes(num_pages, B) bytes.
+ * Errors: SA_ERR_INVALID_ARG for sizes or pointers outside the contract or a
+ *   workspace too small; SA_ERR_UNSUPPORTED / SA_ERR_CUDA as above.
+ */
+size_t sa_cache_workspace_bytes(int num_pages, int B);
+
+/* sa_cache_copy_pages - page src[i] to page dst[i] of every layer of both
+ * pools, i < count (DEVICE int32 lists). No page may be named twice in dst, or
+ * be in src and dst both. Pairs out of range are skipped and latch
+ * SA_ERR_BAD_INDEX. */
+sa_status sa_cache_copy_pages(void *K_pages, void *V_pages, int layers, int num_pages, size_t page_bytes,
+                              const int32_t *src, const int32_t *dst, int count, sa_stream_t stream);
+
+/* sa_cache_fork - row dst[i] becomes a copy of row src[i], i < count (DEVICE
+ * int32 rows): whole pages are shared (ref_count + 1); a last page that is not
+ * full gets its own copy in the lowest free page, in order of i, so either row
+ * may append. dst rows must be empty (length 0; pages they hold in reserve are
+ * given back), named once, and no row may be a source and a destination; a
+ * pair that breaks this is skipped and latches SA_ERR_BAD_INDEX (of pairs with
+ * one destination the first counts). Out of free pages: dst[i] stays empty and
+ * SA_ERR_NO_PAGES is latched. */
+sa_status sa_cache_fork(void *K_pages, void *V_pages, int layers, int num_pages, size_t page_bytes,
+                        int page, int B, int max_pages, const int32_t *src, const int32_t *dst, int count,
+                        const int32_t *table_in, const int32_t *lens_in, const int32_t *ref_in,
+                        int32_t *table_out, int32_t *lens_out, int32_t *ref_out,
+                        void *workspace, size_t workspace_bytes, sa_stream_t stream);
+
+/* sa_cache_free - the rows named (DEVICE int32 [count]) give up their pages:
+ * ref_count - 1 each, table entries -1, length 0. A row named twice gives them
+ * up once; rows out of range latch SA_ERR_BAD_INDEX, as does a page whose count
+ * is already 0 (it stays 0). */
+sa_status sa_cache_free(int num_pages, int B, int max_pages, const int32_t *rows, int count,
+                        const int32_t *table_in, const int32_t *lens_in, const int32_t *ref_in,
+                        int32_t *table_out, int32_t *lens_out, int32_t *ref_out, sa_stream_t stream);
+
+/* sa_cache_trim - every row gives up the pages that the window has left: pages
+ * all of whose tokens lie before seq_lens[b] - reach and that hold no global
+ * position. reach = window / 2 * (largest dilation + 1). A sequence with a
+ * global position still to come (global_idx's last >= seq_lens[b]) keeps every
+ * page, as that token will see them all. Call it when the tokens so far have
+ * been attended to. */
+sa_status sa_cache_trim(int num_pages, int page, int B, int max_pages, int reach,
+                        const int32_t *global_idx, int n_global,
+                        const int32_t *table_in, const int32_t *seq_lens, const int32_t *ref_in,
+                        int32_t *table_out, int32_t *ref_out, sa_stream_t stream);
+
+/* sa_cache_reserve - pages for the new tokens [seq_lens[b] - q_lens[b],
+ * seq_lens[b]) of every row: each table entry past the old tokens' last page up
+ * to the new last page that is -1 gets the lowest free page (ref_count 1), rows
+ * in order. With too few free pages the last entries stay -1 and
+ * SA_ERR_NO_PAGES is latched. */
+sa_status sa_cache_reserve(int num_pages, int page, int B, int max_pages,
+                           const int32_t *seq_lens, const int32_t *q_lens,
+                           const int32_t *table_in, const int32_t *ref_in,
+                           int32_t *table_out, int32_t *ref_out,
+                           void *workspace, size_t workspace_bytes, sa_stream_t stream);
+
+/* sa_cache_compact - leaves the L pages in use (ref_count > 0) at [0, L): the
+ * k-th page in use at or past L moves, in every layer of both pools, to the
+ * k-th free page before L; table and counts follow. */
+sa_status sa_cache_compact(void *K_pages, void *V_pages, int layers, int num_pages, size_t page_bytes,
+                           int B, int max_pages, const int32_t *table_in, const int32_t *ref_in,
+                           int32_t *table_out, int32_t *ref_out,
+                           void *workspace, size_t workspace_bytes, sa_stream_t stream);
 
 #ifdef __cplusplus
 }
