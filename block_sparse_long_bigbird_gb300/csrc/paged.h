@@ -44,15 +44,17 @@ struct PagedProblem {
     float2 *part_ml; // [slots][rows] (running maximum, sum)
 };
 
-// Which kernel serves a call: few rows per key head, or many.
-enum PagedKernel { kPagedRows = 0, kPagedTile = 1 };
+// Which kernel serves a call: few rows per key head, many rows in bf16 on the
+// tensor cores, or many rows on the ordinary units.
+enum PagedKernel { kPagedRows = 0, kPagedTc = 1, kPagedTile = 2 };
 
 // Fills the launcher's fields of `p` and says which kernel runs it.
-PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, int num_sms);
+PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms);
 // Scratch of one call: partial results of split sweeps (0: nothing is split).
 size_t paged_workspace_bytes(const PagedProblem &p);
 cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_tile(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_tc(const PagedProblem &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream);
 
 // Writing and moving pages (paged_cache.cu).

@@ -12,7 +12,7 @@ namespace sa {
 // cache with the ordinary units.
 static int rows_limit(sa_dtype dtype) { return dtype == SA_FP32 ? 8 : 4; }
 
-PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, int num_sms) {
+PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms) {
     p.group = p.Hq / p.Hkv;
     p.log_page = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)p.d);
@@ -23,6 +23,16 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, int num_sms) {
         p.target = 4 * num_sms;
         p.min_split = 4;
         return kPagedRows;
+    }
+    if (dtype == SA_BF16 && !force_simt) {
+        const int most = 128 / p.group;
+        p.tpt_half = p.m < most ? p.m : most;
+        const int halves = p.m > p.tpt_half ? 2 : 1;
+        p.tpt = halves * p.tpt_half;
+        p.rows = halves * p.tpt_half * p.group;
+        p.target = 2 * num_sms;
+        p.min_split = 8;
+        return kPagedTc;
     }
     const int most = 64 / p.group;
     p.tpt = p.tpt_half = p.m < most ? p.m : most;
@@ -125,7 +135,7 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
     p.gidx = n_global > 0 ? global_idx : nullptr;
     p.ng = n_global;
     p.wait_ns = sa::api_wait_ns();
-    const sa::PagedKernel kind = sa::paged_shape(p, dtype, sms);
+    const sa::PagedKernel kind = sa::paged_shape(p, dtype, sa::api_force_simt(), sms);
     const size_t need = sa::paged_workspace_bytes(p);
     if (need) {
         if (ws_ok(workspace, workspace_bytes, need) != SA_OK) return SA_ERR_INVALID_ARG;
@@ -134,6 +144,7 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
     }
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = kind == sa::kPagedRows ? sa::launch_paged_rows(p, dtype, sms, cs)
+                    : kind == sa::kPagedTc ? sa::launch_paged_tc(p, sms, cs)
                                            : sa::launch_paged_tile(p, dtype, sms, cs);
     if (e == cudaSuccess && need) e = sa::launch_paged_merge(p, dtype, sms, cs);
     return finish(e, need ? 2 : 1);
@@ -149,7 +160,7 @@ size_t sa_longformer_paged_workspace_bytes(int B, int Hq, int Hkv, int m, int d,
     if (sa::api_device(&status, &sms) != SA_OK) return 0;
     sa::PagedProblem p = {};
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.m = m; p.d = d; p.page = page; p.max_pages = max_pages;
-    sa::paged_shape(p, dtype, sms);
+    sa::paged_shape(p, dtype, sa::api_force_simt(), sms);
     return sa::paged_workspace_bytes(p);
 }
 

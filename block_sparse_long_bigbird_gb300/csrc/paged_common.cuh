@@ -29,6 +29,8 @@ __device__ __forceinline__ uint64_t low_bits(int c) {  // bits [0, c), c clamped
     return c <= 0 ? 0ull : (c >= 64 ? ~0ull : ((1ull << c) - 1ull));
 }
 
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.402823466e38f); }
+
 // The plan in shared memory. Arrays over sequences, then the global list.
 struct Plan {
     int *q, *s;        // [B] new tokens and tokens in the cache (q = 0 for a refused sequence)
@@ -387,6 +389,11 @@ __device__ __noinline__ float2 exact_row(const PagedProblem &p, const Plan &P, c
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAllLanes, s, o);
             if (s == -CUDART_INF_F) continue;  // weight 0 whatever the maximum
+            if (not_finite(s)) {  // +inf or NaN: so is every element of the row
+#pragma unroll
+                for (int x = 0; x < E; ++x) acc[x] = CUDART_NAN_F;
+                return make_float2(0.f, CUDART_NAN_F);
+            }
             const float mn = fmaxf(m, s);
             const float f = m == -CUDART_INF_F ? 0.f : ptx::ex2(m - mn), w1 = ptx::ex2(s - mn);
             l = l * f + w1;
@@ -417,8 +424,6 @@ __device__ __forceinline__ void store_exact_row(const PagedProblem &p, const Uni
         for (int i = 0; i < E; ++i) O[i] = from_float<T>(acc[i] * inv);
     }
 }
-
-__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.402823466e38f); }
 
 }  // namespace
 }  // namespace sa
