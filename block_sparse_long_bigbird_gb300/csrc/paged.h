@@ -36,8 +36,11 @@ struct PagedProblem {
     int tpt;         // tokens per unit
     int tpt_half;    // tokens per half of a unit (tpt: units of one half)
     int rows;        // rows per unit: tpt * group
-    int target;      // units aimed at when long sweeps are split
-    int min_split;   // fewest 64-key blocks worth a unit of their own
+    int cut;         // whether sweeps may be split (then paged_merge is launched)
+    int slots;       // units that run at a time
+    int max_parts;   // partial results that the workspace holds
+    int min_split;   // fewest 64-key blocks of a split
+    int cost_plain, cost_split;  // what a whole and a split unit cost beside their blocks, in blocks
     float scale_log2;
     unsigned long long wait_ns;
     float *part_o;   // [slots][rows][d] partial sums of split sweeps
@@ -50,11 +53,13 @@ enum PagedKernel { kPagedRows = 0, kPagedTc = 1, kPagedTile = 2 };
 
 // Fills the launcher's fields of `p` and says which kernel runs it.
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms);
+// CTAs of the streaming kernel that fit an SM, by the rows of a unit.
+inline int paged_rows_ctas(int rows) { return rows <= 1 ? 3 : rows <= 4 ? 2 : 1; }
 // Scratch of one call: partial results of split sweeps (0: nothing is split).
 size_t paged_workspace_bytes(const PagedProblem &p);
-cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream);
-cudaError_t launch_paged_tile(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream);
-cudaError_t launch_paged_tc(const PagedProblem &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream);
+cudaError_t launch_paged_tile(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream);
+cudaError_t launch_paged_tc(const PagedProblem &p, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream);
 
 // Writing and moving pages (paged_cache.cu).

@@ -10,6 +10,7 @@ namespace sa {
 
 // At most this many query rows of a key head go to the kernel that streams the
 // cache with the ordinary units.
+constexpr int kNoCutBlocks = 16;
 static int rows_limit(sa_dtype dtype) { return dtype == SA_FP32 ? 8 : 4; }
 
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms) {
@@ -17,41 +18,47 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     p.log_page = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)p.d);
     const long long rows = (long long)p.m * p.group;
+    PagedKernel kind;
     if (rows <= rows_limit(dtype)) {
+        kind = kPagedRows;
         p.tpt = p.tpt_half = p.m;
         p.rows = (int)rows;
-        p.target = 4 * num_sms;
+        p.slots = num_sms * paged_rows_ctas(p.rows);
+        p.max_parts = 16 * num_sms;
         p.min_split = 4;
-        return kPagedRows;
-    }
-    if (dtype == SA_BF16 && !force_simt) {
+        p.cost_plain = 2;
+        p.cost_split = 3;
+    } else if (dtype == SA_BF16 && !force_simt) {
+        kind = kPagedTc;
         const int most = 128 / p.group;
         p.tpt_half = p.m < most ? p.m : most;
         const int halves = p.m > p.tpt_half ? 2 : 1;
         p.tpt = halves * p.tpt_half;
         p.rows = halves * p.tpt_half * p.group;
-        p.target = 2 * num_sms;
+        p.slots = num_sms;
+        p.max_parts = 8 * num_sms;
         p.min_split = 8;
-        return kPagedTc;
+        p.cost_plain = 3;
+        p.cost_split = 6;
+    } else {
+        kind = kPagedTile;
+        const int most = 64 / p.group;
+        p.tpt = p.tpt_half = p.m < most ? p.m : most;
+        p.rows = p.tpt * p.group;
+        p.slots = 2 * num_sms;
+        p.max_parts = 16 * num_sms;
+        p.min_split = 2;
+        p.cost_plain = 1;
+        p.cost_split = 2;
     }
-    const int most = 64 / p.group;
-    p.tpt = p.tpt_half = p.m < most ? p.m : most;
-    p.rows = p.tpt * p.group;
-    p.target = 4 * num_sms;
-    p.min_split = 4;
-    return kPagedTile;
-}
-
-// The plan (paged_common.cuh) cuts a sweep of e blocks into ceil(e / len)
-// pieces only if e > len, with len >= (sum of e) / target: the pieces of cut
-// sweeps are fewer than 2 * target. No sweep is longer than its table row.
-static bool may_split(const PagedProblem &p) {
-    return ((long long)p.max_pages << p.log_page) > 64ll * p.min_split;
+    // No sweep is longer than its table row; short ones are not cut, which
+    // saves the launch that joins the pieces.
+    p.cut = ((long long)p.max_pages << p.log_page) > 64ll * kNoCutBlocks;
+    return kind;
 }
 
 size_t paged_workspace_bytes(const PagedProblem &p) {
-    if (!may_split(p)) return 0;
-    return 2 * (size_t)p.target * p.rows * (p.d + 2) * sizeof(float);
+    return p.cut ? (size_t)p.max_parts * p.rows * (p.d + 2) * sizeof(float) : 0;
 }
 
 }  // namespace sa
@@ -140,12 +147,12 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
     if (need) {
         if (ws_ok(workspace, workspace_bytes, need) != SA_OK) return SA_ERR_INVALID_ARG;
         p.part_o = static_cast<float *>(workspace);
-        p.part_ml = reinterpret_cast<float2 *>(p.part_o + 2 * (size_t)p.target * p.rows * p.d);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)p.max_parts * p.rows * p.d);
     }
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = kind == sa::kPagedRows ? sa::launch_paged_rows(p, dtype, sms, cs)
-                    : kind == sa::kPagedTc ? sa::launch_paged_tc(p, sms, cs)
-                                           : sa::launch_paged_tile(p, dtype, sms, cs);
+    cudaError_t e = kind == sa::kPagedRows ? sa::launch_paged_rows(p, dtype, cs)
+                    : kind == sa::kPagedTc ? sa::launch_paged_tc(p, cs)
+                                           : sa::launch_paged_tile(p, dtype, cs);
     if (e == cudaSuccess && need) e = sa::launch_paged_merge(p, dtype, sms, cs);
     return finish(e, need ? 2 : 1);
 }

@@ -16,12 +16,28 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "paged.h"
 #include "sm103_ptx.cuh"
 
 namespace sa {
 namespace {
+
+// Lets a kernel use up to the largest dynamic shared memory, once per device.
+template <typename K>
+inline cudaError_t allow_smem(K kern, std::atomic<bool> (&done)[64], size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
 
 constexpr unsigned kAllLanes = 0xffffffffu;
 
@@ -40,12 +56,18 @@ struct Plan {
     int *gpos;         // [ng] global positions
     int *gblk;         // [ngb] 64-key blocks that hold one, ascending
     uint64_t *gbit;    // [ngb] which of their keys
-    int *misc;         // [0] ngb, [1] longest stride of a dilated head
+    int *misc;         // [0] ngb, [1] longest stride of a dilated head, [2] longest sweep, [4 + 2 k] costs of kCuts
     int ngb, max_stride;
 };
 
+// Splits tried for the longest sweep.
+constexpr int kCuts = 16;
+__device__ __forceinline__ int cut_of(int k) {
+    return k < 6 ? k + 1 : k < 9 ? 2 * k - 4 : k < 10 ? 16 : k < 11 ? 24 : k < 12 ? 32 : k < 13 ? 48 : k < 14 ? 64 : k < 15 ? 96 : 128;
+}
+
 __host__ __device__ inline size_t plan_bytes(int B, int ng) {
-    const size_t ints = 5 * (size_t)B + 2 + 2 * (size_t)ng + 2;
+    const size_t ints = 5 * (size_t)B + 2 + 2 * (size_t)ng + 4 + kCuts;
     return ((ints * 4 + 15) & ~(size_t)15) + (size_t)ng * 8;
 }
 
@@ -124,7 +146,10 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
         }
         P.gpos[i] = v;
     }
-    if (tid == 0) P.misc[1] = 1;
+    if (tid == 0) {
+        P.misc[1] = 1;
+        P.misc[2] = 0;
+    }
     __syncthreads();
     if (p.dilation)
         for (int h = tid; h < p.Hq; h += nthr) atomicMax(&P.misc[1], head_stride(p, h));
@@ -158,17 +183,55 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     __syncthreads();
     P.ngb = P.misc[0];
     P.max_stride = P.misc[1];
-    if (tid < 32) {
-        // total work in blocks, the split length it implies, then the prefixes
-        long long total = 0;
-        for (int b = lane; b < p.B; b += 32) {
-            const int tiles = (P.q[b] + p.tpt - 1) / p.tpt;
-            total += (long long)tiles * p.Hkv * estimate_blocks(p, P, P.q[b], P.s[b]);
+    // The longest sweep, then what each way of cutting it (and the others into
+    // pieces as long) would cost: rounds of `slots` units of mean length, and a
+    // last round as long as the longest piece. A split unit costs more, as it
+    // writes partial results that are read again.
+    int len = 0x3fffffff;
+    if (p.cut) {
+        const int warp = tid >> 5, nwarps = nthr >> 5;
+        if (tid < p.B) {
+            int e = 0;
+            for (int b = tid; b < p.B; b += nthr) e = max(e, estimate_blocks(p, P, P.q[b], P.s[b]));
+            atomicMax(&P.misc[2], e);
         }
+        __syncthreads();
+        const int longest = P.misc[2];
+        for (int k = warp; k < kCuts; k += nwarps) {
+            const int piece = (longest + cut_of(k) - 1) / cut_of(k);
+            int units = 0, parts = 0;
+            long long total = 0;
+            for (int b = lane; b < p.B; b += 32) {
+                const int n = (P.q[b] + p.tpt - 1) / p.tpt * p.Hkv;
+                const int e = estimate_blocks(p, P, P.q[b], P.s[b]);
+                const int ns = piece > 0 && e > piece ? (e + piece - 1) / piece : 1;
+                units += n * ns;
+                parts += ns > 1 ? n * ns : 0;
+                total += (long long)n * e;
+            }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kAllLanes, total, o);
-        const long long want = (total + p.target - 1) / p.target;
-        const int len = want > p.min_split ? (int)(want > 0x3fffffff ? 0x3fffffff : want) : p.min_split;
+            for (int o = 16; o; o >>= 1) {
+                units += __shfl_xor_sync(kAllLanes, units, o);
+                parts += __shfl_xor_sync(kAllLanes, parts, o);
+                total += __shfl_xor_sync(kAllLanes, total, o);
+            }
+            if (lane == 0) {
+                // in 1/16 blocks; a cut that is too short or needs too much scratch is out
+                const long long own = 16 * total + 16ll * (units - parts) * p.cost_plain + 16ll * parts * p.cost_split;
+                const int u = max(units, 1);
+                const long long mean = own / u;
+                long long cost = (long long)((u + p.slots - 1) / p.slots) * mean + 16ll * piece - 16 * total / u;
+                if (k > 0 && (piece < p.min_split || parts > p.max_parts)) cost = 0x7fffffff;
+                P.misc[4 + k] = (int)(cost > 0x7fffffff ? 0x7fffffff : cost);
+            }
+        }
+        __syncthreads();
+        int best = 0;
+        for (int k = 1; k < kCuts; ++k)
+            if (P.misc[4 + k] < P.misc[4 + best]) best = k;
+        len = max(1, (longest + cut_of(best) - 1) / cut_of(best));
+    }
+    if (tid < 32) {
         const int all_tiles = (p.m + p.tpt - 1) / p.tpt;
         int ubase = 0, sbase = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -176,7 +239,7 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
             int nu = 0, nslot = 0, ns = 1;
             if (b < p.B) {
                 const int tiles = (P.q[b] + p.tpt - 1) / p.tpt;
-                const int est = estimate_blocks(p, P, P.q[b], P.s[b]);
+                const int est = p.cut ? estimate_blocks(p, P, P.q[b], P.s[b]) : 0;
                 ns = est > len ? (est + len - 1) / len : 1;
                 nu = p.Hkv * (tiles * ns + all_tiles - tiles);
                 nslot = ns > 1 ? p.Hkv * tiles * ns : 0;

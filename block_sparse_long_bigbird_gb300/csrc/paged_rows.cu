@@ -324,36 +324,34 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge(const PagedProbl
 }
 
 template <typename T, int D, int R>
-cudaError_t launch_rows(const PagedProblem &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rows(const PagedProblem &p, cudaStream_t stream) {
     const size_t smem = (size_t)kRowsWarps * R * (D + 2) * 4 + plan_bytes(p.B, p.ng);
+    static std::atomic<bool> done[64];
     auto kern = paged_rows<T, D, R>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kern, done, smem);
     if (e != cudaSuccess) return e;
-    int per_sm = 1;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kRowsWarps * 32, smem)) != cudaSuccess) return e;
-    const long long units = (long long)p.B * p.Hkv + 2ll * p.target;
-    const long long grid = (long long)num_sms * (per_sm < 1 ? 1 : per_sm);
-    kern<<<(int)(units < grid ? units : grid), kRowsWarps * 32, smem, stream>>>(p);
+    const long long units = (long long)p.B * p.Hkv + (p.cut ? p.max_parts : 0);
+    kern<<<(int)(units < p.slots ? units : p.slots), kRowsWarps * 32, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t launch_rows_r(const PagedProblem &p, int num_sms, cudaStream_t stream) {
-    if (p.rows <= 1) return launch_rows<T, D, 1>(p, num_sms, stream);
-    if (p.rows <= 2) return launch_rows<T, D, 2>(p, num_sms, stream);
+cudaError_t launch_rows_r(const PagedProblem &p, cudaStream_t stream) {
+    if (p.rows <= 1) return launch_rows<T, D, 1>(p, stream);
+    if (p.rows <= 2) return launch_rows<T, D, 2>(p, stream);
     if constexpr (sizeof(T) == 4) {
-        if (p.rows > 4) return launch_rows<T, D, 8>(p, num_sms, stream);
+        if (p.rows > 4) return launch_rows<T, D, 8>(p, stream);
     }
-    return launch_rows<T, D, 4>(p, num_sms, stream);
+    return launch_rows<T, D, 4>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream) {
+cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream) {
     if (dtype == SA_FP32)
-        return p.d == 64 ? launch_rows_r<float, 64>(p, num_sms, stream) : launch_rows_r<float, 128>(p, num_sms, stream);
-    return p.d == 64 ? launch_rows_r<__nv_bfloat16, 64>(p, num_sms, stream)
-                     : launch_rows_r<__nv_bfloat16, 128>(p, num_sms, stream);
+        return p.d == 64 ? launch_rows_r<float, 64>(p, stream) : launch_rows_r<float, 128>(p, stream);
+    return p.d == 64 ? launch_rows_r<__nv_bfloat16, 64>(p, stream)
+                     : launch_rows_r<__nv_bfloat16, 128>(p, stream);
 }
 
 cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream) {
@@ -361,9 +359,8 @@ cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sm
     void (*kern)(const PagedProblem) =
         dtype == SA_FP32 ? (p.d == 64 ? paged_merge<float, 64> : paged_merge<float, 128>)
                          : (p.d == 64 ? paged_merge<__nv_bfloat16, 64> : paged_merge<__nv_bfloat16, 128>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const long long items = 2ll * p.target * p.rows, grid = 8ll * num_sms;
+    // no more shared memory than a kernel has without asking: the largest plan takes 29 KB
+    const long long items = (long long)p.max_parts * p.rows, grid = 8ll * num_sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items < grid ? items : grid));
     cfg.blockDim = dim3(kMergeWarps * 32);

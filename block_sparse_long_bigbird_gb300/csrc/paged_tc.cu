@@ -59,10 +59,11 @@ struct TcCfg {
     static constexpr int BAR_OFF = ST_OFF + NST * TILE;
     static constexpr int B_KF = 0, B_KE = B_KF + NST, B_IF = B_KE + NST, B_IE = B_IF + kSI, B_QF = B_IE + kSI,
                          B_QE = B_QF + 1, B_SF = B_QE + 1, B_PF = B_SF + 2, B_OF = B_PF + 2, B_OE = B_OF + 2,
-                         B_DRAIN = B_OE + 2, B_COUNT = B_DRAIN + 1;
+                         B_MF = B_OE + 2, B_ME = B_MF + 1, B_DRAIN = B_ME + 1, B_COUNT = B_DRAIN + 1;
     static constexpr int REC_OFF = (BAR_OFF + B_COUNT * 8 + 15) & ~15;
     static constexpr int MISC_OFF = REC_OFF + kSI * (int)sizeof(StepRec);
-    static constexpr int PLAN_OFF = MISC_OFF + 16;
+    static constexpr int ML_OFF = MISC_OFF + 16;       // one-tile units: the second chain's (maximum, sum) per row
+    static constexpr int PLAN_OFF = ML_OFF + 128 * 8;
     static constexpr uint32_t O_COL = 256;
 };
 static_assert(sizeof(StepRec) == 56 && (kSI * sizeof(StepRec)) % 16 == 0, "step record layout");
@@ -120,6 +121,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(bar(C::B_OF + x), 1);
             mbar_init(bar(C::B_OE + x), 4);
         }
+        mbar_init(bar(C::B_MF), 4);
+        mbar_init(bar(C::B_ME), 4);
         mbar_init(bar(C::B_DRAIN), 1);
         fence_mbar_init();
     }
@@ -140,7 +143,255 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int total = P.ubase[p.B];
     uint32_t g = 0;   // steps so far; every role counts the same ones
     bool ok = true;
+    const bool one = p.tpt == p.tpt_half;  // units of one tile: its steps alternate between two chains
 
+    // The launch gave every thread 168 registers (384 x 168 = 64512); the
+    // softmax holds a row of scores, so its 8 warps take 200 and the others 104
+    // (256 x 200 + 128 x 104 = 64512).
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ================================================================ softmax and epilogue of tile x
+        const int x = warp >> 2;
+        const int tid = threadIdx.x & 127;  // row of the tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + x * 128, o_addr = tmem + lane_base + C::O_COL + x * D;
+        const int half_rows = p.tpt_half * p.group;
+        const float sl2 = p.scale_log2;
+        uint32_t sc = 0, oc = 0, oc2 = 0, mc = 0;
+        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+            const Unit U = decode_unit(p, P, u);
+            const int n = U.live ? (U.e1 - U.e0 + 1) >> 1 : 0;
+            int t = 0, head = 0;
+            Row row = {};
+            const bool in = tid < half_rows;
+            if (in) {
+                row_token(p, U, tid, p.tpt_half, t, head);
+                if (!one) t += x * p.tpt_half;
+                row = make_row(p, P, U, head, t);
+            }
+            const bool busy = __any_sync(kAllLanes, row.valid);
+            float mref = -CUDART_INF_F, l = 0.f;
+            bool had = false;
+            for (int i = 0; i < n; ++i, ++g) {
+                const uint32_t slot = g % kSI;
+                if (!(ok = wait_warp(bar(C::B_IF + slot), (g / kSI) & 1, ctl))) break;
+                const int use = recs[slot].use, vz0 = recs[slot].vz0, vz1 = recs[slot].vz1;
+                uint64_t w[2] = {0ull, 0ull};
+                if (((use >> x) & 1) && row.valid) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (recs[slot].blk[k] >= 0)
+                            w[k] = row_mask(row, recs[slot].blk[k], recs[slot].gbits[k], recs[slot].present[k]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
+                if (!((use >> x) & 1)) continue;
+                if (vz0 < vz1) {  // unwritten memory: no NaN may meet a zero weight
+                    const uint32_t sidx = 2 * g + 1, st = sidx % C::NST;
+                    if (!(ok = wait_warp(bar(C::B_KF + st), (sidx / C::NST) & 1, ctl))) break;
+                    uint8_t *v = smem + C::ST_OFF + st * C::TILE;
+                    for (int c = tid; c < (vz1 - vz0) * 8 * C::DC; c += 128) {
+                        const int r = vz0 + c / (8 * C::DC), q = c % (8 * C::DC);
+                        *reinterpret_cast<uint4 *>(v + (q >> 3) * kRegion + r * 128 + (q & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!(ok = wait_warp(bar(C::B_SF + x), sc & 1, ctl))) break;
+                ++sc;
+                if (busy) {
+                    tc_fence_after();
+                    const bool full = __all_sync(kAllLanes, (w[0] & w[1]) == ~0ull || !row.valid);
+                    float s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, s[c]);
+                    tmem_wait_ld();
+                    if (!full) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t b = (uint32_t)(w[c >> 1] >> ((c & 1) * 32));
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) s[c][k] = (b >> k) & 1u ? s[c][k] : -CUDART_INF_F;
+                        }
+                    }
+                    float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) mx4[c] = fmax3(mx4[c], s[c][k], s[c][k + 1]);
+                    float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+                    mx = row.valid ? mx * sl2 : -CUDART_INF_F;
+                    const bool grow = mx > mref + kGrow || (mref == -CUDART_INF_F && mx > mref);
+                    if (__any_sync(kAllLanes, grow)) {
+                        const float ref = grow ? mx : mref;
+                        const float f = grow ? ex2(mref - ref) : 1.f;  // 0 the first time
+                        l *= f;
+                        mref = ref;
+                        if (had) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                tmem_ld32(o_addr + c * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= f;
+                                tmem_st32(o_addr + c * 32, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float nref = mref == -CUDART_INF_F ? 0.f : -mref;
+                    const uint64_t sl2x2 = f2_pack(sl2, sl2), nrefx2 = f2_pack(nref, nref);
+                    uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                float a, e;
+                                f2_unpack(f2_fma(f2_pack(s[2 * h + c][k], s[2 * h + c][k + 1]), sl2x2, nrefx2), a, e);
+                                a = ex2(a);
+                                e = ex2(e);
+                                if (k & 2) sum1 = f2_add(sum1, f2_pack(a, e));
+                                else sum0 = f2_add(sum0, f2_pack(a, e));
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(a, e);
+                                pk[c * 16 + k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                        tmem_st32u(s_addr + h * 32, pk);
+                    }
+                    float a, e;
+                    f2_unpack(f2_add(sum0, sum1), a, e);
+                    l += a + e;
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                had = true;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_PF + x));
+            }
+            if (!ok) break;
+            // ---- epilogue
+            // One-tile units: the second chain hands over its maximum and sum, and
+            // the first chain's warps join both O's (they hold the same lanes).
+            bool had2 = false;
+            float f1 = 1.f, f2 = 0.f;
+            if (one && n > 0) {
+                float2 *ml = reinterpret_cast<float2 *>(smem + C::ML_OFF);
+                if (x == 1) {
+                    if (mc > 0 && !(ok = wait_warp(bar(C::B_ME), (mc - 1) & 1, ctl))) break;
+                    ml[tid] = make_float2(had ? mref : -CUDART_INF_F, had ? l : -1.f);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_MF));
+                    ++mc;
+                    continue;
+                }
+                if (!(ok = wait_warp(bar(C::B_MF), mc & 1, ctl))) break;
+                ++mc;
+                const float2 other = ml[tid];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_ME));
+                had2 = other.y >= 0.f || other.y != other.y;  // -1: no step was its own
+                if (had2) {
+                    const float m = fmaxf(mref, other.x), ref = m == -CUDART_INF_F ? 0.f : m;
+                    f1 = ex2(mref - ref);
+                    f2 = ex2(other.x - ref);
+                    l = l * f1 + other.y * f2;
+                    mref = m;
+                }
+                had2 = __any_sync(kAllLanes, had2);
+            } else if (one && x == 1) {
+                continue;  // the first chain's warps write the zeros
+            }
+            if (had) {
+                if (!(ok = wait_warp(bar(C::B_OF + x), oc & 1, ctl))) break;
+                ++oc;
+                tc_fence_after();
+            }
+            if (had2) {
+                if (!(ok = wait_warp(bar(C::B_OF + 1), oc2 & 1, ctl))) break;
+                ++oc2;
+                tc_fence_after();
+            }
+            const int prow = x * half_rows + tid;  // row within the unit
+            bool bad = false;
+            const float inv = row.valid && l != 0.f ? 1.f / l : 0.f;
+            if (busy || !had) {
+                __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.O) +
+                                      (((size_t)U.b * p.Hq + head) * p.m + (t < p.m ? t : 0)) * D;
+                const size_t at = (size_t)U.slot * p.rows + prow;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    if (had) {
+                        tmem_ld32(o_addr + c * 32, o);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                    }
+                    if (had2) {
+                        float o2[32];
+                        tmem_ld32(o_addr + D + c * 32, o2);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = o[k] * f1 + o2[k] * f2;
+                    }
+                    float z = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);  // NaN if any is infinite or NaN
+                    bad |= z != 0.f;
+                    if (!in || (!row.valid && t >= p.m)) continue;
+                    if (U.ns > 1) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(p.part_o + at * D + c * 32 + k) =
+                                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t b4[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float a = row.valid ? o[q * 8 + 2 * k] * inv : 0.f;
+                                const float e = row.valid ? o[q * 8 + 2 * k + 1] * inv : 0.f;
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(a, e);
+                                b4[k] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                            *reinterpret_cast<uint4 *>(orow + c * 32 + q * 8) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+                        }
+                    }
+                }
+                if (U.ns > 1 && in) p.part_ml[at] = make_float2(row.valid ? mref : -CUDART_INF_F, row.valid ? l : 0.f);
+            } else if (U.ns > 1 && in) {  // no valid row in this warp: the merge writes their zeros
+                p.part_ml[(size_t)U.slot * p.rows + prow] = make_float2(-CUDART_INF_F, 0.f);
+            } else if (in && t < p.m) {
+                uint4 *orow = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.O) +
+                                                        (((size_t)U.b * p.Hq + head) * p.m + t) * D);
+                for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (had || had2) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (had) mbar_arrive(bar(C::B_OE + x));
+                    if (had2) mbar_arrive(bar(C::B_OE + 1));
+                }
+            }
+            unsigned again = __ballot_sync(kAllLanes, row.valid && (had || had2) && (bad || not_finite(l)));
+            while (again) {
+                const int r = __ffs(again) - 1;
+                again &= again - 1;
+                const int rt = __shfl_sync(kAllLanes, t, r), rh = __shfl_sync(kAllLanes, head, r);
+                float a[D / 32];
+                __syncwarp();
+                const float2 ml = exact_row<__nv_bfloat16, D>(p, P, U, rt, rh, a);
+                store_exact_row<__nv_bfloat16, D>(p, U, rt, rh, x * half_rows + (warp & 3) * 32 + r, ml, a);
+            }
+        }
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 8) {
         // ================================================================ producer
         const int bp = min(p.page, 64);      // tokens of a box
@@ -210,6 +461,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         r.vz1 = k * 64 + 64;
                     }
                 }
+                if (one) r.use = (r.use & 1) << (i & 1);
                 if (g >= kSI && !(ok = wait_warp(bar(C::B_IE + slot), ((g / kSI) - 1) & 1, ctl))) break;
                 if (lane == 0) {
                     recs[slot] = r;
@@ -275,9 +527,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!(ok = wait_warp(bar(C::B_KF + sk), ((2 * g) / C::NST) & 1, ctl))) break;
                 }
                 if (i > 0 && !(ok = wait_warp(bar(C::B_KF + sv), ((2 * g - 1) / C::NST) & 1, ctl))) break;
+                auto scores = [&](int x) {
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t dQ = dQ0 + (uint64_t)(((one ? 0 : x) * C::TILE) >> 4);
+                        const uint64_t dK = dK0 + (uint64_t)((sk * C::TILE) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
+                            mma_bf16_ss(tmem + x * 128, dQ + off, dK + off, idesc_qk, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(bar(C::B_SF + x));
+                    }
+                    __syncwarp();
+                };
+                // chains that do not follow on themselves need not wait for the other's weights
+                const bool early = (prev & use) == 0;
+                if (early) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if ((use >> x) & 1) scores(x);
+                }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const uint32_t s_col = tmem + x * 128, o_col = tmem + C::O_COL + x * D;
                     if ((prev >> x) & 1) {
                         if (!(ok = wait_warp(bar(C::B_PF + x), pc[x] & 1, ctl))) break;
                         ++pc[x];
@@ -288,25 +560,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const uint64_t dV = dV0 + (uint64_t)((sv * C::TILE) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
-                                mma_bf16_ts(o_col, s_col + kk * 8, dV + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                                            (first && kk == 0) ? 0u : 1u);
+                                mma_bf16_ts(tmem + C::O_COL + x * D, tmem + x * 128 + kk * 8,
+                                            dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, (first && kk == 0) ? 0u : 1u);
                         }
+                        __syncwarp();
                         started |= 1 << x;
                     }
-                    if ((use >> x) & 1) {
-                        tc_fence_after();
-                        if (leader) {
-                            const uint64_t dQ = dQ0 + (uint64_t)((x * C::TILE) >> 4);
-                            const uint64_t dK = dK0 + (uint64_t)((sk * C::TILE) >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint64_t off = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
-                                mma_bf16_ss(s_col, dQ + off, dK + off, idesc_qk, kk > 0 ? 1u : 0u);
-                            }
-                            mma_commit(bar(C::B_SF + x));
-                        }
-                    }
-                    __syncwarp();
+                    if (!early && ((use >> x) & 1)) scores(x);
                 }
                 if (!ok) break;
                 if (leader) {
@@ -329,201 +589,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (leader) mma_commit(bar(C::B_DRAIN));
         __syncwarp();
         wait_drain(bar(C::B_DRAIN), 0);
-    } else if (warp < 8) {
-        // ================================================================ softmax and epilogue of tile x
-        const int x = warp >> 2;
-        const int tid = threadIdx.x & 127;  // row of the tile = TMEM lane
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem + lane_base + x * 128, o_addr = tmem + lane_base + C::O_COL + x * D;
-        const int half_rows = p.tpt_half * p.group;
-        const float sl2 = p.scale_log2;
-        uint32_t sc = 0, oc = 0;
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-            const Unit U = decode_unit(p, P, u);
-            const int n = U.live ? (U.e1 - U.e0 + 1) >> 1 : 0;
-            int t = 0, head = 0;
-            Row row = {};
-            const bool in = tid < half_rows && (x == 0 || p.tpt > p.tpt_half);
-            if (in) {
-                row_token(p, U, tid, p.tpt_half, t, head);
-                t += x * p.tpt_half;
-                row = make_row(p, P, U, head, t);
-            }
-            const bool busy = __any_sync(kAllLanes, row.valid);
-            float mref = -CUDART_INF_F, l = 0.f;
-            bool had = false;
-            for (int i = 0; i < n; ++i, ++g) {
-                const uint32_t slot = g % kSI;
-                if (!(ok = wait_warp(bar(C::B_IF + slot), (g / kSI) & 1, ctl))) break;
-                const int use = recs[slot].use, vz0 = recs[slot].vz0, vz1 = recs[slot].vz1;
-                uint64_t w[2] = {0ull, 0ull};
-                if (((use >> x) & 1) && row.valid) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (recs[slot].blk[k] >= 0)
-                            w[k] = row_mask(row, recs[slot].blk[k], recs[slot].gbits[k], recs[slot].present[k]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
-                if (!((use >> x) & 1)) continue;
-                if (vz0 < vz1) {  // unwritten memory: no NaN may meet a zero weight
-                    const uint32_t sidx = 2 * g + 1, st = sidx % C::NST;
-                    if (!(ok = wait_warp(bar(C::B_KF + st), (sidx / C::NST) & 1, ctl))) break;
-                    uint8_t *v = smem + C::ST_OFF + st * C::TILE;
-                    for (int c = tid; c < (vz1 - vz0) * 8 * C::DC; c += 128) {
-                        const int r = vz0 + c / (8 * C::DC), q = c % (8 * C::DC);
-                        *reinterpret_cast<uint4 *>(v + (q >> 3) * kRegion + r * 128 + (q & 7) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                }
-                if (!(ok = wait_warp(bar(C::B_SF + x), sc & 1, ctl))) break;
-                ++sc;
-                if (busy) {
-                    tc_fence_after();
-                    const bool full = __all_sync(kAllLanes, (w[0] & w[1]) == ~0ull || !row.valid);
-                    float mx = -CUDART_INF_F;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        tmem_ld32(s_addr + c * 32, s);
-                        tmem_wait_ld();
-                        const uint32_t b = (uint32_t)(w[c >> 1] >> ((c & 1) * 32));
-                        if (full) {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(s[k], s[k + 1]));
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, (b >> k) & 1u ? s[k] : -CUDART_INF_F);
-                        }
-                    }
-                    mx = row.valid ? mx * sl2 : -CUDART_INF_F;
-                    const bool grow = mx > mref + kGrow || (mref == -CUDART_INF_F && mx > mref);
-                    if (__any_sync(kAllLanes, grow)) {
-                        const float ref = grow ? mx : mref;
-                        const float f = grow ? ex2(mref - ref) : 1.f;  // 0 the first time
-                        l *= f;
-                        mref = ref;
-                        if (had) {
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                float o[32];
-                                tmem_ld32(o_addr + c * 32, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= f;
-                                tmem_st32(o_addr + c * 32, o);
-                            }
-                            tmem_wait_st();
-                        }
-                    }
-                    const float nref = mref == -CUDART_INF_F ? 0.f : -mref;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float s[32];
-                            tmem_ld32(s_addr + h * 64 + c * 32, s);
-                            tmem_wait_ld();
-                            const uint32_t b = (uint32_t)(w[h] >> (c * 32));
-                            if (!full) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) s[k] = (b >> k) & 1u ? s[k] : -CUDART_INF_F;
-                            }
-                            float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float a = ex2(fmaf(s[k], sl2, nref)), e = ex2(fmaf(s[k + 1], sl2, nref));
-                                sum0 += a;
-                                sum1 += e;
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(a, e);
-                                pk[c * 16 + k / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                            }
-                            l += sum0 + sum1;
-                        }
-                        tmem_st32u(s_addr + h * 32, pk);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                }
-                had = true;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_PF + x));
-            }
-            if (!ok) break;
-            // ---- epilogue
-            if (had) {
-                if (!(ok = wait_warp(bar(C::B_OF + x), oc & 1, ctl))) break;
-                ++oc;
-                tc_fence_after();
-            }
-            const int prow = x * half_rows + tid;  // row within the unit
-            bool bad = false;
-            const float inv = row.valid && l != 0.f ? 1.f / l : 0.f;
-            if (busy || !had) {
-                __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.O) +
-                                      (((size_t)U.b * p.Hq + head) * p.m + (t < p.m ? t : 0)) * D;
-                const size_t at = (size_t)U.slot * p.rows + prow;
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
-                    if (had) {
-                        tmem_ld32(o_addr + c * 32, o);
-                        tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
-                    }
-                    float z = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);  // NaN if any is infinite or NaN
-                    bad |= z != 0.f;
-                    if (!in || (!row.valid && t >= p.m)) continue;
-                    if (U.ns > 1) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(p.part_o + at * D + c * 32 + k) =
-                                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t b4[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float a = row.valid ? o[q * 8 + 2 * k] * inv : 0.f;
-                                const float e = row.valid ? o[q * 8 + 2 * k + 1] * inv : 0.f;
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(a, e);
-                                b4[k] = *reinterpret_cast<const uint32_t *>(&two);
-                            }
-                            *reinterpret_cast<uint4 *>(orow + c * 32 + q * 8) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
-                        }
-                    }
-                }
-                if (U.ns > 1 && in) p.part_ml[at] = make_float2(row.valid ? mref : -CUDART_INF_F, row.valid ? l : 0.f);
-            } else if (U.ns > 1 && in) {  // no valid row in this warp: the merge writes their zeros
-                p.part_ml[(size_t)U.slot * p.rows + prow] = make_float2(-CUDART_INF_F, 0.f);
-            } else if (in && t < p.m) {
-                uint4 *orow = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.O) +
-                                                        (((size_t)U.b * p.Hq + head) * p.m + t) * D);
-                for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            if (had) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_OE + x));
-            }
-            unsigned again = __ballot_sync(kAllLanes, row.valid && had && (bad || not_finite(l)));
-            while (again) {
-                const int r = __ffs(again) - 1;
-                again &= again - 1;
-                const int rt = __shfl_sync(kAllLanes, t, r), rh = __shfl_sync(kAllLanes, head, r);
-                float a[D / 32];
-                __syncwarp();
-                const float2 ml = exact_row<__nv_bfloat16, D>(p, P, U, rt, rh, a);
-                store_exact_row<__nv_bfloat16, D>(p, U, rt, rh, x * half_rows + (warp & 3) * 32 + r, ml, a);
-            }
-        }
+    }
     }
     __syncwarp();
     tc_fence_before();
@@ -563,7 +629,7 @@ bool make_map(CUtensorMap *m, const void *base, int d, int rows, long long slice
 }
 
 template <int D>
-cudaError_t launch_tc_d(const PagedProblem &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tc_d(const PagedProblem &p, cudaStream_t stream) {
     using C = TcCfg<D>;
     const size_t smem = C::PLAN_OFF + plan_bytes(p.B, p.ng) + 1024;
     if (smem > 232448) return cudaErrorNotSupported;
@@ -574,20 +640,21 @@ cudaError_t launch_tc_d(const PagedProblem &p, int num_sms, cudaStream_t stream)
         !make_map(&mv, p.V, D, p.page, (long long)p.num_pages * p.Hkv, bp, 1))
         return cudaErrorInvalidValue;
     auto kern = paged_tc<D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> done[64];
+    cudaError_t e = allow_smem(kern, done, smem);
     if (e != cudaSuccess) return e;
-    const long long units = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt) + 2ll * p.target;
-    kern<<<(int)(units < num_sms ? units : num_sms), kTcThreads, smem, stream>>>(mq, mk, mv, p);
+    const long long units = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt) + (p.cut ? p.max_parts : 0);
+    kern<<<(int)(units < p.slots ? units : p.slots), kTcThreads, smem, stream>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_paged_tc(const PagedProblem &p, int num_sms, cudaStream_t stream) {
-    return p.d == 64 ? launch_tc_d<64>(p, num_sms, stream) : launch_tc_d<128>(p, num_sms, stream);
+cudaError_t launch_paged_tc(const PagedProblem &p, cudaStream_t stream) {
+    return p.d == 64 ? launch_tc_d<64>(p, stream) : launch_tc_d<128>(p, stream);
 }
 
-static_assert(TcCfg<128>::PLAN_OFF + 1024 + ((5 * kPagedMaxBatch + 2 * kPagedMaxGlobal + 4) * 4 + 16) +
+static_assert(TcCfg<128>::PLAN_OFF + 1024 + ((5 * kPagedMaxBatch + 2 * kPagedMaxGlobal + 6 + kCuts) * 4 + 16) +
                       kPagedMaxGlobal * 8 <= 232448,
               "the largest plan fits beside the tiles");
 

@@ -229,26 +229,25 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
 }
 
 template <typename T, int D>
-cudaError_t launch_tile(const PagedProblem &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tile(const PagedProblem &p, cudaStream_t stream) {
     const size_t smem = TileSmem<T, D>::PLAN + plan_bytes(p.B, p.ng);
+    static std::atomic<bool> done[64];
     auto kern = paged_tile<T, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kern, done, smem);
     if (e != cudaSuccess) return e;
-    int per_sm = 1;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kTT, smem)) != cudaSuccess) return e;
-    const long long units = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt) + 2ll * p.target;
-    const long long grid = (long long)num_sms * (per_sm < 1 ? 1 : per_sm);
+    const long long units = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt) + (p.cut ? p.max_parts : 0);
+    const long long grid = (D == 64 ? 2ll : 1ll) * p.slots;
     kern<<<(int)(units < grid ? units : grid), kTT, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_paged_tile(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream) {
+cudaError_t launch_paged_tile(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream) {
     if (dtype == SA_FP32)
-        return p.d == 64 ? launch_tile<float, 64>(p, num_sms, stream) : launch_tile<float, 128>(p, num_sms, stream);
-    return p.d == 64 ? launch_tile<__nv_bfloat16, 64>(p, num_sms, stream)
-                     : launch_tile<__nv_bfloat16, 128>(p, num_sms, stream);
+        return p.d == 64 ? launch_tile<float, 64>(p, stream) : launch_tile<float, 128>(p, stream);
+    return p.d == 64 ? launch_tile<__nv_bfloat16, 64>(p, stream)
+                     : launch_tile<__nv_bfloat16, 128>(p, stream);
 }
 
 }  // namespace sa

@@ -11,8 +11,6 @@ are always changed in place. Nothing here waits for the device: what a kernel
 finds wrong in a table or a list is reported by ``get_last_device_status``.
 """
 
-import ctypes
-
 import torch
 
 from . import _lib
@@ -24,13 +22,13 @@ _INT = torch.int32
 def _call(name, device, stream, *args):
     """Run a C entry point on `device` and `stream` (default: its current one)."""
     fn = getattr(_lib.lib(), name)
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream.cuda_stream)
+    index = device.index
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, handle)
     if st != _lib.SA_OK:
         raise _lib.SparseAttnError(st, name)
 
@@ -56,13 +54,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _ints(name, t, device, shape):
-    """`t` must be a contiguous int32 tensor on `device` of `shape` (None: any size there)."""
-    if t is None:
-        return
-    if t.dtype is not _INT or t.device != device or not t.is_contiguous() or t.dim() != len(shape) \
-            or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device} (None: any size)")
+def _ints(name, t, device, *shape):
+    """`t` must be a contiguous int32 tensor on `device` of `shape` (-1: any size there)."""
+    if t.dtype is _INT and t.device == device and t.is_contiguous():
+        got = t.shape
+        if got == shape or (len(got) == len(shape) and all(n < 0 or n == m for n, m in zip(shape, got))):
+            return
+    raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device} (-1: any size)")
 
 
 def _pools(K_pages, V_pages, dims):
@@ -99,16 +97,19 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     _new_rows("Q", Q, K_pages, None)
     B, Hq, m, _ = Q.shape
     dev = Q.device
-    _ints("block_table", block_table, dev, (B, None))
-    _ints("seq_lens", seq_lens, dev, (B,))
-    _ints("q_lens", q_lens, dev, (B,))
-    _ints("dilation", dilation, dev, (Hq,))
-    _ints("global_idx", global_idx, dev, (None,))
+    _ints("block_table", block_table, dev, B, -1)
+    _ints("seq_lens", seq_lens, dev, B)
+    if q_lens is not None:
+        _ints("q_lens", q_lens, dev, B)
+    if dilation is not None:
+        _ints("dilation", dilation, dev, Hq)
+    if global_idx is not None:
+        _ints("global_idx", global_idx, dev, -1)
     n_global = 0 if global_idx is None else global_idx.numel()
     max_pages = block_table.shape[1]
     dt = _DTYPE[Q.dtype]
     if workspace is None:
-        workspace = _scratch(paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, Q.dtype, dev), dev, stream)
+        workspace = _scratch(_workspace_bytes(dev, B, Hq, Hkv, m, d, page, max_pages, dt), dev, stream)
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on Q's device")
     if out is None:
@@ -122,13 +123,20 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     return out
 
 
-def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None):
-    """Scratch bytes of a longformer_attn_paged_fwd call of these sizes."""
+def _workspace_bytes(device, *sizes):
     fn = _lib.lib().sa_longformer_paged_workspace_bytes
-    if device is not None and device.index is not None and torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return fn(B, Hq, Hkv, m, d, page, max_pages, _DTYPE[dtype])
-    return fn(B, Hq, Hkv, m, d, page, max_pages, _DTYPE[dtype])
+    if torch._C._cuda_getDevice() == device.index:
+        return fn(*sizes)
+    with torch.cuda.device(device):
+        return fn(*sizes)
+
+
+def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None):
+    """Scratch bytes of a longformer_attn_paged_fwd call of these sizes on `device` (default: the current one)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    return _workspace_bytes(dev, B, Hq, Hkv, m, d, page, max_pages, _DTYPE[dtype])
 
 
 def cache_append(K_new, V_new, K_pages, V_pages, block_table, seq_lens, q_lens=None, stream=None):
@@ -141,9 +149,10 @@ def cache_append(K_new, V_new, K_pages, V_pages, block_table, seq_lens, q_lens=N
     if V_new.shape != K_new.shape:
         raise ValueError("K_new and V_new must share shape")
     dev = K_pages.device
-    _ints("block_table", block_table, dev, (B, None))
-    _ints("seq_lens", seq_lens, dev, (B,))
-    _ints("q_lens", q_lens, dev, (B,))
+    _ints("block_table", block_table, dev, B, -1)
+    _ints("seq_lens", seq_lens, dev, B)
+    if q_lens is not None:
+        _ints("q_lens", q_lens, dev, B)
     _call("sa_cache_append", dev, stream, K_new.data_ptr(), V_new.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
           B, Hkv, m, d, page, num_pages, block_table.shape[1], block_table.data_ptr(), seq_lens.data_ptr(),
           _ptr(q_lens), _DTYPE[K_pages.dtype])
@@ -173,8 +182,8 @@ def _book(block_table, ref_count, num_pages=None, device=None):
     dev = block_table.device
     if not block_table.is_cuda or (device is not None and dev != device):
         raise ValueError("block_table must be a CUDA tensor on the pools' device")
-    _ints("block_table", block_table, dev, (None, None))
-    _ints("ref_count", ref_count, dev, (num_pages,))
+    _ints("block_table", block_table, dev, -1, -1)
+    _ints("ref_count", ref_count, dev, -1 if num_pages is None else num_pages)
     return dev, block_table.shape[0], block_table.shape[1], ref_count.numel()
 
 
@@ -187,8 +196,8 @@ def cache_copy_pages(K_pages, V_pages, src, dst, stream=None):
     """Copy page src[i] to page dst[i] in every layer; returns (K_pages, V_pages). No page twice in dst, or in both."""
     layers, num_pages, page_bytes, _ = _pool_args(K_pages, V_pages)
     dev = K_pages.device
-    _ints("src", src, dev, (None,))
-    _ints("dst", dst, dev, (src.numel(),))
+    _ints("src", src, dev, -1)
+    _ints("dst", dst, dev, src.numel())
     _call("sa_cache_copy_pages", dev, stream, K_pages.data_ptr(), V_pages.data_ptr(), layers, num_pages, page_bytes,
           src.data_ptr(), dst.data_ptr(), src.numel())
     return K_pages, V_pages
@@ -201,9 +210,9 @@ def cache_fork(K_pages, V_pages, block_table, seq_lens, ref_count, src, dst, out
     """
     layers, num_pages, page_bytes, page = _pool_args(K_pages, V_pages)
     dev, B, max_pages, _ = _book(block_table, ref_count, num_pages, K_pages.device)
-    _ints("seq_lens", seq_lens, dev, (B,))
-    _ints("src", src, dev, (None,))
-    _ints("dst", dst, dev, (src.numel(),))
+    _ints("seq_lens", seq_lens, dev, B)
+    _ints("src", src, dev, -1)
+    _ints("dst", dst, dev, src.numel())
     table, lens, refs = _outputs(out, (block_table, seq_lens, ref_count), stream)
     n_bytes = cache_workspace_bytes(num_pages, B)
     ws = _scratch(n_bytes, dev, stream)
@@ -216,8 +225,8 @@ def cache_fork(K_pages, V_pages, block_table, seq_lens, ref_count, src, dst, out
 def cache_free(block_table, seq_lens, ref_count, rows, out=None, stream=None):
     """The rows give up their pages; returns (block_table, seq_lens, ref_count)."""
     dev, B, max_pages, num_pages = _book(block_table, ref_count)
-    _ints("seq_lens", seq_lens, dev, (B,))
-    _ints("rows", rows, dev, (None,))
+    _ints("seq_lens", seq_lens, dev, B)
+    _ints("rows", rows, dev, -1)
     table, lens, refs = _outputs(out, (block_table, seq_lens, ref_count), stream)
     _call("sa_cache_free", dev, stream, num_pages, B, max_pages, rows.data_ptr(), rows.numel(), block_table.data_ptr(),
           seq_lens.data_ptr(), ref_count.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
@@ -227,8 +236,9 @@ def cache_free(block_table, seq_lens, ref_count, rows, out=None, stream=None):
 def cache_trim(block_table, seq_lens, ref_count, page, reach, global_idx=None, out=None, stream=None):
     """Rows give up the pages that the window (reach tokens back) has left; returns (block_table, ref_count)."""
     dev, B, max_pages, num_pages = _book(block_table, ref_count)
-    _ints("seq_lens", seq_lens, dev, (B,))
-    _ints("global_idx", global_idx, dev, (None,))
+    _ints("seq_lens", seq_lens, dev, B)
+    if global_idx is not None:
+        _ints("global_idx", global_idx, dev, -1)
     n_global = 0 if global_idx is None else global_idx.numel()
     table, refs = _outputs(out, (block_table, ref_count), stream)
     _call("sa_cache_trim", dev, stream, num_pages, page, B, max_pages, reach,
@@ -240,8 +250,8 @@ def cache_trim(block_table, seq_lens, ref_count, page, reach, global_idx=None, o
 def cache_reserve(block_table, seq_lens, q_lens, ref_count, page, out=None, stream=None):
     """Pages for the new tokens [seq_lens - q_lens, seq_lens) of every row; returns (block_table, ref_count)."""
     dev, B, max_pages, num_pages = _book(block_table, ref_count)
-    _ints("seq_lens", seq_lens, dev, (B,))
-    _ints("q_lens", q_lens, dev, (B,))
+    _ints("seq_lens", seq_lens, dev, B)
+    _ints("q_lens", q_lens, dev, B)
     table, refs = _outputs(out, (block_table, ref_count), stream)
     n_bytes = cache_workspace_bytes(num_pages, B)
     ws = _scratch(n_bytes, dev, stream)
