@@ -13,6 +13,7 @@ namespace sa {
 constexpr int kPagedMaxBatch = 1024;   // sequences per call: every CTA plans over them in shared memory
 constexpr int kPagedMaxGlobal = 512;   // global positions per call: kept in shared memory
 constexpr int kPagedMaxGroup = 64;     // query heads per key head: one token's group fits any row tile
+constexpr int kPagedMaxHeads = 256;    // key heads per call: their strides are kept in shared memory
 constexpr long long kPagedMaxLen = 1ll << 30;  // tokens per sequence (positions are 32-bit)
 
 // One attention call over a paged cache, as validated by the host API.
@@ -36,15 +37,14 @@ struct PagedProblem {
     int tpt;         // tokens per unit
     int tpt_half;    // tokens per half of a unit (tpt: units of one half)
     int rows;        // rows per unit: tpt * group
-    int cut;         // whether sweeps may be split (then paged_merge is launched)
-    int slots;       // units that run at a time
-    int max_parts;   // partial results that the workspace holds
-    int min_split;   // fewest 64-key blocks of a split
-    int cost_plain, cost_split;  // what a whole and a split unit cost beside their blocks, in blocks
+    int cut;         // whether tiles may be split (then paged_merge is launched)
+    int slots;       // CTAs that share the work
+    int min_piece;   // fewest 64-key blocks worth a CTA of their own
+    int cost;        // what a tile costs beside its blocks, in blocks
     float scale_log2;
     unsigned long long wait_ns;
-    float *part_o;   // [slots][rows][d] partial sums of split sweeps
-    float2 *part_ml; // [slots][rows] (running maximum, sum)
+    float *part_o;   // [2 slots][rows][d] partial sums of split tiles
+    float2 *part_ml; // [2 slots][rows] (running maximum, sum)
 };
 
 // Which kernel serves a call: few rows per key head, many rows in bf16 on the
@@ -55,7 +55,7 @@ enum PagedKernel { kPagedRows = 0, kPagedTc = 1, kPagedTile = 2 };
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms);
 // CTAs of the streaming kernel that fit an SM, by the rows of a unit.
 inline int paged_rows_ctas(int rows) { return rows <= 1 ? 3 : rows <= 4 ? 2 : 1; }
-// Scratch of one call: partial results of split sweeps (0: nothing is split).
+// Scratch of one call: partial results of split tiles (0: nothing is split).
 size_t paged_workspace_bytes(const PagedProblem &p);
 cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream);
 cudaError_t launch_paged_tile(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream);

@@ -10,7 +10,7 @@ namespace sa {
 
 // At most this many query rows of a key head go to the kernel that streams the
 // cache with the ordinary units.
-constexpr int kNoCutBlocks = 16;
+constexpr int kNoCutBlocks = 17;
 static int rows_limit(sa_dtype dtype) { return dtype == SA_FP32 ? 8 : 4; }
 
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms) {
@@ -19,15 +19,14 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)p.d);
     const long long rows = (long long)p.m * p.group;
     PagedKernel kind;
+    int per_sm = 1;
     if (rows <= rows_limit(dtype)) {
         kind = kPagedRows;
         p.tpt = p.tpt_half = p.m;
         p.rows = (int)rows;
-        p.slots = num_sms * paged_rows_ctas(p.rows);
-        p.max_parts = 16 * num_sms;
-        p.min_split = 4;
-        p.cost_plain = 2;
-        p.cost_split = 3;
+        per_sm = paged_rows_ctas(p.rows);
+        p.min_piece = 4;
+        p.cost = 1;
     } else if (dtype == SA_BF16 && !force_simt) {
         kind = kPagedTc;
         const int most = 128 / p.group;
@@ -35,30 +34,29 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
         const int halves = p.m > p.tpt_half ? 2 : 1;
         p.tpt = halves * p.tpt_half;
         p.rows = halves * p.tpt_half * p.group;
-        p.slots = num_sms;
-        p.max_parts = 8 * num_sms;
-        p.min_split = 8;
-        p.cost_plain = 3;
-        p.cost_split = 6;
+        p.min_piece = 8;
+        p.cost = 3;
     } else {
         kind = kPagedTile;
         const int most = 64 / p.group;
         p.tpt = p.tpt_half = p.m < most ? p.m : most;
         p.rows = p.tpt * p.group;
-        p.slots = 2 * num_sms;
-        p.max_parts = 16 * num_sms;
-        p.min_split = 2;
-        p.cost_plain = 1;
-        p.cost_split = 2;
+        per_sm = p.d == 64 ? 4 : 2;
+        p.min_piece = 2;
+        p.cost = 1;
     }
-    // No sweep is longer than its table row; short ones are not cut, which
+    // No tile walks more than its table row. Short walks are not split, which
     // saves the launch that joins the pieces.
-    p.cut = ((long long)p.max_pages << p.log_page) > 64ll * kNoCutBlocks;
+    const long long tiles = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt);
+    const long long longest = ((((long long)p.max_pages << p.log_page) + 63) >> 6) + p.cost;
+    p.cut = longest > kNoCutBlocks;
+    const long long most = p.cut ? tiles * (longest / p.min_piece + 1) : tiles;
+    p.slots = (int)(most < (long long)num_sms * per_sm ? most : (long long)num_sms * per_sm);
     return kind;
 }
 
 size_t paged_workspace_bytes(const PagedProblem &p) {
-    return p.cut ? (size_t)p.max_parts * p.rows * (p.d + 2) * sizeof(float) : 0;
+    return p.cut ? 2 * (size_t)p.slots * p.rows * (p.d + 2) * sizeof(float) : 0;
 }
 
 }  // namespace sa
@@ -127,7 +125,7 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
     if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return SA_ERR_INVALID_ARG;
     sa_status s = sizes_ok(B, Hkv, m, d, page, num_pages, max_pages);
     if (s != SA_OK) return s;
-    if (Hq / Hkv > sa::kPagedMaxGroup || n_global > sa::kPagedMaxGlobal || (long long)B * Hq > (1ll << 30))
+    if (Hq / Hkv > sa::kPagedMaxGroup || Hkv > sa::kPagedMaxHeads || n_global > sa::kPagedMaxGlobal || (long long)B * Hq > (1ll << 30))
         return SA_ERR_UNSUPPORTED;
     sa::PagedProblem p = {};
     int sms = 0;
@@ -147,7 +145,7 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
     if (need) {
         if (ws_ok(workspace, workspace_bytes, need) != SA_OK) return SA_ERR_INVALID_ARG;
         p.part_o = static_cast<float *>(workspace);
-        p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)p.max_parts * p.rows * p.d);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + 2 * (size_t)p.slots * p.rows * p.d);
     }
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = kind == sa::kPagedRows ? sa::launch_paged_rows(p, dtype, cs)
@@ -160,7 +158,7 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
 size_t sa_longformer_paged_workspace_bytes(int B, int Hq, int Hkv, int m, int d, int page, int max_pages,
                                            sa_dtype dtype) {
     if ((dtype != SA_BF16 && dtype != SA_FP32) || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
-        Hq / Hkv > sa::kPagedMaxGroup || sizes_ok(B, Hkv, m, d, page, 1, max_pages) != SA_OK)
+        Hq / Hkv > sa::kPagedMaxGroup || Hkv > sa::kPagedMaxHeads || sizes_ok(B, Hkv, m, d, page, 1, max_pages) != SA_OK)
         return 0;
     unsigned *status = nullptr;
     int sms = 0;

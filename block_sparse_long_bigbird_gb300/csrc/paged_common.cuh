@@ -3,12 +3,16 @@
 // of a row against a block, and an exact path for rows that ordinary
 // arithmetic spoils.
 //
-// A unit is one tile of query rows (a few tokens times the query heads of one
-// key head) against one stretch of the 64-key blocks that any of its rows may
-// see. The lengths live on the device, so no host code can cut the sweeps:
-// every CTA reads them (at most kPagedMaxBatch) and computes the same plan in
-// shared memory. That costs about a microsecond, where a planning kernel of
-// its own would cost a launch.
+// A tile is a few tokens times the query heads of one key head; it walks the
+// 64-key blocks that any of its rows may see. All tiles' blocks (and a constant
+// for what a tile costs besides) are laid end to end, and CTA c of n takes the
+// stretch [T c / n, T (c + 1) / n): every CTA gets the same amount of work
+// whatever the lengths of the sequences, and a tile is split only where a
+// boundary falls into it, so there are fewer than 2 n partial results. The part
+// of a tile that one CTA takes is a unit. The lengths live on the device, so no
+// host code can do this: every CTA reads them (at most kPagedMaxBatch) and
+// computes the same plan in shared memory, which costs one or two microseconds
+// where a planning kernel would cost a launch.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -49,42 +53,36 @@ __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.402
 
 // The plan in shared memory. Arrays over sequences, then the global list.
 struct Plan {
+    long long *vbase;  // [B + 1] where a sequence's tiles begin on the common axis
+    uint64_t *gbit;    // [ngb] global keys of those blocks
     int *q, *s;        // [B] new tokens and tokens in the cache (q = 0 for a refused sequence)
-    int *ns;           // [B] splits of each of the sequence's sweeps
-    int *ubase;        // [B + 1] first unit
-    int *sbase;        // [B + 1] first partial-result slot
     int *gpos;         // [ng] global positions
     int *gblk;         // [ngb] 64-key blocks that hold one, ascending
-    uint64_t *gbit;    // [ngb] which of their keys
-    int *misc;         // [0] ngb, [1] longest stride of a dilated head, [2] longest sweep, [4 + 2 k] costs of kCuts
-    int ngb, max_stride;
+    int *hstride;      // [Hkv] longest stride of a key head's query heads (with dilation)
+    int *misc;         // [0] ngb, [1] tiles
+    int ngb;
+    int ctas;          // CTAs that share the axis
+    long long total;   // its length
 };
 
-// Splits tried for the longest sweep.
-constexpr int kCuts = 16;
-__device__ __forceinline__ int cut_of(int k) {
-    return k < 6 ? k + 1 : k < 9 ? 2 * k - 4 : k < 10 ? 16 : k < 11 ? 24 : k < 12 ? 32 : k < 13 ? 48 : k < 14 ? 64 : k < 15 ? 96 : 128;
+__host__ __device__ inline size_t plan_bytes(int B, int ng, int Hkv) {
+    const size_t ints = 2 * (size_t)B + 2 * (size_t)ng + Hkv + 2;
+    return 8 * (size_t)(B + 1 + ng) + ((ints * 4 + 15) & ~(size_t)15);
 }
 
-__host__ __device__ inline size_t plan_bytes(int B, int ng) {
-    const size_t ints = 5 * (size_t)B + 2 + 2 * (size_t)ng + 4 + kCuts;
-    return ((ints * 4 + 15) & ~(size_t)15) + (size_t)ng * 8;
-}
-
-__device__ __forceinline__ Plan plan_at(void *smem, int B, int ng) {
+__device__ __forceinline__ Plan plan_at(void *smem, int B, int ng, int Hkv) {
     Plan P;
-    P.gbit = reinterpret_cast<uint64_t *>(smem);
-    int *w = reinterpret_cast<int *>(P.gbit + ng);
-    P.q = w;
-    P.s = w + B;
-    P.ns = w + 2 * B;
-    P.ubase = w + 3 * B;
-    P.sbase = w + 4 * B + 1;
-    P.gpos = w + 5 * B + 2;
+    P.vbase = reinterpret_cast<long long *>(smem);
+    P.gbit = reinterpret_cast<uint64_t *>(P.vbase + B + 1);
+    P.q = reinterpret_cast<int *>(P.gbit + ng);
+    P.s = P.q + B;
+    P.gpos = P.s + B;
     P.gblk = P.gpos + ng;
-    P.misc = P.gblk + ng;
+    P.hstride = P.gblk + ng;
+    P.misc = P.hstride + Hkv;
     P.ngb = 0;
-    P.max_stride = 1;
+    P.ctas = 1;
+    P.total = 0;
     return P;
 }
 
@@ -115,13 +113,13 @@ __device__ __forceinline__ int lower_bound(const int *a, int n, int v) {
     return lo;
 }
 
-// Upper estimate of the 64-key blocks that one tile of a sequence walks.
-__device__ __forceinline__ int estimate_blocks(const PagedProblem &p, const Plan &P, int q, int s) {
-    if (q == 0) return 0;
+// Length on the common axis of one tile of a sequence for a key head of that
+// stride: an upper estimate of the blocks it walks, and its fixed cost.
+__device__ __forceinline__ int tile_length(const PagedProblem &p, const Plan &P, int q, int s, int stride) {
     const int all = (s + 63) >> 6;
-    const long long span = (long long)head_reach(p, P.max_stride) + min(q, p.tpt);
+    const long long span = (long long)head_reach(p, stride) + min(q, p.tpt);
     const long long band = (span >> 6) + 2 + P.ngb;
-    return band < all ? (int)band : all;
+    return (band < all ? (int)band : all) + p.cost;
 }
 
 // Computed by the whole CTA. Ends with a barrier.
@@ -146,13 +144,13 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
         }
         P.gpos[i] = v;
     }
-    if (tid == 0) {
-        P.misc[1] = 1;
-        P.misc[2] = 0;
-    }
-    __syncthreads();
     if (p.dilation)
-        for (int h = tid; h < p.Hq; h += nthr) atomicMax(&P.misc[1], head_stride(p, h));
+        for (int h = tid; h < p.Hkv; h += nthr) {
+            int st = 1;
+            for (int g = 0; g < p.group; ++g) st = max(st, head_stride(p, h * p.group + g));
+            P.hstride[h] = st;
+        }
+    __syncthreads();
     if (tid < 32) {
         int n = 0, kept = 0, last = -1;  // blocks and entries so far, the last entry's block
         for (int i0 = 0; i0 < p.ng; i0 += 32) {
@@ -182,99 +180,125 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     }
     __syncthreads();
     P.ngb = P.misc[0];
-    P.max_stride = P.misc[1];
-    // The longest sweep, then what each way of cutting it (and the others into
-    // pieces as long) would cost: rounds of `slots` units of mean length, and a
-    // last round as long as the longest piece. A split unit costs more, as it
-    // writes partial results that are read again.
-    int len = 0x3fffffff;
-    if (p.cut) {
-        const int warp = tid >> 5, nwarps = nthr >> 5;
-        if (tid < p.B) {
-            int e = 0;
-            for (int b = tid; b < p.B; b += nthr) e = max(e, estimate_blocks(p, P, P.q[b], P.s[b]));
-            atomicMax(&P.misc[2], e);
+    const int all_tiles = (p.m + p.tpt - 1) / p.tpt;
+    for (int b = tid; b < p.B; b += nthr) {  // each sequence's length on the axis
+        const int q = P.q[b], tiles = (q + p.tpt - 1) / p.tpt;
+        long long n = (long long)p.Hkv * (all_tiles - tiles);  // tiles without tokens: one each
+        if (!p.dilation) {
+            n += (long long)p.Hkv * tiles * tile_length(p, P, q, P.s[b], 1);
+        } else {
+            for (int h = 0; h < p.Hkv; ++h) n += (long long)tiles * tile_length(p, P, q, P.s[b], P.hstride[h]);
         }
-        __syncthreads();
-        const int longest = P.misc[2];
-        for (int k = warp; k < kCuts; k += nwarps) {
-            const int piece = (longest + cut_of(k) - 1) / cut_of(k);
-            int units = 0, parts = 0;
-            long long total = 0;
-            for (int b = lane; b < p.B; b += 32) {
-                const int n = (P.q[b] + p.tpt - 1) / p.tpt * p.Hkv;
-                const int e = estimate_blocks(p, P, P.q[b], P.s[b]);
-                const int ns = piece > 0 && e > piece ? (e + piece - 1) / piece : 1;
-                units += n * ns;
-                parts += ns > 1 ? n * ns : 0;
-                total += (long long)n * e;
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                units += __shfl_xor_sync(kAllLanes, units, o);
-                parts += __shfl_xor_sync(kAllLanes, parts, o);
-                total += __shfl_xor_sync(kAllLanes, total, o);
-            }
-            if (lane == 0) {
-                // in 1/16 blocks; a cut that is too short or needs too much scratch is out
-                const long long own = 16 * total + 16ll * (units - parts) * p.cost_plain + 16ll * parts * p.cost_split;
-                const int u = max(units, 1);
-                const long long mean = own / u;
-                long long cost = (long long)((u + p.slots - 1) / p.slots) * mean + 16ll * piece - 16 * total / u;
-                if (k > 0 && (piece < p.min_split || parts > p.max_parts)) cost = 0x7fffffff;
-                P.misc[4 + k] = (int)(cost > 0x7fffffff ? 0x7fffffff : cost);
-            }
-        }
-        __syncthreads();
-        int best = 0;
-        for (int k = 1; k < kCuts; ++k)
-            if (P.misc[4 + k] < P.misc[4 + best]) best = k;
-        len = max(1, (longest + cut_of(best) - 1) / cut_of(best));
-    }
-    if (tid < 32) {
-        const int all_tiles = (p.m + p.tpt - 1) / p.tpt;
-        int ubase = 0, sbase = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int b = b0 + lane;
-            int nu = 0, nslot = 0, ns = 1;
-            if (b < p.B) {
-                const int tiles = (P.q[b] + p.tpt - 1) / p.tpt;
-                const int est = p.cut ? estimate_blocks(p, P, P.q[b], P.s[b]) : 0;
-                ns = est > len ? (est + len - 1) / len : 1;
-                nu = p.Hkv * (tiles * ns + all_tiles - tiles);
-                nslot = ns > 1 ? p.Hkv * tiles * ns : 0;
-                P.ns[b] = ns;
-            }
-            int iu = nu, is = nslot;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(kAllLanes, iu, o), c = __shfl_up_sync(kAllLanes, is, o);
-                if (lane >= o) {
-                    iu += a;
-                    is += c;
-                }
-            }
-            if (b < p.B) {
-                P.ubase[b] = ubase + iu - nu;
-                P.sbase[b] = sbase + is - nslot;
-            }
-            ubase += __shfl_sync(kAllLanes, iu, 31);
-            sbase += __shfl_sync(kAllLanes, is, 31);
-        }
-        if (lane == 0) {
-            P.ubase[p.B] = ubase;
-            P.sbase[p.B] = sbase;
-        }
+        P.vbase[b + 1] = n;
     }
     __syncthreads();
+    if (tid < 32) {
+        long long base = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            long long v = b < p.B ? P.vbase[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long a = __shfl_up_sync(kAllLanes, v, o);
+                if (lane >= o) v += a;
+            }
+            if (b < p.B) P.vbase[b + 1] = base + v;
+            base += __shfl_sync(kAllLanes, v, 31);
+        }
+        if (lane == 0) P.vbase[0] = 0;
+    }
+    __syncthreads();
+    P.total = P.vbase[p.B];
+    // as many CTAs as there are tiles, or pieces worth having
+    const long long tiles = (long long)p.B * p.Hkv * all_tiles;
+    const long long pieces = p.cut ? P.total / p.min_piece : 0;
+    const long long want = pieces > tiles ? pieces : tiles;
+    P.ctas = want < p.slots ? (int)want : p.slots;
 }
 
-// One unit: `live` false means rows that are only zeroed (past q of their sequence).
-struct Unit {
-    int b, hk, t0, split, ns, slot;  // slot: partial-result slot (ns > 1)
+// Where CTA c's stretch begins, and the CTA whose stretch holds x.
+__device__ __forceinline__ long long cta_begin(const Plan &P, int c) { return P.total * c / P.ctas; }
+__device__ __forceinline__ int cta_of(const Plan &P, long long x) { return (int)(((x + 1) * P.ctas - 1) / P.total); }
+
+// A tile on the axis, and how to get to the next one. `live` false: its rows are
+// only zeroed (past q of their sequence).
+struct Tile {
+    int b, hk, t0;
     int q, s;
+    int tiles, i, len;  // the sequence's tiles, this one's number (of the padding, once past them), length
     bool live;
-    int lo_blk, n_glob, e0, e1;      // entries [e0, e1): first the global blocks before lo_blk, then lo_blk ...
+    long long begin, end;
+
+    __device__ __forceinline__ void place(const PagedProblem &p) {
+        live = hk < p.Hkv;
+        end = begin + (live ? len : 1);
+        // the longest sweeps first
+        t0 = (live ? tiles - 1 - i : tiles + i % ((p.m + p.tpt - 1) / p.tpt - tiles)) * p.tpt;
+    }
+    __device__ __forceinline__ int head(const PagedProblem &p) const {  // key head
+        return live ? hk : i / ((p.m + p.tpt - 1) / p.tpt - tiles);
+    }
+    __device__ __forceinline__ void start(const PagedProblem &p, const Plan &P, int seq) {
+        b = seq;
+        q = P.q[b];
+        s = P.s[b];
+        begin = P.vbase[b];
+        tiles = (q + p.tpt - 1) / p.tpt;
+        i = 0;
+        hk = tiles > 0 ? 0 : p.Hkv;
+        if (tiles > 0) len = tile_length(p, P, q, s, p.dilation ? P.hstride[0] : 1);
+    }
+    __device__ __forceinline__ void advance(const PagedProblem &p, const Plan &P) {
+        begin = end;
+        if (begin == P.vbase[b + 1]) {
+            if (b + 1 < p.B) start(p, P, b + 1);
+        } else if (++i == tiles && live) {
+            i = 0;
+            if (++hk < p.Hkv && p.dilation) len = tile_length(p, P, q, s, P.hstride[hk]);
+        }
+        place(p);
+    }
+};
+
+__device__ __forceinline__ Tile find_tile(const PagedProblem &p, const Plan &P, long long x) {
+    Tile T;
+    int lo = 0, hi = p.B;  // last b with vbase[b] <= x; every sequence has a length
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (P.vbase[mid] <= x) lo = mid; else hi = mid;
+    }
+    T.len = 0;
+    T.start(p, P, lo);
+    long long off = x - T.begin;
+    if (T.tiles > 0) {
+        if (!p.dilation) {
+            const long long per = (long long)T.len * T.tiles;
+            T.hk = (int)min(off / per, (long long)p.Hkv);
+            T.begin += T.hk * per;
+            off -= T.hk * per;
+        } else {
+            for (; T.hk < p.Hkv; ++T.hk) {
+                T.len = tile_length(p, P, T.q, T.s, P.hstride[T.hk]);
+                const long long per = (long long)T.len * T.tiles;
+                if (off < per) break;
+                T.begin += per;
+                off -= per;
+            }
+        }
+    }
+    T.i = (int)(T.hk < p.Hkv ? off / T.len : off);
+    T.begin += T.hk < p.Hkv ? (long long)T.i * T.len : off;
+    T.place(p);
+    return T;
+}
+
+// One CTA's part of a tile.
+struct Unit {
+    int b, hk, t0;
+    int q, s;
+    bool live, split;
+    int slot;                    // partial-result slot (split)
+    int lo_blk, n_glob, e0, e1;  // entries [e0, e1): first the global blocks before lo_blk, then lo_blk ...
 };
 
 // Is a position among the global ones?
@@ -284,54 +308,55 @@ __device__ __forceinline__ bool is_global(const Plan &P, const PagedProblem &p, 
     return i < p.ng && P.gpos[i] == pos;
 }
 
-__device__ __forceinline__ Unit decode_unit(const PagedProblem &p, const Plan &P, int u) {
-    Unit U;
-    int lo = 0, hi = p.B;  // last b with ubase[b] <= u
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (P.ubase[mid] <= u) lo = mid; else hi = mid;
+// The units of a CTA, in order: next() fills the following one and returns
+// whether there is one.
+struct Units {
+    Tile T;
+    long long v, end;
+    int c;
+    __device__ __forceinline__ Units(const PagedProblem &p, const Plan &P, int cta) : v(0), end(0), c(cta) {
+        if (cta >= P.ctas) return;
+        v = cta_begin(P, cta);
+        end = cta_begin(P, cta + 1);
+        T = find_tile(p, P, v);
+        if (!p.cut && T.begin < v) {  // whole tiles only: those that begin in the stretch
+            v = T.end;
+            if (v < end) T.advance(p, P);
+        }
     }
-    U.b = lo;
-    U.q = P.q[lo];
-    U.s = P.s[lo];
-    U.ns = P.ns[lo];
-    int r = u - P.ubase[lo];
-    const int tiles = (U.q + p.tpt - 1) / p.tpt;
-    const int n_live = p.Hkv * tiles * U.ns;
-    U.slot = 0;
-    U.lo_blk = U.n_glob = U.e0 = U.e1 = 0;
-    if (r >= n_live) {
-        r -= n_live;
-        const int pad = (p.m + p.tpt - 1) / p.tpt - tiles;
-        U.live = false;
-        U.split = 0;
-        U.ns = 1;
-        U.hk = r / pad;
-        U.t0 = (tiles + r % pad) * p.tpt;
-        return U;
+    __device__ __forceinline__ bool next(const PagedProblem &p, const Plan &P, Unit &U) {
+        if (v >= end) return false;
+        if (v == T.end) T.advance(p, P);
+        U.b = T.b;
+        U.hk = T.head(p);
+        U.t0 = T.t0;
+        U.q = T.q;
+        U.s = T.s;
+        U.live = T.live;
+        U.lo_blk = U.n_glob = U.e0 = U.e1 = 0;
+        const long long begin = v, stop = p.cut && T.end > end ? end : T.end;
+        U.split = begin > T.begin || stop < T.end;
+        U.slot = 2 * c + (begin == T.begin);
+        v = stop;
+        if (!T.live) return true;
+        const int p0 = U.s - U.q + U.t0, p1 = U.s - U.q + min(U.t0 + p.tpt, U.q) - 1;
+        int first = max(0, p0 - head_reach(p, p.dilation ? P.hstride[U.hk] : 1));
+        if (p.ng) {  // a global row sees everything before it
+            const int i = lower_bound(P.gpos, p.ng, p0);
+            if (i < p.ng && P.gpos[i] <= p1) first = 0;
+        }
+        U.lo_blk = first >> 6;
+        U.n_glob = p.ng ? lower_bound(P.gblk, P.ngb, U.lo_blk) : 0;
+        const int n = U.n_glob + (p1 >> 6) - U.lo_blk + 1;
+        U.e1 = n;
+        if (U.split) {
+            const long long len = T.end - T.begin;
+            U.e0 = (int)(n * (begin - T.begin) / len);
+            U.e1 = (int)(n * (stop - T.begin) / len);
+        }
+        return true;
     }
-    U.live = true;
-    U.slot = P.sbase[lo] + r;
-    U.split = r % U.ns;
-    r /= U.ns;
-    U.hk = r / tiles;
-    U.t0 = (tiles - 1 - r % tiles) * p.tpt;  // the longest sweeps first
-    const int p0 = U.s - U.q + U.t0, p1 = U.s - U.q + min(U.t0 + p.tpt, U.q) - 1;
-    int stride = 1;
-    if (p.dilation)
-        for (int g = 0; g < p.group; ++g) stride = max(stride, head_stride(p, U.hk * p.group + g));
-    int first = max(0, p0 - head_reach(p, stride));
-    if (p.ng) {  // a global row sees everything before it
-        const int i = lower_bound(P.gpos, p.ng, p0);
-        if (i < p.ng && P.gpos[i] <= p1) first = 0;
-    }
-    U.lo_blk = first >> 6;
-    U.n_glob = p.ng ? lower_bound(P.gblk, P.ngb, U.lo_blk) : 0;
-    const int n = U.n_glob + (p1 >> 6) - U.lo_blk + 1;
-    U.e0 = (int)((long long)n * U.split / U.ns);
-    U.e1 = (int)((long long)n * (U.split + 1) / U.ns);
-    return U;
-}
+};
 
 __device__ __forceinline__ int entry_block(const Plan &P, const Unit &U, int e) {
     return e < U.n_glob ? P.gblk[e] : U.lo_blk + e - U.n_glob;
@@ -475,7 +500,7 @@ __device__ __forceinline__ void store_exact_row(const PagedProblem &p, const Uni
                                                 float2 ml, const float (&acc)[D / 32]) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
-    if (U.ns > 1) {
+    if (U.split) {
         const size_t at = (size_t)U.slot * p.rows + row;
 #pragma unroll
         for (int i = 0; i < E; ++i) p.part_o[at * D + lane * E + i] = acc[i];

@@ -36,15 +36,16 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) 
     float *jm = reinterpret_cast<float *>(smem);
     float *jl = jm + kRowsWarps * R;
     float *ja = jl + kRowsWarps * R;
-    Plan P = plan_at(ja + kRowsWarps * R * D, p.B, p.ng);
+    Plan P = plan_at(ja + kRowsWarps * R * D, p.B, p.ng, p.Hkv);
     make_plan(p, P);
+    asm volatile("griddepcontrol.launch_dependents;");  // the join may start planning
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int grp = lane / LPK, sub = lane % LPK;
     const T *Kp = static_cast<const T *>(p.K), *Vp = static_cast<const T *>(p.V);
 
-    const int total = P.ubase[p.B];
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-        const Unit U = decode_unit(p, P, u);
+    Units units(p, P, blockIdx.x);
+    Unit U;
+    while (units.next(p, P, U)) {
         float q[R][VE], acc[R][VE], m[R], l[R];
         // lane r masks for row r; the warp reads the masks from there
         Row mine;
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) 
             }
             int t, head;
             row_token(p, U, r, p.tpt, t, head);
-            if (U.ns > 1) {
+            if (U.split) {
                 const size_t slot = (size_t)U.slot * p.rows + r;
                 p.part_o[slot * D + x] = a;
                 if (x == 0) p.part_ml[slot] = make_float2(mx, ls);
@@ -241,97 +242,94 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) 
     }
 }
 
-// Joins the partial results of split sweeps, split by split in order: four
-// warps take a row, each a stretch of its splits. Launched so that its plan is
-// computed while the sweeps still run.
-constexpr int kMergeWarps = 4;
+// Joins the partial results of split tiles, piece by piece in order. A work item
+// is a boundary between two CTAs (a tile belongs to the first boundary inside
+// it) and kMergeRows rows of its tile. Tiles of few pieces: a warp per row.
+// Tiles of many (few rows against a long cache): the four warps share a row's
+// pieces. Launched so that its plan is computed while the sweeps still run.
+constexpr int kMergeWarps = 4, kMergeRows = 16, kMergeMany = 12;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge(const PagedProblem p) {
     constexpr int E = D / 32;
     extern __shared__ __align__(16) uint8_t smem[];
-    float *jm = reinterpret_cast<float *>(smem);  // [warp]
-    float *jl = jm + kMergeWarps;
-    float *ja = jl + kMergeWarps;  // [warp][D]
-    Plan P = plan_at(ja + kMergeWarps * D, p.B, p.ng);
+    float *jl = reinterpret_cast<float *>(smem);  // [warp]
+    float *ja = jl + 2 * kMergeWarps;             // [warp][D]
+    Plan P = plan_at(ja + kMergeWarps * D, p.B, p.ng, p.Hkv);
     make_plan(p, P);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the sweeps' results are visible from here on
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slots = P.sbase[p.B];
-    // work items: (slot of a sweep's first split, row)
-    const long long n_items = (long long)slots * p.rows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunks = (p.rows + kMergeRows - 1) / kMergeRows;
+    const int half_rows = p.tpt_half * p.group;
+    const long long n_items = (long long)(P.ctas - 1) * chunks;
     for (long long w = blockIdx.x; w < n_items; w += gridDim.x) {
-        const int row = (int)(w % p.rows), slot = (int)(w / p.rows);
-        int b = 0, hi = p.B;  // last sequence with sbase <= slot (its range is not empty)
-        while (hi - b > 1) {
-            const int mid = (b + hi) >> 1;
-            if (P.sbase[mid] <= slot) b = mid; else hi = mid;
-        }
-        const int ns = P.ns[b];
-        int r = slot - P.sbase[b];
-        if (r % ns) continue;
-        r /= ns;
-        const int tiles = (P.q[b] + p.tpt - 1) / p.tpt;
-        Unit U;
-        U.hk = r / tiles;
-        U.t0 = (tiles - 1 - r % tiles) * p.tpt;
-        // tiled kernels put the tokens of a unit's two halves apart: a row's
-        // token and head come from the half it is in
-        const int half_rows = p.rows > p.group * p.tpt_half ? p.rows / 2 : p.rows;
-        const int x = row / half_rows;
-        U.t0 += x * p.tpt_half;
-        int t, head;
-        row_token(p, U, row - x * half_rows, p.tpt_half, t, head);
-        const float2 *ml = p.part_ml + (size_t)slot * p.rows + row;
-        const float *po = p.part_o + ((size_t)slot * p.rows + row) * D + lane * E;
-        float mx = -CUDART_INF_F;
-        for (int c = lane; c < ns; c += 32) mx = fmaxf(mx, ml[(size_t)c * p.rows].x);
+        const int c = 1 + (int)(w / chunks), row0 = (int)(w % chunks) * kMergeRows;
+        const long long at = cta_begin(P, c);
+        const Tile tile = find_tile(p, P, at);
+        if (!tile.live || tile.begin == at || tile.begin < cta_begin(P, c - 1)) continue;
+        const int ns = cta_of(P, tile.end - 1) - c + 2;  // pieces: slot 2 c - 1, then 2 c, 2 c + 2, ...
+        const bool many = ns > kMergeMany;
+        const int step = many ? 1 : kMergeWarps;
+        for (int row = row0 + (many ? 0 : warp); row < min(row0 + kMergeRows, p.rows); row += step) {
+            // the two halves of a unit hold different tokens
+            Unit U;
+            const int x = row / half_rows;
+            U.hk = tile.hk;
+            U.t0 = tile.t0 + x * p.tpt_half;
+            int t, head;
+            row_token(p, U, row - x * half_rows, p.tpt_half, t, head);
+            if (t >= p.m) continue;
+            auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * c - 1 : 2 * (c + k - 1)) * p.rows + row; };
+            float mx = -CUDART_INF_F;
+            for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, p.part_ml[slot(k)].x);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, o));
-        const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-        float l = 0.f, acc[E];
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, o));
+            const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+            float l = 0.f, acc[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = 0.f;
-        const int c0 = ns * warp / kMergeWarps, c1 = ns * (warp + 1) / kMergeWarps;
+            for (int i = 0; i < E; ++i) acc[i] = 0.f;
+            const int k0 = many ? ns * warp / kMergeWarps : 0, k1 = many ? ns * (warp + 1) / kMergeWarps : ns;
 #pragma unroll 4
-        for (int c = c0; c < c1; ++c) {
-            const float2 y = ml[(size_t)c * p.rows];
-            const float f = ptx::ex2(y.x - ref);
-            l = fmaf(y.y, f, l);
-            const float *src = po + (size_t)c * p.rows * D;
+            for (int k = k0; k < k1; ++k) {
+                const size_t sl = slot(k);
+                const float2 y = p.part_ml[sl];
+                const float f = ptx::ex2(y.x - ref);
+                l = fmaf(y.y, f, l);
+                const float *src = p.part_o + sl * D + lane * E;
 #pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = fmaf(src[i], f, acc[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i) ja[warp * D + lane * E + i] = acc[i];
-        if (lane == 0) jl[warp] = l;
-        __syncthreads();
-        if (t < p.m) {
-            for (int d = tid; d < D; d += kMergeWarps * 32) {
-                float a = 0.f, ls = 0.f;
-#pragma unroll
-                for (int k = 0; k < kMergeWarps; ++k) {
-                    a += ja[k * D + d];
-                    ls += jl[k];
-                }
-                const bool valid = t < P.q[b];
-                static_cast<T *>(p.O)[(((size_t)b * p.Hq + head) * p.m + t) * D + d] =
-                    from_float<T>(!valid || ls == 0.f ? 0.f : a / ls);
+                for (int i = 0; i < E; ++i) acc[i] = fmaf(src[i], f, acc[i]);
             }
+            if (many) {
+                __syncthreads();  // the row before has been read
+#pragma unroll
+                for (int i = 0; i < E; ++i) ja[warp * D + lane * E + i] = acc[i];
+                if (lane == 0) jl[warp] = l;
+                __syncthreads();
+                if (warp != 0) continue;
+                l = jl[0];
+#pragma unroll
+                for (int k = 1; k < kMergeWarps; ++k) {
+                    l += jl[k];
+#pragma unroll
+                    for (int i = 0; i < E; ++i) acc[i] += ja[k * D + lane * E + i];
+                }
+            }
+            T *O = static_cast<T *>(p.O) + (((size_t)tile.b * p.Hq + head) * p.m + t) * D + lane * E;
+            const bool zero = t >= tile.q || l == 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) O[i] = from_float<T>(zero ? 0.f : acc[i] / l);
         }
-        __syncthreads();
     }
 }
 
 template <typename T, int D, int R>
 cudaError_t launch_rows(const PagedProblem &p, cudaStream_t stream) {
-    const size_t smem = (size_t)kRowsWarps * R * (D + 2) * 4 + plan_bytes(p.B, p.ng);
+    const size_t smem = (size_t)kRowsWarps * R * (D + 2) * 4 + plan_bytes(p.B, p.ng, p.Hkv);
     static std::atomic<bool> done[64];
     auto kern = paged_rows<T, D, R>;
     cudaError_t e = allow_smem(kern, done, smem);
     if (e != cudaSuccess) return e;
-    const long long units = (long long)p.B * p.Hkv + (p.cut ? p.max_parts : 0);
-    kern<<<(int)(units < p.slots ? units : p.slots), kRowsWarps * 32, smem, stream>>>(p);
+    kern<<<p.slots, kRowsWarps * 32, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -355,12 +353,12 @@ cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, cudaStream_
 }
 
 cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream) {
-    const size_t smem = (size_t)kMergeWarps * (p.d + 2) * 4 + plan_bytes(p.B, p.ng);
+    const size_t smem = (size_t)kMergeWarps * (p.d + 2) * 4 + plan_bytes(p.B, p.ng, p.Hkv);
     void (*kern)(const PagedProblem) =
         dtype == SA_FP32 ? (p.d == 64 ? paged_merge<float, 64> : paged_merge<float, 128>)
                          : (p.d == 64 ? paged_merge<__nv_bfloat16, 64> : paged_merge<__nv_bfloat16, 128>);
     // no more shared memory than a kernel has without asking: the largest plan takes 29 KB
-    const long long items = (long long)p.max_parts * p.rows, grid = 8ll * num_sms;
+    const long long items = (long long)p.slots * ((p.rows + kMergeRows - 1) / kMergeRows), grid = 8ll * num_sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items < grid ? items : grid));
     cfg.blockDim = dim3(kMergeWarps * 32);

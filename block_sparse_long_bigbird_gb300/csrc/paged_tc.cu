@@ -6,11 +6,12 @@
 // are two MMA tiles of 128 rows that share every key and value they load: a
 // 128-key stage serves 2 x 128 x 128 products, which halves the L2 traffic per
 // flop, and one tile's softmax overlaps the other's MMAs.
-//   * The producer warp walks the unit's 64-key blocks two at a time, looks the
-//     pages up (a step ahead), and loads K and V with one tensor copy per page
-//     piece: the pool is {d, page, num_pages * Hkv}, a box is 64 columns of one
-//     page (at most 64 tokens). A missing page is loaded from coordinate -1,
-//     which fills with zeros, so stages always fill.
+//   * Two loader warps walk the unit's 64-key blocks two at a time, look the
+//     pages up (a step ahead), and load K and V with one tensor copy per page
+//     piece; a third warp writes down what each step holds for the
+//     two tiles. The pool is {d, page, num_pages * Hkv}, a box is 64 columns of
+//     one page (at most 64 tokens). A missing page is loaded from coordinate
+//     -1, which fills with zeros, so stages always fill.
 //   * The MMA warp runs S_x = Q_x K^T for each tile into 128 TMEM columns and
 //     O_x += P_x V with P_x read from TMEM, where the softmax wrote it (bf16)
 //     over the first half of S_x. One thread issues all MMAs, so they complete
@@ -26,6 +27,8 @@
 // its copies and MMAs, frees TMEM and exits.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "paged_common.cuh"
 #include "tc_sync.cuh"
 
@@ -35,14 +38,14 @@ namespace {
 using namespace ptx;
 using namespace tcsync;
 
-constexpr int kTcThreads = 384;  // 8 softmax warps, producer, MMA, two spare (register budget of warpgroups)
+constexpr int kTcThreads = 384;  // 8 softmax warps, K loader, MMA issuer, step records, V loader
 constexpr int kRegion = 128 * 128;  // 128 rows x 128 B: one 64-column piece of a tile
 constexpr float kGrow = 8.0f;       // growth of the maximum (log2) that rescales O
 constexpr int kSI = 4;              // step records in flight
 
 struct StepRec {
     int blk[2];          // 64-key blocks (-1: none)
-    int use;             // bit x: tile x has a row that sees something here
+    int use;             // bit x: tile x has a row that sees something here; bit 2 + x: every row sees every key
     int vz0, vz1;        // V rows to zero (keys where no token was written)
     int pad;
     uint64_t gbits[2];   // global keys
@@ -58,7 +61,7 @@ struct TcCfg {
     static constexpr int ST_OFF = 2 * TILE;
     static constexpr int BAR_OFF = ST_OFF + NST * TILE;
     static constexpr int B_KF = 0, B_KE = B_KF + NST, B_IF = B_KE + NST, B_IE = B_IF + kSI, B_QF = B_IE + kSI,
-                         B_QE = B_QF + 1, B_SF = B_QE + 1, B_PF = B_SF + 2, B_OF = B_PF + 2, B_OE = B_OF + 2,
+                         B_QE = B_QF + 1, B_SF = B_QE + 1, B_PF = B_SF + 2, B_OF = B_PF + 4, B_OE = B_OF + 2,
                          B_MF = B_OE + 2, B_ME = B_MF + 1, B_DRAIN = B_ME + 1, B_COUNT = B_DRAIN + 1;
     static constexpr int REC_OFF = (BAR_OFF + B_COUNT * 8 + 15) & ~15;
     static constexpr int MISC_OFF = REC_OFF + kSI * (int)sizeof(StepRec);
@@ -68,9 +71,11 @@ struct TcCfg {
 };
 static_assert(sizeof(StepRec) == 56 && (kSI * sizeof(StepRec)) % 16 == 0, "step record layout");
 
-// Last token of tile x of a unit, its first visible position, and whether it has rows at all.
+// What tile x of a unit sees, and whether it has rows at all.
 struct TileSpan {
-    int p1, first;
+    int p0, p1;   // positions of its first and last token
+    int first;    // first position that any of its rows may see in a window
+    int last;     // first position that the windows of all its rows hold (stride 1)
     bool live;
 };
 
@@ -78,9 +83,10 @@ __device__ __forceinline__ TileSpan tile_span(const PagedProblem &p, const Plan 
     TileSpan s;
     const int t0 = U.t0 + x * p.tpt_half;
     s.live = U.live && t0 < U.q && (x == 0 || p.tpt > p.tpt_half);
-    const int p0 = U.s - U.q + t0;
+    const int p0 = s.p0 = U.s - U.q + t0;
     s.p1 = U.s - U.q + min(t0 + p.tpt_half, U.q) - 1;
     s.first = max(0, p0 - head_reach(p, stride));
+    s.last = s.p1 - head_reach(p, 1);
     if (p.ng && s.live) {
         const int i = lower_bound(P.gpos, p.ng, p0);
         if (i < p.ng && P.gpos[i] <= s.p1) s.first = 0;
@@ -117,7 +123,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(bar(C::B_QE), 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(C::B_SF + x), 1);
-            mbar_init(bar(C::B_PF + x), 4);
+            mbar_init(bar(C::B_PF + 2 * x), 4);
+            mbar_init(bar(C::B_PF + 2 * x + 1), 4);
             mbar_init(bar(C::B_OF + x), 1);
             mbar_init(bar(C::B_OE + x), 4);
         }
@@ -135,21 +142,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
     }
-    Plan P = plan_at(smem + C::PLAN_OFF, p.B, p.ng);
+    Plan P = plan_at(smem + C::PLAN_OFF, p.B, p.ng, p.Hkv);
     tc_fence_before();
     make_plan(p, P);
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    const int total = P.ubase[p.B];
+    asm volatile("griddepcontrol.launch_dependents;");  // the join may start planning
     uint32_t g = 0;   // steps so far; every role counts the same ones
     bool ok = true;
     const bool one = p.tpt == p.tpt_half;  // units of one tile: its steps alternate between two chains
+    Units units(p, P, blockIdx.x);
+    Unit U;
+    // Position in the stage ring of step i's K and V, in a unit of n steps that
+    // begins at step g0. Two tiles: K and V in turn, as they are used. Two
+    // chains of one tile: V of a step is used after K of the next.
+    auto k_at = [&](uint32_t g0, int i) { return 2 * g0 + (uint32_t)(one && i > 0 ? 2 * i - 1 : 2 * i); };
+    auto v_at = [&](uint32_t g0, int i, int n) {
+        return 2 * g0 + (uint32_t)(one ? (i == n - 1 ? 2 * n - 1 : 2 * i + 2) : 2 * i + 1);
+    };
 
     // The launch gave every thread 168 registers (384 x 168 = 64512); the
-    // softmax holds a row of scores, so its 8 warps take 200 and the others 104
-    // (256 x 200 + 128 x 104 = 64512).
+    // softmax holds a row of scores, so its 8 warps take 192 and the others 120
+    // (256 x 192 + 128 x 120 = 64512).
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         // ================================================================ softmax and epilogue of tile x
         const int x = warp >> 2;
         const int tid = threadIdx.x & 127;  // row of the tile = TMEM lane
@@ -158,9 +174,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int half_rows = p.tpt_half * p.group;
         const float sl2 = p.scale_log2;
         uint32_t sc = 0, oc = 0, oc2 = 0, mc = 0;
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-            const Unit U = decode_unit(p, P, u);
+        while (ok && units.next(p, P, U)) {
             const int n = U.live ? (U.e1 - U.e0 + 1) >> 1 : 0;
+            const uint32_t g0 = g;
             int t = 0, head = 0;
             Row row = {};
             const bool in = tid < half_rows;
@@ -176,8 +192,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t slot = g % kSI;
                 if (!(ok = wait_warp(bar(C::B_IF + slot), (g / kSI) & 1, ctl))) break;
                 const int use = recs[slot].use, vz0 = recs[slot].vz0, vz1 = recs[slot].vz1;
-                uint64_t w[2] = {0ull, 0ull};
-                if (((use >> x) & 1) && row.valid) {
+                uint64_t w[2] = {~0ull, ~0ull};
+                const bool all = (use >> (2 + x)) & 1;
+                if (((use >> x) & 1) && !all) {
+                    w[0] = w[1] = 0ull;
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         if (recs[slot].blk[k] >= 0)
@@ -186,8 +204,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
                 if (!((use >> x) & 1)) continue;
-                if (vz0 < vz1) {  // unwritten memory: no NaN may meet a zero weight
-                    const uint32_t sidx = 2 * g + 1, st = sidx % C::NST;
+                if (!(ok = wait_warp(bar(C::B_SF + x), sc & 1, ctl))) break;
+                ++sc;
+                // Unwritten memory: no NaN may meet a zero weight. (Not before S is
+                // there: only then are the products that read what the stage held
+                // before complete, and the wait below is for this step's V.)
+                if (vz0 < vz1) {
+                    const uint32_t sidx = v_at(g0, i, n), st = sidx % C::NST;
                     if (!(ok = wait_warp(bar(C::B_KF + st), (sidx / C::NST) & 1, ctl))) break;
                     uint8_t *v = smem + C::ST_OFF + st * C::TILE;
                     for (int c = tid; c < (vz1 - vz0) * 8 * C::DC; c += 128) {
@@ -197,11 +220,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                if (!(ok = wait_warp(bar(C::B_SF + x), sc & 1, ctl))) break;
-                ++sc;
                 if (busy) {
                     tc_fence_after();
-                    const bool full = __all_sync(kAllLanes, (w[0] & w[1]) == ~0ull || !row.valid);
+                    const bool full = all || __all_sync(kAllLanes, (w[0] & w[1]) == ~0ull || !row.valid);
                     float s[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, s[c]);
@@ -260,16 +281,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 pk[c * 16 + k / 2] = *reinterpret_cast<const uint32_t *>(&two);
                             }
                         tmem_st32u(s_addr + h * 32, pk);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::B_PF + 2 * x + h));
                     }
                     float a, e;
                     f2_unpack(f2_add(sum0, sum1), a, e);
                     l += a + e;
-                    tmem_wait_st();
-                    tc_fence_before();
+                } else if (lane == 0) {  // no row of this warp is used: let the others go on
+                    mbar_arrive(bar(C::B_PF + 2 * x));
+                    mbar_arrive(bar(C::B_PF + 2 * x + 1));
                 }
                 had = true;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_PF + x));
             }
             if (!ok) break;
             // ---- epilogue
@@ -343,7 +367,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);  // NaN if any is infinite or NaN
                     bad |= z != 0.f;
                     if (!in || (!row.valid && t >= p.m)) continue;
-                    if (U.ns > 1) {
+                    if (U.split) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
                             *reinterpret_cast<float4 *>(p.part_o + at * D + c * 32 + k) =
@@ -363,8 +387,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                 }
-                if (U.ns > 1 && in) p.part_ml[at] = make_float2(row.valid ? mref : -CUDART_INF_F, row.valid ? l : 0.f);
-            } else if (U.ns > 1 && in) {  // no valid row in this warp: the merge writes their zeros
+                if (U.split && in) p.part_ml[at] = make_float2(row.valid ? mref : -CUDART_INF_F, row.valid ? l : 0.f);
+            } else if (U.split && in) {  // no valid row in this warp: the merge writes their zeros
                 p.part_ml[(size_t)U.slot * p.rows + prow] = make_float2(-CUDART_INF_F, 0.f);
             } else if (in && t < p.m) {
                 uint4 *orow = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.O) +
@@ -391,37 +415,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == 8) {
-        // ================================================================ producer
-        const int bp = min(p.page, 64);      // tokens of a box
-        const int log_bp = min(p.log_page, 6);
-        const int ppb = 64 >> log_bp;        // boxes per block and piece
-        const int log_ppb = 6 - log_bp;
-        const int nbox = 2 * ppb * C::DC;    // per K or V stage
-        const uint64_t sub_bits = low_bits(bp);
-        uint32_t qc = 0, armed = 0;
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-            const Unit U = decode_unit(p, P, u);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (warp == 8 || warp == 11) {
+        // ================================================================ K (8) and V (11) loaders
+        const bool is_k = warp == 8;
+        const CUtensorMap *tm = is_k ? &tmK : &tmV;
+        const int log_bp = min(p.log_page, 6);  // tokens of a box: a page, at most 64
+        const int log_ppb = 6 - log_bp;         // boxes per block and 64-column piece
+        const int nbox = (2 << log_ppb) * C::DC;
+        const bool big = p.page > 64;
+        // this lane's box of a stage, before the lanes are moved on: a thread's
+        // copies complete one after another, different threads' overlap
+        uint32_t qc = 0, turn = 0;
+        uint32_t armed = 0, phase = 0;  // per stage: filled by this warp, and the parity of the last time
+        while (ok && units.next(p, P, U)) {
             const int n = (U.e1 - U.e0 + 1) >> 1;
             if (!U.live || n == 0) continue;
-            int stride = 1;
-            if (p.dilation)
-                for (int h = 0; h < p.group; ++h) stride = max(stride, head_stride(p, U.hk * p.group + h));
-            const TileSpan sp0 = tile_span(p, P, U, 0, stride), sp1 = tile_span(p, P, U, 1, stride);
-            // this lane's page of step i: entry lane / ppb of the step, piece lane % ppb
-            auto look = [&](int i, int &blk) -> int {
-                const int e = U.e0 + 2 * i + (lane >> log_ppb);
-                blk = -1;
-                if (lane >= 2 * ppb || e >= U.e1) return -1;
-                blk = entry_block(P, U, e);
-                const int pos = (blk << 6) + ((lane & (ppb - 1)) << log_bp);
-                return pos < U.s ? page_of(p, U.b, pos) : -1;
-            };
-            int blk, pg = look(0, blk);
-            if (qc > 0 && !(ok = wait_warp(bar(C::B_QE), (qc - 1) & 1, ctl))) break;
-            {
-                const int halves = sp1.live ? 2 : 1;
+            if (is_k) {
+                if (qc > 0 && !(ok = wait_warp(bar(C::B_QE), (qc - 1) & 1, ctl))) break;
+                const int halves = !one && U.t0 + p.tpt_half < U.q ? 2 : 1;
                 const int bytes = p.tpt_half * p.group * 128;
                 if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QF), (uint32_t)(halves * C::DC * bytes));
                 __syncwarp();
@@ -432,146 +444,218 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 ++qc;
             }
+            // coordinates (y, z) of this lane's box in step i; z = -1 reads zeros
+            auto look = [&](int i, int box, int &y) -> int {
+                const int piece = box / C::DC, e = U.e0 + 2 * i + (piece >> log_ppb);
+                y = 0;
+                if (box >= nbox || i >= n || e >= U.e1) return -1;
+                const int blk = entry_block(P, U, e);
+                const int pos = (blk << 6) + ((piece & ((1 << log_ppb) - 1)) << log_bp);
+                const int pg = pos < U.s ? page_of(p, U.b, pos) : -1;
+                if (pg < 0) return -1;
+                if (big) y = (blk & 1) * 64;
+                return pg * p.Hkv + U.hk;
+            };
+            int y, z, box = (lane - (int)turn) & 31;
+            z = look(0, box, y);
+            for (int i = 0; i < n; ++i) {
+                const uint32_t sidx = is_k ? k_at(g, i) : v_at(g, i, n), st = sidx % C::NST;
+                turn = (turn + nbox) & 31;
+                const int box1 = (lane - (int)turn) & 31;
+                int y1;
+                const int z1 = look(i + 1, box1, y1);  // on its way during this step's wait
+                if (sidx >= C::NST && !(ok = wait_warp(bar(C::B_KE + st), ((sidx / C::NST) - 1) & 1, ctl))) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KF + st), C::TILE);
+                __syncwarp();
+                if (box < nbox)
+                    tma_load_3d(sbase + C::ST_OFF + st * C::TILE + (box % C::DC) * kRegion +
+                                    ((box / C::DC) << log_bp) * 128,
+                                tm, bar(C::B_KF + st), (box % C::DC) * 64, y, z);
+                armed |= 1u << st;
+                phase = (phase & ~(1u << st)) | (((sidx / C::NST) & 1u) << st);
+                box = box1;
+                y = y1;
+                z = z1;
+            }
+            g += n;
+        }
+        if (!ok) {  // abort: wait for this warp's copies still in flight
+            for (int i = 0; i < C::NST; ++i)
+                if ((armed >> i) & 1u) wait_drain(bar(C::B_KF + i), (phase >> i) & 1u);
+            if (is_k && qc) wait_drain(bar(C::B_QF), (qc - 1) & 1);
+        }
+    } else if (warp == 10) {
+        // ================================================================ step records
+        // What each step holds for the tiles, ahead of their use. Lane l looks
+        // up piece l % ppb of entry l / ppb.
+        const int log_bp = min(p.log_page, 6), log_ppb = 6 - log_bp, ppb = 1 << log_ppb;
+        while (ok && units.next(p, P, U)) {
+            const int n = (U.e1 - U.e0 + 1) >> 1;
+            if (!U.live || n == 0) continue;
+            const int stride = p.dilation ? P.hstride[U.hk] : 1;
+            const TileSpan sp0 = tile_span(p, P, U, 0, stride), sp1 = tile_span(p, P, U, 1, stride);
+            auto look = [&](int i, int &blk) -> int {
+                const int e = U.e0 + 2 * i + (lane >> log_ppb);
+                blk = -1;
+                if (lane >= 2 * ppb || e >= U.e1) return -1;
+                blk = entry_block(P, U, e);
+                const int pos = (blk << 6) + ((lane & (ppb - 1)) << log_bp);
+                return pos < U.s ? page_of(p, U.b, pos) : -1;
+            };
+            int blk, pg = look(0, blk);
             for (int i = 0; i < n; ++i, ++g) {
                 const uint32_t slot = g % kSI;
                 int nblk = -1, npg = -1;
-                if (i + 1 < n) npg = look(i + 1, nblk);  // on its way during this step's waits
-                // the step's record: every lane computes it, lane 0 stores it
-                StepRec r;
-                const unsigned there = __ballot_sync(kAllLanes, pg >= 0);
-                r.use = 0;
-                r.vz0 = r.vz1 = 0;
-                r.pad = 0;
+                if (i + 1 < n) npg = look(i + 1, nblk);
+                // lanes 0 and 1 each do one of the step's two blocks
+                const unsigned there = __ballot_sync(kAllLanes, pg >= 0) >> ((lane & 1) << log_ppb);
+                const int b = __shfl_sync(kAllLanes, blk, (lane & 1) << log_ppb);
+                uint64_t w = 0ull;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int b = __shfl_sync(kAllLanes, blk, k << log_ppb);
-                    r.blk[k] = b;
-                    r.gbits[k] = b < 0 ? 0ull : global_bits(P, p, b);
-                    uint64_t w = 0ull;
-                    for (int s = 0; s < ppb; ++s)
-                        if ((there >> ((k << log_ppb) + s)) & 1u) w |= sub_bits << (s << log_bp);
-                    r.present[k] = w;
-                    if (b < 0) continue;
-                    const int j0 = b << 6;
-                    if (sp0.live && j0 <= sp0.p1 && (j0 + 63 >= sp0.first || r.gbits[k])) r.use |= 1;
-                    if (sp1.live && j0 <= sp1.p1 && (j0 + 63 >= sp1.first || r.gbits[k])) r.use |= 2;
-                    const int written = U.s - j0;  // keys of the block that hold tokens
-                    if (written < 64) {
-                        r.vz0 = k * 64 + max(written, 0);
-                        r.vz1 = k * 64 + 64;
-                    }
+                for (int s = 0; s < 4; ++s)
+                    if (s < ppb && ((there >> s) & 1u)) w |= low_bits(1 << log_bp) << (s << log_bp);
+                const uint64_t gb = b < 0 ? 0ull : global_bits(P, p, b);
+                const int j0 = b << 6;
+                int use = 0, written = 64;
+                if (b >= 0) {
+                    if (sp0.live && j0 <= sp0.p1 && (j0 + 63 >= sp0.first || gb)) use |= 1;
+                    if (sp1.live && j0 <= sp1.p1 && (j0 + 63 >= sp1.first || gb)) use |= 2;
+                    written = max(min(U.s - j0, 64), 0);  // keys of the block that hold tokens
                 }
-                if (one) r.use = (r.use & 1) << (i & 1);
+                const bool whole = stride == 1 && w == ~0ull;
+                int all = 0;
+                if (whole && j0 + 63 <= sp0.p0 && j0 >= sp0.last) all |= 4;
+                if (whole && j0 + 63 <= sp1.p0 && j0 >= sp1.last) all |= 8;
+                const int use2 = use | __shfl_xor_sync(kAllLanes, use, 1);
+                const int all2 = all & __shfl_xor_sync(kAllLanes, all, 1);
+                const int written2 = __shfl_xor_sync(kAllLanes, written, 1);
                 if (g >= kSI && !(ok = wait_warp(bar(C::B_IE + slot), ((g / kSI) - 1) & 1, ctl))) break;
-                if (lane == 0) {
-                    recs[slot] = r;
-                    mbar_arrive(bar(C::B_IF + slot));
+                if (lane < 2) {
+                    StepRec &r = recs[slot];
+                    r.blk[lane] = b;
+                    r.gbits[lane] = gb;
+                    r.present[lane] = w;
+                    if (lane == 0) {
+                        r.use = one ? ((use2 & 1) << (i & 1)) | ((all2 & 4) ? 12 : 0) : use2 | all2;
+                        // only the last block of a sequence holds unwritten keys
+                        r.vz0 = written < 64 ? written : 64 + written2;
+                        r.vz1 = written < 64 ? 64 : 128;
+                    }
                 }
                 __syncwarp();
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t sidx = 2 * g + kv, st = sidx % C::NST;
-                    if (sidx >= C::NST && !(ok = wait_warp(bar(C::B_KE + st), ((sidx / C::NST) - 1) & 1, ctl))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KF + st), C::TILE);
-                    __syncwarp();
-                    ++armed;
-                    // box index of this lane, moved on every stage: a thread's
-                    // copies complete one after another, different threads' overlap
-                    const int box = (lane - (int)((sidx * (uint32_t)nbox) & 31u)) & 31;
-                    const int piece = box / C::DC, dc = box % C::DC;
-                    const int from = box < nbox ? piece : 0;
-                    const int bpg = __shfl_sync(kAllLanes, pg, from), bblk = __shfl_sync(kAllLanes, blk, from);
-                    if (box < nbox) {
-                        const int y = p.page > 64 ? (bblk & 1) * 64 : 0;
-                        const int z = bpg < 0 ? -1 : bpg * p.Hkv + U.hk;
-                        tma_load_3d(sbase + C::ST_OFF + st * C::TILE + dc * kRegion + (piece << log_bp) * 128,
-                                    kv ? &tmV : &tmK, bar(C::B_KF + st), dc * 64, z < 0 ? 0 : y, z);
-                    }
-                }
-                if (!ok) break;
+                if (lane == 0) mbar_arrive(bar(C::B_IF + slot));
                 blk = nblk;
                 pg = npg;
             }
-        }
-        if (!ok) {  // abort: wait for the copies still in flight
-            for (uint32_t i = 0; i < (uint32_t)C::NST && i < armed; ++i)
-                wait_drain(bar(C::B_KF + i), ((armed - 1 - i) / C::NST) & 1);
-            if (qc) wait_drain(bar(C::B_QF), (qc - 1) & 1);
         }
     } else if (warp == 9) {
         // ================================================================ MMA issuer
         constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false);
         constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
+        // The whole warp runs the loop and the waits, so descriptors and TMEM
+        // addresses stay warp-uniform; one elected lane issues the MMAs and the
+        // commits that track them.
         const bool leader = elect_one();
         const uint64_t dQ0 = desc_sw128(sbase + C::Q_OFF, 16);
         const uint64_t dK0 = desc_sw128(sbase + C::ST_OFF, 16);
         const uint64_t dV0 = desc_sw128(sbase + C::ST_OFF, kRegion);
         uint32_t qc = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
-        for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-            const Unit U = decode_unit(p, P, u);
+        auto filled = [&](uint32_t sidx) {
+            return wait_warp(bar(C::B_KF + sidx % C::NST), (sidx / C::NST) & 1, ctl);
+        };
+        // tiles that use step gs; waits for its record
+        auto step_use = [&](uint32_t gs, int &use) -> bool {
+            const uint32_t slot = gs % kSI;
+            if (!wait_warp(bar(C::B_IF + slot), (gs / kSI) & 1, ctl)) return false;
+            use = recs[slot].use & 3;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
+            return true;
+        };
+        while (ok && units.next(p, P, U)) {
             const int n = (U.e1 - U.e0 + 1) >> 1;
             if (!U.live || n == 0) continue;
+            int use = 0, next_use = 0;
+            if (!(ok = step_use(g, next_use))) break;
             if (!(ok = wait_warp(bar(C::B_QF), qc & 1, ctl))) break;
             ++qc;
+            const uint32_t g0 = g;
             int prev = 0;        // tiles whose P of the step before is to be used
             int started = 0;     // tiles with a product in O already
-            for (int i = 0; i <= n; ++i) {
-                int use = 0;
-                const uint32_t sk = (2 * g) % C::NST, sv = (2 * g - 1) % C::NST;  // K of step g, V of step g - 1
-                if (i < n) {
-                    const uint32_t slot = g % kSI;
-                    if (!(ok = wait_warp(bar(C::B_IF + slot), (g / kSI) & 1, ctl))) break;
-                    use = recs[slot].use;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
-                    if (!(ok = wait_warp(bar(C::B_KF + sk), ((2 * g) / C::NST) & 1, ctl))) break;
+            // S_X = Q_X K^T with the K of ring position kx
+            auto scores = [&](auto X, uint32_t kx) {
+                constexpr int x = decltype(X)::value;
+                tc_fence_after();
+                if (leader) {
+                    const uint64_t dQ = one ? dQ0 : dQ0 + (uint64_t)((x * C::TILE) >> 4);
+                    const uint64_t dK = dK0 + (uint64_t)(((kx % C::NST) * C::TILE) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
+                        mma_bf16_ss(tmem + x * 128, dQ + off, dK + off, idesc_qk, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(bar(C::B_SF + x));
                 }
-                if (i > 0 && !(ok = wait_warp(bar(C::B_KF + sv), ((2 * g - 1) / C::NST) & 1, ctl))) break;
-                auto scores = [&](int x) {
+                __syncwarp();
+            };
+            // O_X (+)= P_X V with the V of ring position vx: 64 keys as soon as their weights are there
+            auto weigh = [&](auto X, uint32_t vx) -> bool {
+                constexpr int x = decltype(X)::value;
+                const bool first = !((started >> x) & 1);
+                if (first && oc[x] > 0 && !wait_warp(bar(C::B_OE + x), (oc[x] - 1) & 1, ctl)) return false;
+                const uint64_t dV = dV0 + (uint64_t)(((vx % C::NST) * C::TILE) >> 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait_warp(bar(C::B_PF + 2 * x + h), pc[x] & 1, ctl)) return false;
                     tc_fence_after();
                     if (leader) {
-                        const uint64_t dQ = dQ0 + (uint64_t)(((one ? 0 : x) * C::TILE) >> 4);
-                        const uint64_t dK = dK0 + (uint64_t)((sk * C::TILE) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
-                            mma_bf16_ss(tmem + x * 128, dQ + off, dK + off, idesc_qk, kk > 0 ? 1u : 0u);
-                        }
-                        mma_commit(bar(C::B_SF + x));
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            mma_bf16_ts(tmem + C::O_COL + x * D, tmem + x * 128 + kk * 8,
+                                        dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, (first && kk == 0) ? 0u : 1u);
                     }
                     __syncwarp();
-                };
-                // chains that do not follow on themselves need not wait for the other's weights
-                const bool early = (prev & use) == 0;
-                if (early) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        if ((use >> x) & 1) scores(x);
                 }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if ((prev >> x) & 1) {
-                        if (!(ok = wait_warp(bar(C::B_PF + x), pc[x] & 1, ctl))) break;
-                        ++pc[x];
-                        const bool first = !((started >> x) & 1);
-                        if (first && oc[x] > 0 && !(ok = wait_warp(bar(C::B_OE + x), (oc[x] - 1) & 1, ctl))) break;
-                        tc_fence_after();
-                        if (leader) {
-                            const uint64_t dV = dV0 + (uint64_t)((sv * C::TILE) >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                mma_bf16_ts(tmem + C::O_COL + x * D, tmem + x * 128 + kk * 8,
-                                            dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, (first && kk == 0) ? 0u : 1u);
-                        }
-                        __syncwarp();
-                        started |= 1 << x;
+                ++pc[x];
+                started |= 1 << x;
+                return true;
+            };
+            auto release = [&](uint32_t sidx) {
+                if (leader) mma_commit(bar(C::B_KE + sidx % C::NST));
+                __syncwarp();
+            };
+            const std::integral_constant<int, 0> T0{};
+            const std::integral_constant<int, 1> T1{};
+            for (int i = 0; i <= n; ++i) {
+                use = i < n ? next_use : 0;
+                const uint32_t kx = k_at(g0, i), vx = i > 0 ? v_at(g0, i - 1, n) : 0;
+                if (one) {  // the chains take turns: this step's scores need not wait for the other's weights
+                    if (i < n) {
+                        if (!(ok = filled(kx))) break;
+                        if (use & 1) scores(T0, kx);
+                        if (use & 2) scores(T1, kx);
+                        release(kx);
                     }
-                    if (!early && ((use >> x) & 1)) scores(x);
+                    if (i + 1 < n && !(ok = step_use(g + 1, next_use))) break;
+                    if (i > 0) {
+                        if (!(ok = filled(vx))) break;
+                        if ((prev & 1) && !(ok = weigh(T0, vx))) break;
+                        if ((prev & 2) && !(ok = weigh(T1, vx))) break;
+                        release(vx);
+                    }
+                } else {
+                    if (i < n && !(ok = filled(kx))) break;
+                    if (i > 0 && !(ok = filled(vx))) break;
+                    if ((prev & 1) && !(ok = weigh(T0, vx))) break;
+                    if (use & 1) scores(T0, kx);
+                    // while the other tile's softmax works: the next step's record
+                    if (i + 1 < n && !(ok = step_use(g + 1, next_use))) break;
+                    if ((prev & 2) && !(ok = weigh(T1, vx))) break;
+                    if (use & 2) scores(T1, kx);
+                    if (i > 0) release(vx);
+                    if (i < n) release(kx);
                 }
-                if (!ok) break;
                 if (leader) {
-                    if (i > 0) mma_commit(bar(C::B_KE + sv));
-                    if (i < n) mma_commit(bar(C::B_KE + sk));
                     if (i == n - 1) mma_commit(bar(C::B_QE));
                     if (i == n) {
                         if (started & 1) mma_commit(bar(C::B_OF + 0));
@@ -631,7 +715,7 @@ bool make_map(CUtensorMap *m, const void *base, int d, int rows, long long slice
 template <int D>
 cudaError_t launch_tc_d(const PagedProblem &p, cudaStream_t stream) {
     using C = TcCfg<D>;
-    const size_t smem = C::PLAN_OFF + plan_bytes(p.B, p.ng) + 1024;
+    const size_t smem = C::PLAN_OFF + plan_bytes(p.B, p.ng, p.Hkv) + 1024;
     if (smem > 232448) return cudaErrorNotSupported;
     CUtensorMap mq, mk, mv;
     const int bp = p.page < 64 ? p.page : 64;
@@ -643,8 +727,7 @@ cudaError_t launch_tc_d(const PagedProblem &p, cudaStream_t stream) {
     static std::atomic<bool> done[64];
     cudaError_t e = allow_smem(kern, done, smem);
     if (e != cudaSuccess) return e;
-    const long long units = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt) + (p.cut ? p.max_parts : 0);
-    kern<<<(int)(units < p.slots ? units : p.slots), kTcThreads, smem, stream>>>(mq, mk, mv, p);
+    kern<<<p.slots, kTcThreads, smem, stream>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 
@@ -654,8 +737,8 @@ cudaError_t launch_paged_tc(const PagedProblem &p, cudaStream_t stream) {
     return p.d == 64 ? launch_tc_d<64>(p, stream) : launch_tc_d<128>(p, stream);
 }
 
-static_assert(TcCfg<128>::PLAN_OFF + 1024 + ((5 * kPagedMaxBatch + 2 * kPagedMaxGlobal + 6 + kCuts) * 4 + 16) +
-                      kPagedMaxGlobal * 8 <= 232448,
+static_assert(TcCfg<128>::PLAN_OFF + 1024 + (2 * kPagedMaxBatch + 2 * kPagedMaxGlobal + kPagedMaxHeads + 2) * 4 + 16 +
+                      (kPagedMaxBatch + 1 + kPagedMaxGlobal) * 8 <= 232448,
               "the largest plan fits beside the tiles");
 
 }  // namespace sa

@@ -38,15 +38,16 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
     float *Ps = reinterpret_cast<float *>(smem + L::S);    // [key][kPad rows]
     uint64_t *masks = reinterpret_cast<uint64_t *>(smem + L::MASK);
     int *flags = reinterpret_cast<int *>(smem + L::FLAG);
-    Plan P = plan_at(smem + L::PLAN, p.B, p.ng);
+    Plan P = plan_at(smem + L::PLAN, p.B, p.ng, p.Hkv);
     make_plan(p, P);
+    asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ty = tid >> 4, tx = tid & 15;  // rows ty * 8 ..., keys and columns tx * 4 ...
     const T *Kp = static_cast<const T *>(p.K), *Vp = static_cast<const T *>(p.V);
 
-    const int total = P.ubase[p.B];
-    for (int u = blockIdx.x; u < total; u += gridDim.x) {
-        const Unit U = decode_unit(p, P, u);
+    Units units(p, P, blockIdx.x);
+    Unit U;
+    while (units.next(p, P, U)) {
         // threads 0..63: one row each, for the masks
         Row row = {};
         if (tid < kTR) {
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
 #pragma unroll
             for (int x = 0; x < 4 * ND; ++x) bad |= not_finite(acc[r][x]);
             if (bad && valid) flags[rr] = 1;
-            if (U.ns > 1) {
+            if (U.split) {
                 const size_t slot = (size_t)U.slot * p.rows + rr;
 #pragma unroll
                 for (int h = 0; h < ND; ++h)
@@ -230,14 +231,12 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
 
 template <typename T, int D>
 cudaError_t launch_tile(const PagedProblem &p, cudaStream_t stream) {
-    const size_t smem = TileSmem<T, D>::PLAN + plan_bytes(p.B, p.ng);
+    const size_t smem = TileSmem<T, D>::PLAN + plan_bytes(p.B, p.ng, p.Hkv);
     static std::atomic<bool> done[64];
     auto kern = paged_tile<T, D>;
     cudaError_t e = allow_smem(kern, done, smem);
     if (e != cudaSuccess) return e;
-    const long long units = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt) + (p.cut ? p.max_parts : 0);
-    const long long grid = (D == 64 ? 2ll : 1ll) * p.slots;
-    kern<<<(int)(units < grid ? units : grid), kTT, smem, stream>>>(p);
+    kern<<<p.slots, kTT, smem, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -494,7 +494,7 @@ sa_status bigbird_attn_fwd_noalloc(const void *Q, const void *K, const void *V, 
  * 2 * (max_pages * page) sees every earlier token.
  *
  * Q, O: DEVICE [B][Hq][m][d], contiguous, 16-byte aligned, O not aliasing Q.
- * Hq: a multiple of Hkv, at most 64 query heads per key head; head h reads key
+ * Hq: a multiple of Hkv (at most 256), at most 64 query heads per key head; head h reads key
  *   head h / (Hq / Hkv).
  * Rows t >= q_lens[b], and rows that see no key, are written as zeros. What
  * memory holds where no token was written, or at keys a row does not see, does
@@ -514,7 +514,7 @@ sa_status bigbird_attn_fwd_noalloc(const void *Q, const void *K, const void *V, 
  *   the partial results of long sweeps cut into pieces.
  * Errors: SA_ERR_INVALID_ARG for any size or pointer outside the contract or a
  *   workspace too small; SA_ERR_UNSUPPORTED without an sm_103 device, or past
- *   the limits (B, group, n_global, lengths); SA_ERR_CUDA if a launch fails.
+ *   the limits (B, heads, n_global, lengths); SA_ERR_CUDA if a launch fails.
  */
 sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const void *V_pages, void *O,
                                     int B, int Hq, int Hkv, int m, int d,
