@@ -6,16 +6,17 @@
 // are two MMA tiles of 128 rows that share every key and value they load: a
 // 128-key stage serves 2 x 128 x 128 products, which halves the L2 traffic per
 // flop, and one tile's softmax overlaps the other's MMAs.
-//   * Two loader warps walk the unit's 64-key blocks two at a time, look the
-//     pages up (a step ahead), and load K and V with one tensor copy per page
-//     piece; a third warp writes down what each step holds for the
+//   * The loader warp walks the unit's 64-key blocks two at a time, looks the
+//     pages up (a step ahead), and loads K and V with one tensor copy per page
+//     piece; another warp writes down what each step holds for the
 //     two tiles. The pool is {d, page, num_pages * Hkv}, a box is 64 columns of
 //     one page (at most 64 tokens). A missing page is loaded from coordinate
 //     -1, which fills with zeros, so stages always fill.
-//   * The MMA warp runs S_x = Q_x K^T for each tile into 128 TMEM columns and
+//   * An MMA warp per tile runs S_x = Q_x K^T into 128 TMEM columns and
 //     O_x += P_x V with P_x read from TMEM, where the softmax wrote it (bf16)
-//     over the first half of S_x. One thread issues all MMAs, so they complete
-//     in order: S_x of a step complete means P_x V of the step before is too.
+//     over the first half of S_x. One thread issues a tile's MMAs, so they
+//     complete in order: S_x of a step complete means P_x V of the step before
+//     is too.
 //   * A warpgroup per tile runs the softmax, one thread per row: masks, running
 //     maximum (kept until it grows by more than 2^8, then O is rescaled in
 //     place), weights and their sum in fp32, P rounded to bf16 (relative 2^-8,
@@ -38,14 +39,24 @@ namespace {
 using namespace ptx;
 using namespace tcsync;
 
-constexpr int kTcThreads = 384;  // 8 softmax warps, K loader, MMA issuer, step records, V loader
+constexpr int kTcThreads = 384;  // 8 softmax warps, loader, two MMA issuers, step records
 constexpr int kRegion = 128 * 128;  // 128 rows x 128 B: one 64-column piece of a tile
 constexpr float kGrow = 8.0f;       // growth of the maximum (log2) that rescales O
 constexpr int kSI = 4;              // step records in flight
+constexpr int kNU = 4;              // units in flight
+
+constexpr int kNowhere = 0x40000200;  // past every position
+
+struct UnitRec {
+    Unit U;
+    int n;      // steps
+    int end;    // nonzero: there is no further unit
+};
 
 struct StepRec {
-    int blk[2];          // 64-key blocks (-1: none)
-    int use;             // bit x: tile x has a row that sees something here; bit 2 + x: every row sees every key
+    int j0[2];           // first keys of the two 64-key blocks (kNowhere: none)
+    int use;             // bit x: tile x has a row that sees something here; 2 + x: all its rows see every key;
+                         // 4: every row sees an interval of the keys and no others
     int vz0, vz1;        // V rows to zero (keys where no token was written)
     int pad;
     uint64_t gbits[2];   // global keys
@@ -62,14 +73,15 @@ struct TcCfg {
     static constexpr int BAR_OFF = ST_OFF + NST * TILE;
     static constexpr int B_KF = 0, B_KE = B_KF + NST, B_IF = B_KE + NST, B_IE = B_IF + kSI, B_QF = B_IE + kSI,
                          B_QE = B_QF + 1, B_SF = B_QE + 1, B_PF = B_SF + 2, B_OF = B_PF + 4, B_OE = B_OF + 2,
-                         B_MF = B_OE + 2, B_ME = B_MF + 1, B_DRAIN = B_ME + 1, B_COUNT = B_DRAIN + 1;
+                         B_MF = B_OE + 2, B_ME = B_MF + 1, B_UF = B_ME + 1, B_UE = B_UF + kNU, B_DRAIN = B_UE + kNU, B_COUNT = B_DRAIN + 2;
     static constexpr int REC_OFF = (BAR_OFF + B_COUNT * 8 + 15) & ~15;
-    static constexpr int MISC_OFF = REC_OFF + kSI * (int)sizeof(StepRec);
+    static constexpr int UNIT_OFF = REC_OFF + kSI * (int)sizeof(StepRec);
+    static constexpr int MISC_OFF = UNIT_OFF + kNU * (int)sizeof(UnitRec);
     static constexpr int ML_OFF = MISC_OFF + 16;       // one-tile units: the second chain's (maximum, sum) per row
     static constexpr int PLAN_OFF = ML_OFF + 128 * 8;
     static constexpr uint32_t O_COL = 256;
 };
-static_assert(sizeof(StepRec) == 56 && (kSI * sizeof(StepRec)) % 16 == 0, "step record layout");
+static_assert((kSI * sizeof(StepRec)) % 16 == 0 && (kNU * sizeof(UnitRec)) % 16 == 0, "record layout");
 
 // What tile x of a unit sees, and whether it has rows at all.
 struct TileSpan {
@@ -94,6 +106,13 @@ __device__ __forceinline__ TileSpan tile_span(const PagedProblem &p, const Plan 
     return s;
 }
 
+// `n` bits from bit `at` on (both clamped to 32).
+__device__ __forceinline__ uint32_t bit_run(int at, int n) {
+    uint32_t m;
+    asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(m) : "r"(at), "r"(n));
+    return m;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -105,22 +124,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
     StepRec *recs = reinterpret_cast<StepRec *>(smem + C::REC_OFF);
+    UnitRec *unit_recs = reinterpret_cast<UnitRec *>(smem + C::UNIT_OFF);
     auto bar = [&](int i) { return sbase + C::BAR_OFF + 8u * (uint32_t)i; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Ctl ctl{abort_flag, p.status, p.wait_ns};
+    const bool one = p.tpt == p.tpt_half;  // units of one tile: its steps alternate between two chains
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int i = 0; i < C::NST; ++i) {
             mbar_init(bar(C::B_KF + i), 1);
-            mbar_init(bar(C::B_KE + i), 1);
+            mbar_init(bar(C::B_KE + i), one ? 1 : 2);  // the MMA warps that read the stage
         }
         for (int i = 0; i < kSI; ++i) {
             mbar_init(bar(C::B_IF + i), 1);
-            mbar_init(bar(C::B_IE + i), 9);  // 8 softmax warps and the MMA warp
+            mbar_init(bar(C::B_IE + i), one ? 8 : 10);  // 8 softmax warps, with two tiles the MMA warps too
+        }
+        for (int i = 0; i < kNU; ++i) {
+            mbar_init(bar(C::B_UF + i), 1);
+            mbar_init(bar(C::B_UE + i), 11);  // all warps but the one that writes them
         }
         mbar_init(bar(C::B_QF), 1);
-        mbar_init(bar(C::B_QE), 1);
+        mbar_init(bar(C::B_QE), 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(C::B_SF + x), 1);
             mbar_init(bar(C::B_PF + 2 * x), 4);
@@ -131,6 +156,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(bar(C::B_MF), 4);
         mbar_init(bar(C::B_ME), 4);
         mbar_init(bar(C::B_DRAIN), 1);
+        mbar_init(bar(C::B_DRAIN + 1), 1);
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -150,22 +176,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");  // the join may start planning
     uint32_t g = 0;   // steps so far; every role counts the same ones
     bool ok = true;
-    const bool one = p.tpt == p.tpt_half;  // units of one tile: its steps alternate between two chains
-    Units units(p, P, blockIdx.x);
-    Unit U;
-    // Position in the stage ring of step i's K and V, in a unit of n steps that
-    // begins at step g0. Two tiles: K and V in turn, as they are used. Two
-    // chains of one tile: V of a step is used after K of the next.
-    auto k_at = [&](uint32_t g0, int i) { return 2 * g0 + (uint32_t)(one && i > 0 ? 2 * i - 1 : 2 * i); };
-    auto v_at = [&](uint32_t g0, int i, int n) {
-        return 2 * g0 + (uint32_t)(one ? (i == n - 1 ? 2 * n - 1 : 2 * i + 2) : 2 * i + 1);
+    uint32_t uc = 0;  // units so far
+    // The following unit's record; `done` once there is none.
+    bool done = false;
+    auto next_unit = [&]() -> const UnitRec & {
+        const uint32_t slot = uc % kNU;
+        ok = wait_warp(bar(C::B_UF + slot), (uc / kNU) & 1, ctl);
+        ++uc;
+        done = !ok || unit_recs[slot].end;
+        return unit_recs[slot];
+    };
+    auto unit_done = [&]() {  // this warp has no more use for the unit's record
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_UE + (uc - 1) % kNU));
+    };
+    // Stage of step i's K (kv = 0) or V (1) in the unit that begins at step g,
+    // and the number of times that it has been filled before. Two tiles use one
+    // ring of all stages; two chains of one tile have a ring each, since a
+    // chain that ran ahead on a shared ring could take the parity of a stage
+    // that the other's data has yet to fill for that of its own.
+    // (h0, h1: steps of the two chains so far.)
+    uint32_t h0 = 0, h1 = 0;
+    struct Pos {
+        uint32_t st, times;
+    };
+    auto stage = [&](int i, int kv) -> Pos {
+        if (!one) {
+            const uint32_t n = 2 * (g + (uint32_t)i) + (uint32_t)kv;
+            return {n % C::NST, n / C::NST};
+        }
+        const uint32_t n = 2 * ((i & 1 ? h1 : h0) + (uint32_t)(i >> 1)) + (uint32_t)kv;
+        return {(i & 1 ? C::NST / 2 : 0) + n % (C::NST / 2), n / (C::NST / 2)};
+    };
+    auto unit_steps = [&](int n) {  // past a unit of n steps
+        g += (uint32_t)n;
+        h0 += (uint32_t)(n + 1) >> 1;
+        h1 += (uint32_t)n >> 1;
     };
 
     // The launch gave every thread 168 registers (384 x 168 = 64512); the
-    // softmax holds a row of scores, so its 8 warps take 192 and the others 120
-    // (256 x 192 + 128 x 120 = 64512).
+    // softmax holds a row of scores, so its 8 warps take 200 and the others 104
+    // (256 x 200 + 128 x 104 = 64512).
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ================================================================ softmax and epilogue of tile x
         const int x = warp >> 2;
         const int tid = threadIdx.x & 127;  // row of the tile = TMEM lane
@@ -173,33 +226,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t s_addr = tmem + lane_base + x * 128, o_addr = tmem + lane_base + C::O_COL + x * D;
         const int half_rows = p.tpt_half * p.group;
         const float sl2 = p.scale_log2;
+        const int my_g = tid / p.tpt_half, my_t = tid - my_g * p.tpt_half + (one ? 0 : x * p.tpt_half);
+        const bool in = tid < half_rows;
         uint32_t sc = 0, oc = 0, oc2 = 0, mc = 0;
-        while (ok && units.next(p, P, U)) {
-            const int n = U.live ? (U.e1 - U.e0 + 1) >> 1 : 0;
-            const uint32_t g0 = g;
-            int t = 0, head = 0;
+        while (ok) {
+            const UnitRec &R = next_unit();
+            if (done) break;
+            const Unit &U = R.U;
+            const int n = R.n;
+            const int t = in ? U.t0 + my_t : 0, head = in ? U.hk * p.group + my_g : 0;
             Row row = {};
-            const bool in = tid < half_rows;
-            if (in) {
-                row_token(p, U, tid, p.tpt_half, t, head);
-                if (!one) t += x * p.tpt_half;
-                row = make_row(p, P, U, head, t);
-            }
+            if (in) row = make_row(p, P, U, head, t);
+            // positions the row's window holds (stride 1): [first, after)
+            const int after = row.valid ? row.pos + 1 : -1;
+            const int first = row.glob ? -1 : max(row.pos - row.reach, -1);
             const bool busy = __any_sync(kAllLanes, row.valid);
             float mref = -CUDART_INF_F, l = 0.f;
             bool had = false;
-            for (int i = 0; i < n; ++i, ++g) {
-                const uint32_t slot = g % kSI;
-                if (!(ok = wait_warp(bar(C::B_IF + slot), (g / kSI) & 1, ctl))) break;
+            for (int i = 0; i < n; ++i) {
+                const uint32_t gs = g + (uint32_t)i, slot = gs % kSI;
+                if (!(ok = wait_warp(bar(C::B_IF + slot), (gs / kSI) & 1, ctl))) break;
                 const int use = recs[slot].use, vz0 = recs[slot].vz0, vz1 = recs[slot].vz1;
-                uint64_t w[2] = {~0ull, ~0ull};
+                uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};  // visible keys, 32 at a time
                 const bool all = (use >> (2 + x)) & 1;
                 if (((use >> x) & 1) && !all) {
-                    w[0] = w[1] = 0ull;
+                    const int j0[2] = {recs[slot].j0[0], recs[slot].j0[1]};
+                    if (use & 16) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (recs[slot].blk[k] >= 0)
-                            w[k] = row_mask(row, recs[slot].blk[k], recs[slot].gbits[k], recs[slot].present[k]);
+                        for (int c = 0; c < 4; ++c) {
+                            const int j = j0[c >> 1] + (c & 1) * 32;
+                            const int lo = max(first - j, 0), hi = min(after - j, 32);
+                            w[c] = bit_run(lo, max(hi - lo, 0));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint64_t m =
+                                j0[k] == kNowhere ? 0ull : row_mask(row, j0[k] >> 6, recs[slot].gbits[k], recs[slot].present[k]);
+                            w[2 * k] = (uint32_t)m;
+                            w[2 * k + 1] = (uint32_t)(m >> 32);
+                        }
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
@@ -210,9 +277,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // there: only then are the products that read what the stage held
                 // before complete, and the wait below is for this step's V.)
                 if (vz0 < vz1) {
-                    const uint32_t sidx = v_at(g0, i, n), st = sidx % C::NST;
-                    if (!(ok = wait_warp(bar(C::B_KF + st), (sidx / C::NST) & 1, ctl))) break;
-                    uint8_t *v = smem + C::ST_OFF + st * C::TILE;
+                    const Pos v_at = stage(i, 1);
+                    if (!(ok = wait_warp(bar(C::B_KF + v_at.st), v_at.times & 1, ctl))) break;
+                    uint8_t *v = smem + C::ST_OFF + v_at.st * C::TILE;
                     for (int c = tid; c < (vz1 - vz0) * 8 * C::DC; c += 128) {
                         const int r = vz0 + c / (8 * C::DC), q = c % (8 * C::DC);
                         *reinterpret_cast<uint4 *>(v + (q >> 3) * kRegion + r * 128 + (q & 7) * 16) =
@@ -222,24 +289,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (busy) {
                     tc_fence_after();
-                    const bool full = all || __all_sync(kAllLanes, (w[0] & w[1]) == ~0ull || !row.valid);
+                    // 32 keys that no row of the warp sees need no exponentials,
+                    // those that all see need no masks
+                    int some = 15, full = 15;
+                    if (!all) {
+                        some = full = 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (__any_sync(kAllLanes, w[c] != 0u)) some |= 1 << c;
+                            if (__all_sync(kAllLanes, w[c] == ~0u || !row.valid)) full |= 1 << c;
+                        }
+                    }
                     float s[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, s[c]);
                     tmem_wait_ld();
-                    if (!full) {
+                    float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                    if (full == 15) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) mx4[c] = fmax3(mx4[c], s[c][k], s[c][k + 1]);
+                    } else {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const uint32_t b = (uint32_t)(w[c >> 1] >> ((c & 1) * 32));
+                            if (!((some >> c) & 1)) continue;
+                            if (!((full >> c) & 1)) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) s[c][k] = (b >> k) & 1u ? s[c][k] : -CUDART_INF_F;
+                                for (int k = 0; k < 32; ++k) s[c][k] = (w[c] >> k) & 1u ? s[c][k] : -CUDART_INF_F;
+                            }
+                            float m0 = -CUDART_INF_F, m1 = m0;
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                m0 = fmax3(m0, s[c][k], s[c][k + 1]);
+                                m1 = fmax3(m1, s[c][k + 2], s[c][k + 3]);
+                            }
+                            mx4[c] = fmaxf(m0, m1);
                         }
                     }
-                    float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) mx4[c] = fmax3(mx4[c], s[c][k], s[c][k + 1]);
                     float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
                     mx = row.valid ? mx * sl2 : -CUDART_INF_F;
                     const bool grow = mx > mref + kGrow || (mref == -CUDART_INF_F && mx > mref);
@@ -268,7 +355,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         uint32_t pk[32];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < 2; ++c) {
+                            if (!((some >> (2 * h + c)) & 1)) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) pk[c * 16 + k] = 0u;
+                                continue;
+                            }
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
                                 float a, e;
@@ -280,6 +372,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 const __nv_bfloat162 two = __floats2bfloat162_rn(a, e);
                                 pk[c * 16 + k / 2] = *reinterpret_cast<const uint32_t *>(&two);
                             }
+                        }
                         tmem_st32u(s_addr + h * 32, pk);
                         tmem_wait_st();
                         tc_fence_before();
@@ -296,6 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 had = true;
             }
             if (!ok) break;
+            unit_steps(n);
             // ---- epilogue
             // One-tile units: the second chain hands over its maximum and sum, and
             // the first chain's warps join both O's (they hold the same lanes).
@@ -309,6 +403,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_MF));
                     ++mc;
+                    unit_done();
                     continue;
                 }
                 if (!(ok = wait_warp(bar(C::B_MF), mc & 1, ctl))) break;
@@ -326,6 +421,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 had2 = __any_sync(kAllLanes, had2);
             } else if (one && x == 1) {
+                unit_done();
                 continue;  // the first chain's warps write the zeros
             }
             if (had) {
@@ -362,10 +458,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = o[k] * f1 + o2[k] * f2;
                     }
-                    float z = 0.f;
+                    float z[4] = {0.f, 0.f, 0.f, 0.f};  // NaN if any is infinite or NaN
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) z = fmaf(o[k], 0.f, z);  // NaN if any is infinite or NaN
-                    bad |= z != 0.f;
+                    for (int k = 0; k < 32; ++k) z[k & 3] = fmaf(o[k], 0.f, z[k & 3]);
+                    bad |= z[0] + z[1] + z[2] + z[3] != 0.f;
                     if (!in || (!row.valid && t >= p.m)) continue;
                     if (U.split) {
 #pragma unroll
@@ -413,26 +509,57 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float2 ml = exact_row<__nv_bfloat16, D>(p, P, U, rt, rh, a);
                 store_exact_row<__nv_bfloat16, D>(p, U, rt, rh, x * half_rows + (warp & 3) * 32 + r, ml, a);
             }
+            unit_done();
         }
     } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    if (warp == 8 || warp == 11) {
-        // ================================================================ K (8) and V (11) loaders
-        const bool is_k = warp == 8;
-        const CUtensorMap *tm = is_k ? &tmK : &tmV;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 8) {
+        // ================================================================ loader of Q, K and V
         const int log_bp = min(p.log_page, 6);  // tokens of a box: a page, at most 64
         const int log_ppb = 6 - log_bp;         // boxes per block and 64-column piece
-        const int nbox = (2 << log_ppb) * C::DC;
+        const int nbox = (2 << log_ppb) * C::DC;  // at most 16 per stage
         const bool big = p.page > 64;
-        // this lane's box of a stage, before the lanes are moved on: a thread's
-        // copies complete one after another, different threads' overlap
         uint32_t qc = 0, turn = 0;
-        uint32_t armed = 0, phase = 0;  // per stage: filled by this warp, and the parity of the last time
-        while (ok && units.next(p, P, U)) {
-            const int n = (U.e1 - U.e0 + 1) >> 1;
-            if (!U.live || n == 0) continue;
-            if (is_k) {
-                if (qc > 0 && !(ok = wait_warp(bar(C::B_QE), (qc - 1) & 1, ctl))) break;
+        uint32_t armed = 0, phase = 0;  // per stage: filled, and the parity of the last time
+        while (ok) {
+            const UnitRec &R = next_unit();
+            if (done) break;
+            const Unit U = R.U;
+            const int n = R.n;
+            unit_done();
+            if (n == 0) continue;
+            // A step's boxes: K on lanes [turn, turn + nbox), V on the nbox after
+            // them, modulo 32; the lanes move on every step, as a thread's copies
+            // complete one after another and different threads' overlap. Each lane
+            // has the coordinates of its box; z = -1 reads zeros.
+            auto look = [&](int i, int &box, int &y) -> int {
+                box = (lane - (int)turn) & 31;
+                const int kb = box < nbox ? box : box - nbox;
+                const int piece = kb / C::DC, e = U.e0 + 2 * i + (piece >> log_ppb);
+                y = 0;
+                if (kb >= nbox || i >= n || e >= U.e1) return -1;
+                const int blk = entry_block(P, U, e);
+                const int pos = (blk << 6) + ((piece & ((1 << log_ppb) - 1)) << log_bp);
+                const int pg = pos < U.s ? page_of(p, U.b, pos) : -1;
+                if (pg < 0) return -1;
+                if (big) y = (blk & 1) * 64;
+                return pg * p.Hkv + U.hk;
+            };
+            auto fill = [&](const CUtensorMap *tm, Pos at, int kb, int y, int z) -> bool {
+                const uint32_t st = at.st;
+                if (at.times > 0 && !wait_warp(bar(C::B_KE + st), (at.times - 1) & 1, ctl)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KF + st), C::TILE);
+                __syncwarp();
+                if (kb >= 0 && kb < nbox)
+                    tma_load_3d(sbase + C::ST_OFF + st * C::TILE + (kb % C::DC) * kRegion + ((kb / C::DC) << log_bp) * 128,
+                                tm, bar(C::B_KF + st), (kb % C::DC) * 64, y, z);
+                armed |= 1u << st;
+                phase = (phase & ~(1u << st)) | ((at.times & 1u) << st);
+                return true;
+            };
+            int box, y, z = look(0, box, y);
+            if (qc > 0 && !(ok = wait_warp(bar(C::B_QE), (qc - 1) & 1, ctl))) break;
+            {
                 const int halves = !one && U.t0 + p.tpt_half < U.q ? 2 : 1;
                 const int bytes = p.tpt_half * p.group * 128;
                 if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QF), (uint32_t)(halves * C::DC * bytes));
@@ -444,54 +571,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 ++qc;
             }
-            // coordinates (y, z) of this lane's box in step i; z = -1 reads zeros
-            auto look = [&](int i, int box, int &y) -> int {
-                const int piece = box / C::DC, e = U.e0 + 2 * i + (piece >> log_ppb);
-                y = 0;
-                if (box >= nbox || i >= n || e >= U.e1) return -1;
-                const int blk = entry_block(P, U, e);
-                const int pos = (blk << 6) + ((piece & ((1 << log_ppb) - 1)) << log_bp);
-                const int pg = pos < U.s ? page_of(p, U.b, pos) : -1;
-                if (pg < 0) return -1;
-                if (big) y = (blk & 1) * 64;
-                return pg * p.Hkv + U.hk;
-            };
-            int y, z, box = (lane - (int)turn) & 31;
-            z = look(0, box, y);
+            int pbox = 0, py = 0, pz = 0;  // the step before, whose V is still to be loaded (one tile)
             for (int i = 0; i < n; ++i) {
-                const uint32_t sidx = is_k ? k_at(g, i) : v_at(g, i, n), st = sidx % C::NST;
-                turn = (turn + nbox) & 31;
-                const int box1 = (lane - (int)turn) & 31;
-                int y1;
-                const int z1 = look(i + 1, box1, y1);  // on its way during this step's wait
-                if (sidx >= C::NST && !(ok = wait_warp(bar(C::B_KE + st), ((sidx / C::NST) - 1) & 1, ctl))) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KF + st), C::TILE);
-                __syncwarp();
-                if (box < nbox)
-                    tma_load_3d(sbase + C::ST_OFF + st * C::TILE + (box % C::DC) * kRegion +
-                                    ((box / C::DC) << log_bp) * 128,
-                                tm, bar(C::B_KF + st), (box % C::DC) * 64, y, z);
-                armed |= 1u << st;
-                phase = (phase & ~(1u << st)) | (((sidx / C::NST) & 1u) << st);
+                turn = (turn + 2 * nbox) & 31;
+                int box1, y1;
+                const int z1 = look(i + 1, box1, y1);  // on its way during this step's waits
+                if (!(ok = fill(&tmK, stage(i, 0), box, y, z))) break;
+                if (one) {
+                    if (i > 0 && !(ok = fill(&tmV, stage(i - 1, 1), pbox - nbox, py, pz))) break;
+                    if (i == n - 1 && !(ok = fill(&tmV, stage(i, 1), box - nbox, y, z))) break;
+                    pbox = box;
+                    py = y;
+                    pz = z;
+                } else if (!(ok = fill(&tmV, stage(i, 1), box - nbox, y, z))) {
+                    break;
+                }
                 box = box1;
                 y = y1;
                 z = z1;
             }
-            g += n;
+            unit_steps(n);
         }
-        if (!ok) {  // abort: wait for this warp's copies still in flight
+        if (!ok) {  // abort: wait for the copies still in flight
             for (int i = 0; i < C::NST; ++i)
                 if ((armed >> i) & 1u) wait_drain(bar(C::B_KF + i), (phase >> i) & 1u);
-            if (is_k && qc) wait_drain(bar(C::B_QF), (qc - 1) & 1);
+            if (qc) wait_drain(bar(C::B_QF), (qc - 1) & 1);
         }
     } else if (warp == 10) {
         // ================================================================ step records
         // What each step holds for the tiles, ahead of their use. Lane l looks
         // up piece l % ppb of entry l / ppb.
         const int log_bp = min(p.log_page, 6), log_ppb = 6 - log_bp, ppb = 1 << log_ppb;
-        while (ok && units.next(p, P, U)) {
-            const int n = (U.e1 - U.e0 + 1) >> 1;
-            if (!U.live || n == 0) continue;
+        Units units(p, P, blockIdx.x);
+        Unit U;
+        for (bool more = true; ok && more; ++uc) {
+            more = units.next(p, P, U);
+            const int n = more && U.live ? (U.e1 - U.e0 + 1) >> 1 : 0;
+            const uint32_t us = uc % kNU;
+            if (uc >= kNU && !(ok = wait_warp(bar(C::B_UE + us), ((uc / kNU) - 1) & 1, ctl))) break;
+            if (lane == 0) {
+                if (more) unit_recs[us].U = U;
+                unit_recs[us].n = n;
+                unit_recs[us].end = !more;
+                mbar_arrive(bar(C::B_UF + us));
+            }
+            __syncwarp();
+            if (n == 0) continue;
             const int stride = p.dilation ? P.hstride[U.hk] : 1;
             const TileSpan sp0 = tile_span(p, P, U, 0, stride), sp1 = tile_span(p, P, U, 1, stride);
             auto look = [&](int i, int &blk) -> int {
@@ -522,8 +647,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (sp1.live && j0 <= sp1.p1 && (j0 + 63 >= sp1.first || gb)) use |= 2;
                     written = max(min(U.s - j0, 64), 0);  // keys of the block that hold tokens
                 }
+                // "plain": rows see an interval of the block's keys and no others
+                int all = stride == 1 && gb == 0ull && (b < 0 || (w | ~low_bits(written)) == ~0ull) ? 16 : 0;
                 const bool whole = stride == 1 && w == ~0ull;
-                int all = 0;
                 if (whole && j0 + 63 <= sp0.p0 && j0 >= sp0.last) all |= 4;
                 if (whole && j0 + 63 <= sp1.p0 && j0 >= sp1.last) all |= 8;
                 const int use2 = use | __shfl_xor_sync(kAllLanes, use, 1);
@@ -532,11 +658,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (g >= kSI && !(ok = wait_warp(bar(C::B_IE + slot), ((g / kSI) - 1) & 1, ctl))) break;
                 if (lane < 2) {
                     StepRec &r = recs[slot];
-                    r.blk[lane] = b;
+                    r.j0[lane] = b < 0 ? kNowhere : j0;
                     r.gbits[lane] = gb;
                     r.present[lane] = w;
                     if (lane == 0) {
-                        r.use = one ? ((use2 & 1) << (i & 1)) | ((all2 & 4) ? 12 : 0) : use2 | all2;
+                        r.use = one ? ((use2 & 1) << (i & 1)) | ((all2 & 4) ? 12 : 0) | (all2 & 16) : use2 | all2;
                         // only the last block of a sequence holds unwritten keys
                         r.vz0 = written < 64 ? written : 64 + written2;
                         r.vz1 = written < 64 ? 64 : 128;
@@ -548,131 +674,108 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 pg = npg;
             }
         }
-    } else if (warp == 9) {
-        // ================================================================ MMA issuer
-        constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false);
-        constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
+    } else {
+        // ================================================================ MMA issuers: warp 9 for tile (or chain) 0, 11 for 1
         // The whole warp runs the loop and the waits, so descriptors and TMEM
         // addresses stay warp-uniform; one elected lane issues the MMAs and the
         // commits that track them.
+        constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false);
+        constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
+        const int x = (warp - 9) >> 1;
         const bool leader = elect_one();
-        const uint64_t dQ0 = desc_sw128(sbase + C::Q_OFF, 16);
+        const uint64_t dQ = desc_sw128(sbase + C::Q_OFF + (one ? 0 : x) * C::TILE, 16);
         const uint64_t dK0 = desc_sw128(sbase + C::ST_OFF, 16);
         const uint64_t dV0 = desc_sw128(sbase + C::ST_OFF, kRegion);
-        uint32_t qc = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
-        auto filled = [&](uint32_t sidx) {
-            return wait_warp(bar(C::B_KF + sidx % C::NST), (sidx / C::NST) & 1, ctl);
-        };
-        // tiles that use step gs; waits for its record
-        auto step_use = [&](uint32_t gs, int &use) -> bool {
-            const uint32_t slot = gs % kSI;
-            if (!wait_warp(bar(C::B_IF + slot), (gs / kSI) & 1, ctl)) return false;
-            use = recs[slot].use & 3;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
-            return true;
-        };
-        while (ok && units.next(p, P, U)) {
-            const int n = (U.e1 - U.e0 + 1) >> 1;
-            if (!U.live || n == 0) continue;
-            int use = 0, next_use = 0;
-            if (!(ok = step_use(g, next_use))) break;
+        const uint32_t s_col = tmem + x * 128, o_col = tmem + C::O_COL + x * D;
+        const uint32_t b_sf = bar(C::B_SF + x), b_pf = bar(C::B_PF + 2 * x);
+        uint32_t qc = 0, pc = 0, oc = 0;
+        auto filled = [&](Pos at) { return wait_warp(bar(C::B_KF + at.st), at.times & 1, ctl); };
+        while (ok) {
+            const int n = next_unit().n;
+            if (done) break;
+            unit_done();
+            if (n == 0) continue;
             if (!(ok = wait_warp(bar(C::B_QF), qc & 1, ctl))) break;
             ++qc;
-            const uint32_t g0 = g;
-            int prev = 0;        // tiles whose P of the step before is to be used
-            int started = 0;     // tiles with a product in O already
-            // S_X = Q_X K^T with the K of ring position kx
-            auto scores = [&](auto X, uint32_t kx) {
-                constexpr int x = decltype(X)::value;
-                tc_fence_after();
-                if (leader) {
-                    const uint64_t dQ = one ? dQ0 : dQ0 + (uint64_t)((x * C::TILE) >> 4);
-                    const uint64_t dK = dK0 + (uint64_t)(((kx % C::NST) * C::TILE) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
-                        mma_bf16_ss(tmem + x * 128, dQ + off, dK + off, idesc_qk, kk > 0 ? 1u : 0u);
-                    }
-                    mma_commit(bar(C::B_SF + x));
-                }
-                __syncwarp();
-            };
-            // O_X (+)= P_X V with the V of ring position vx: 64 keys as soon as their weights are there
-            auto weigh = [&](auto X, uint32_t vx) -> bool {
-                constexpr int x = decltype(X)::value;
-                const bool first = !((started >> x) & 1);
-                if (first && oc[x] > 0 && !wait_warp(bar(C::B_OE + x), (oc[x] - 1) & 1, ctl)) return false;
-                const uint64_t dV = dV0 + (uint64_t)(((vx % C::NST) * C::TILE) >> 4);
+            bool started = false;
+            int pend = -1;  // step whose weights are to be used
+            // O (+)= P V of the pending step: 64 keys as soon as their weights are there
+            auto weigh = [&]() -> bool {
+                const Pos vx = stage(pend, 1);
+                if (!started && oc > 0 && !wait_warp(bar(C::B_OE + x), (oc - 1) & 1, ctl)) return false;
+                if (!filled(vx)) return false;
+                const uint64_t dV = dV0 + (uint64_t)((vx.st * C::TILE) >> 4);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (!wait_warp(bar(C::B_PF + 2 * x + h), pc[x] & 1, ctl)) return false;
+                    if (!wait_warp(b_pf + 8 * h, pc & 1, ctl)) return false;
                     tc_fence_after();
                     if (leader) {
 #pragma unroll
                         for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                            mma_bf16_ts(tmem + C::O_COL + x * D, tmem + x * 128 + kk * 8,
-                                        dV + (uint64_t)((kk * 2048) >> 4), idesc_pv, (first && kk == 0) ? 0u : 1u);
+                            mma_bf16_ts(o_col, s_col + kk * 8, dV + (uint64_t)((kk * 2048) >> 4), idesc_pv,
+                                        (!started && kk == 0) ? 0u : 1u);
+                        if (h == 1) mma_commit(bar(C::B_KE + vx.st));
                     }
                     __syncwarp();
                 }
-                ++pc[x];
-                started |= 1 << x;
+                ++pc;
+                started = true;
+                pend = -1;
                 return true;
             };
-            auto release = [&](uint32_t sidx) {
-                if (leader) mma_commit(bar(C::B_KE + sidx % C::NST));
-                __syncwarp();
-            };
-            const std::integral_constant<int, 0> T0{};
-            const std::integral_constant<int, 1> T1{};
-            for (int i = 0; i <= n; ++i) {
-                use = i < n ? next_use : 0;
-                const uint32_t kx = k_at(g0, i), vx = i > 0 ? v_at(g0, i - 1, n) : 0;
-                if (one) {  // the chains take turns: this step's scores need not wait for the other's weights
-                    if (i < n) {
-                        if (!(ok = filled(kx))) break;
-                        if (use & 1) scores(T0, kx);
-                        if (use & 2) scores(T1, kx);
-                        release(kx);
-                    }
-                    if (i + 1 < n && !(ok = step_use(g + 1, next_use))) break;
-                    if (i > 0) {
-                        if (!(ok = filled(vx))) break;
-                        if ((prev & 1) && !(ok = weigh(T0, vx))) break;
-                        if ((prev & 2) && !(ok = weigh(T1, vx))) break;
-                        release(vx);
-                    }
-                } else {
-                    if (i < n && !(ok = filled(kx))) break;
-                    if (i > 0 && !(ok = filled(vx))) break;
-                    if ((prev & 1) && !(ok = weigh(T0, vx))) break;
-                    if (use & 1) scores(T0, kx);
-                    // while the other tile's softmax works: the next step's record
-                    if (i + 1 < n && !(ok = step_use(g + 1, next_use))) break;
-                    if ((prev & 2) && !(ok = weigh(T1, vx))) break;
-                    if (use & 2) scores(T1, kx);
-                    if (i > 0) release(vx);
-                    if (i < n) release(kx);
+            const int step = one ? 2 : 1;
+            for (int i = one ? x : 0; i < n; i += step) {
+                bool use = true;
+                if (!one) {
+                    const uint32_t gs = g + i, slot = gs % kSI;
+                    if (!(ok = wait_warp(bar(C::B_IF + slot), (gs / kSI) & 1, ctl))) break;
+                    use = (recs[slot].use >> x) & 1;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
                 }
+                if (pend >= 0 && !(ok = weigh())) break;
+                const Pos kx = stage(i, 0);
+                if (!(ok = filled(kx))) break;
+                if (!use) {  // the other tile's alone. (Its stages are filled: an arrival
+                             // cannot be taken for one of the time before.)
+                    const Pos vx = stage(i, 1);
+                    if (!(ok = filled(vx))) break;
+                    if (lane == 0) {
+                        mbar_arrive(bar(C::B_KE + kx.st));
+                        mbar_arrive(bar(C::B_KE + vx.st));
+                    }
+                    __syncwarp();
+                    continue;
+                }
+                tc_fence_after();
                 if (leader) {
-                    if (i == n - 1) mma_commit(bar(C::B_QE));
-                    if (i == n) {
-                        if (started & 1) mma_commit(bar(C::B_OF + 0));
-                        if (started & 2) mma_commit(bar(C::B_OF + 1));
+                    const uint64_t dK = dK0 + (uint64_t)((kx.st * C::TILE) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
+                        mma_bf16_ss(s_col, dQ + off, dK + off, idesc_qk, kk > 0 ? 1u : 0u);
                     }
+                    mma_commit(b_sf);
+                    mma_commit(bar(C::B_KE + kx.st));
                 }
                 __syncwarp();
-                prev = use;
-                if (i < n) ++g;
+                pend = i;
             }
-            oc[0] += started & 1;
-            oc[1] += (started >> 1) & 1;
+            if (!ok) break;
+            if (leader) mma_commit(bar(C::B_QE));
+            __syncwarp();
+            if (pend >= 0 && !(ok = weigh())) break;
+            if (started) {
+                if (leader) mma_commit(bar(C::B_OF + x));
+                __syncwarp();
+                ++oc;
+            }
+            unit_steps(n);
         }
         // every MMA issued has completed once this arrives
-        if (leader) mma_commit(bar(C::B_DRAIN));
+        if (leader) mma_commit(bar(C::B_DRAIN + x));
         __syncwarp();
-        wait_drain(bar(C::B_DRAIN), 0);
+        wait_drain(bar(C::B_DRAIN + x), 0);
     }
     }
     __syncwarp();
