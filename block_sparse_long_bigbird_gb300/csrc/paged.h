@@ -43,7 +43,7 @@ struct PagedProblem {
     int cost;        // what a tile costs beside its blocks, in blocks
     float scale_log2;
     unsigned long long wait_ns;
-    float *part_o;   // [2 slots][rows][d] partial sums of split tiles
+    float *part_o;   // [2 slots][d / 4][rows][4] partial sums of split tiles
     float2 *part_ml; // [2 slots][rows] (running maximum, sum)
 };
 

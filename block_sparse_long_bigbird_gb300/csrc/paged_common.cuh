@@ -494,6 +494,13 @@ __device__ __noinline__ float2 exact_row(const PagedProblem &p, const Plan &P, c
     return make_float2(m, l);
 }
 
+// Where elements [4 k, 4 k + 4) of a row's partial sums lie: rows side by side, so
+// that threads that hold a row each write whole lines.
+template <int D>
+__device__ __forceinline__ size_t part_at(const PagedProblem &p, int slot, int k, int row) {
+    return (((size_t)slot * (D / 4) + k) * p.rows + row) * 4;
+}
+
 // Stores what exact_row returned: the finished row, or its split's partial.
 template <typename T, int D>
 __device__ __forceinline__ void store_exact_row(const PagedProblem &p, const Unit &U, int t, int head, int row,
@@ -501,10 +508,10 @@ __device__ __forceinline__ void store_exact_row(const PagedProblem &p, const Uni
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     if (U.split) {
-        const size_t at = (size_t)U.slot * p.rows + row;
 #pragma unroll
-        for (int i = 0; i < E; ++i) p.part_o[at * D + lane * E + i] = acc[i];
-        if (lane == 0) p.part_ml[at] = ml;
+        for (int i = 0; i < E; ++i)
+            p.part_o[part_at<D>(p, U.slot, (lane * E + i) >> 2, row) + ((lane * E + i) & 3)] = acc[i];
+        if (lane == 0) p.part_ml[(size_t)U.slot * p.rows + row] = ml;
     } else {
         T *O = static_cast<T *>(p.O) + (((size_t)U.b * p.Hq + head) * p.m + t) * D + lane * E;
         const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;

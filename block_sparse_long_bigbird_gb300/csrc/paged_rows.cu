@@ -230,9 +230,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) 
             int t, head;
             row_token(p, U, r, p.tpt, t, head);
             if (U.split) {
-                const size_t slot = (size_t)U.slot * p.rows + r;
-                p.part_o[slot * D + x] = a;
-                if (x == 0) p.part_ml[slot] = make_float2(mx, ls);
+                p.part_o[part_at<D>(p, U.slot, x >> 2, r) + (x & 3)] = a;
+                if (x == 0) p.part_ml[(size_t)U.slot * p.rows + r] = make_float2(mx, ls);
             } else if (t < p.m) {
                 static_cast<T *>(p.O)[(((size_t)U.b * p.Hq + head) * p.m + t) * D + x] =
                     from_float<T>(ls == 0.f ? 0.f : a / ls);
@@ -244,33 +243,65 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) 
 
 // Joins the partial results of split tiles, piece by piece in order. A work item
 // is a boundary between two CTAs (a tile belongs to the first boundary inside
-// it) and kMergeRows rows of its tile. Tiles of few pieces: a warp per row.
-// Tiles of many (few rows against a long cache): the four warps share a row's
-// pieces. Launched so that its plan is computed while the sweeps still run.
-constexpr int kMergeWarps = 4, kMergeRows = 16, kMergeMany = 12;
+// it) and a share of its tile's groups of sixteen elements; a thread takes a
+// group. Where a tile is cut into many pieces (few rows against a long cache)
+// kMergeShare threads take a group, each a stretch of the pieces. Launched so
+// that its plan is computed while the sweeps still run.
+constexpr int kMergeThreads = 128, kMergeShare = 8, kMergeMany = 12;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge(const PagedProblem p) {
-    constexpr int E = D / 32;
+__global__ void __launch_bounds__(kMergeThreads) paged_merge(const PagedProblem p, int per_tile) {
     extern __shared__ __align__(16) uint8_t smem[];
-    float *jl = reinterpret_cast<float *>(smem);  // [warp]
-    float *ja = jl + 2 * kMergeWarps;             // [warp][D]
-    Plan P = plan_at(ja + kMergeWarps * D, p.B, p.ng, p.Hkv);
+    Plan P = plan_at(smem, p.B, p.ng, p.Hkv);
     make_plan(p, P);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the sweeps' results are visible from here on
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int chunks = (p.rows + kMergeRows - 1) / kMergeRows;
+    const int groups = p.rows * (D / 16);
     const int half_rows = p.tpt_half * p.group;
-    const long long n_items = (long long)(P.ctas - 1) * chunks;
+    const long long n_items = (long long)(P.ctas - 1) * per_tile;
     for (long long w = blockIdx.x; w < n_items; w += gridDim.x) {
-        const int c = 1 + (int)(w / chunks), row0 = (int)(w % chunks) * kMergeRows;
+        const int c = 1 + (int)(w / per_tile), chunk = (int)(w % per_tile);
         const long long at = cta_begin(P, c);
         const Tile tile = find_tile(p, P, at);
         if (!tile.live || tile.begin == at || tile.begin < cta_begin(P, c - 1)) continue;
         const int ns = cta_of(P, tile.end - 1) - c + 2;  // pieces: slot 2 c - 1, then 2 c, 2 c + 2, ...
-        const bool many = ns > kMergeMany;
-        const int step = many ? 1 : kMergeWarps;
-        for (int row = row0 + (many ? 0 : warp); row < min(row0 + kMergeRows, p.rows); row += step) {
+        const int share = ns > kMergeMany ? kMergeShare : 1;
+        auto slot = [&](int k) { return k == 0 ? 2 * c - 1 : 2 * (c + k - 1); };
+        for (int idx = chunk * kMergeThreads + (int)threadIdx.x; idx - (int)threadIdx.x < groups * share;
+             idx += per_tile * kMergeThreads) {
+            const int gi = idx / share, part = idx % share;  // the threads that share a group are neighbours
+            const bool in = gi < groups;
+            const int row = in ? gi % p.rows : 0, k16 = in ? gi / p.rows : 0;
+            float mx = -CUDART_INF_F;
+            for (int k = part; k < ns; k += share) mx = fmaxf(mx, p.part_ml[(size_t)slot(k) * p.rows + row].x);
+            for (int o = 1; o < share; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, o));
+            const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+            float l = 0.f, acc[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+            const int k0 = ns * part / share, k1 = ns * (part + 1) / share;
+#pragma unroll 2
+            for (int k = k0; k < k1; ++k) {
+                const float2 y = p.part_ml[(size_t)slot(k) * p.rows + row];
+                float4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = *reinterpret_cast<const float4 *>(p.part_o + part_at<D>(p, slot(k), 4 * k16 + i, row));
+                const float f = ptx::ex2(y.x - ref);
+                l = fmaf(y.y, f, l);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[4 * i] = fmaf(v[i].x, f, acc[4 * i]);
+                    acc[4 * i + 1] = fmaf(v[i].y, f, acc[4 * i + 1]);
+                    acc[4 * i + 2] = fmaf(v[i].z, f, acc[4 * i + 2]);
+                    acc[4 * i + 3] = fmaf(v[i].w, f, acc[4 * i + 3]);
+                }
+            }
+            for (int o = 1; o < share; o <<= 1) {
+                l += __shfl_xor_sync(kAllLanes, l, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] += __shfl_xor_sync(kAllLanes, acc[i], o);
+            }
+            if (!in || part != 0) continue;
             // the two halves of a unit hold different tokens
             Unit U;
             const int x = row / half_rows;
@@ -279,45 +310,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge(const PagedProbl
             int t, head;
             row_token(p, U, row - x * half_rows, p.tpt_half, t, head);
             if (t >= p.m) continue;
-            auto slot = [&](int k) { return (size_t)(k == 0 ? 2 * c - 1 : 2 * (c + k - 1)) * p.rows + row; };
-            float mx = -CUDART_INF_F;
-            for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, p.part_ml[slot(k)].x);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAllLanes, mx, o));
-            const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-            float l = 0.f, acc[E];
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = 0.f;
-            const int k0 = many ? ns * warp / kMergeWarps : 0, k1 = many ? ns * (warp + 1) / kMergeWarps : ns;
-#pragma unroll 4
-            for (int k = k0; k < k1; ++k) {
-                const size_t sl = slot(k);
-                const float2 y = p.part_ml[sl];
-                const float f = ptx::ex2(y.x - ref);
-                l = fmaf(y.y, f, l);
-                const float *src = p.part_o + sl * D + lane * E;
-#pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] = fmaf(src[i], f, acc[i]);
-            }
-            if (many) {
-                __syncthreads();  // the row before has been read
-#pragma unroll
-                for (int i = 0; i < E; ++i) ja[warp * D + lane * E + i] = acc[i];
-                if (lane == 0) jl[warp] = l;
-                __syncthreads();
-                if (warp != 0) continue;
-                l = jl[0];
-#pragma unroll
-                for (int k = 1; k < kMergeWarps; ++k) {
-                    l += jl[k];
-#pragma unroll
-                    for (int i = 0; i < E; ++i) acc[i] += ja[k * D + lane * E + i];
-                }
-            }
-            T *O = static_cast<T *>(p.O) + (((size_t)tile.b * p.Hq + head) * p.m + t) * D + lane * E;
             const bool zero = t >= tile.q || l == 0.f;
+            __align__(16) T o[16];
 #pragma unroll
-            for (int i = 0; i < E; ++i) O[i] = from_float<T>(zero ? 0.f : acc[i] / l);
+            for (int i = 0; i < 16; ++i) o[i] = from_float<T>(zero ? 0.f : acc[i] / l);
+            uint4 *O = reinterpret_cast<uint4 *>(static_cast<T *>(p.O) +
+                                                 (((size_t)tile.b * p.Hq + head) * p.m + t) * D + 16 * k16);
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); ++i) O[i] = reinterpret_cast<const uint4 *>(o)[i];
         }
     }
 }
@@ -353,15 +353,19 @@ cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, cudaStream_
 }
 
 cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream) {
-    const size_t smem = (size_t)kMergeWarps * (p.d + 2) * 4 + plan_bytes(p.B, p.ng, p.Hkv);
-    void (*kern)(const PagedProblem) =
+    const size_t smem = plan_bytes(p.B, p.ng, p.Hkv);
+    void (*kern)(const PagedProblem, int) =
         dtype == SA_FP32 ? (p.d == 64 ? paged_merge<float, 64> : paged_merge<float, 128>)
                          : (p.d == 64 ? paged_merge<__nv_bfloat16, 64> : paged_merge<__nv_bfloat16, 128>);
     // no more shared memory than a kernel has without asking: the largest plan takes 29 KB
-    const long long items = (long long)p.slots * ((p.rows + kMergeRows - 1) / kMergeRows), grid = 8ll * num_sms;
+    // CTAs per tile: as many as its groups keep busy, within what fits the GPU at a time
+    const long long busy = ((long long)p.rows * (p.d / 16) + kMergeThreads - 1) / kMergeThreads;
+    long long per_tile = 8ll * num_sms / p.slots;
+    per_tile = per_tile > busy ? busy : per_tile < 1 ? 1 : per_tile;
+    const long long items = per_tile * p.slots, grid = 8ll * num_sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items < grid ? items : grid));
-    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
@@ -369,7 +373,7 @@ cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sm
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, p, (int)per_tile);
 }
 
 }  // namespace sa

@@ -12,11 +12,13 @@
 //     two tiles. The pool is {d, page, num_pages * Hkv}, a box is 64 columns of
 //     one page (at most 64 tokens). A missing page is loaded from coordinate
 //     -1, which fills with zeros, so stages always fill.
-//   * An MMA warp per tile runs S_x = Q_x K^T into 128 TMEM columns and
-//     O_x += P_x V with P_x read from TMEM, where the softmax wrote it (bf16)
-//     over the first half of S_x. One thread issues a tile's MMAs, so they
-//     complete in order: S_x of a step complete means P_x V of the step before
-//     is too.
+//   * An MMA warp per tile runs S_x = Q_x K^T into two slots of 64 TMEM columns,
+//     a half step each, and O_x += P_x V with P_x read from TMEM, where the
+//     softmax wrote it (bf16) over its S slot. One thread issues a tile's MMAs,
+//     so they complete in order. While the softmax works on one half, the MMAs
+//     use the other's weights and fill its slot again: with one slot of 128
+//     columns both waited for each other (a step of two tiles took 3700 clocks
+//     at d = 64, of which the MMAs need 1024).
 //   * A warpgroup per tile runs the softmax, one thread per row: masks, running
 //     maximum (kept until it grows by more than 2^8, then O is rescaled in
 //     place), weights and their sum in fp32, P rounded to bf16 (relative 2^-8,
@@ -72,7 +74,7 @@ struct TcCfg {
     static constexpr int ST_OFF = 2 * TILE;
     static constexpr int BAR_OFF = ST_OFF + NST * TILE;
     static constexpr int B_KF = 0, B_KE = B_KF + NST, B_IF = B_KE + NST, B_IE = B_IF + kSI, B_QF = B_IE + kSI,
-                         B_QE = B_QF + 1, B_SF = B_QE + 1, B_PF = B_SF + 2, B_OF = B_PF + 4, B_OE = B_OF + 2,
+                         B_QE = B_QF + 1, B_SF = B_QE + 1, B_PF = B_SF + 4, B_PD = B_PF + 4, B_OF = B_PD + 2, B_OE = B_OF + 2,
                          B_MF = B_OE + 2, B_ME = B_MF + 1, B_UF = B_ME + 1, B_UE = B_UF + kNU, B_DRAIN = B_UE + kNU, B_COUNT = B_DRAIN + 2;
     static constexpr int REC_OFF = (BAR_OFF + B_COUNT * 8 + 15) & ~15;
     static constexpr int UNIT_OFF = REC_OFF + kSI * (int)sizeof(StepRec);
@@ -147,7 +149,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(bar(C::B_QF), 1);
         mbar_init(bar(C::B_QE), 2);
         for (int x = 0; x < 2; ++x) {
-            mbar_init(bar(C::B_SF + x), 1);
+            mbar_init(bar(C::B_SF + 2 * x), 1);
+            mbar_init(bar(C::B_SF + 2 * x + 1), 1);
+            mbar_init(bar(C::B_PD + x), 1);
             mbar_init(bar(C::B_PF + 2 * x), 4);
             mbar_init(bar(C::B_PF + 2 * x + 1), 4);
             mbar_init(bar(C::B_OF + x), 1);
@@ -229,6 +233,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int my_g = tid / p.tpt_half, my_t = tid - my_g * p.tpt_half + (one ? 0 : x * p.tpt_half);
         const bool in = tid < half_rows;
         uint32_t sc = 0, oc = 0, oc2 = 0, mc = 0;
+        uint32_t handed = 0;  // halves whose weights were handed over
         while (ok) {
             const UnitRec &R = next_unit();
             if (done) break;
@@ -271,92 +276,99 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
                 if (!((use >> x) & 1)) continue;
-                if (!(ok = wait_warp(bar(C::B_SF + x), sc & 1, ctl))) break;
-                ++sc;
-                // Unwritten memory: no NaN may meet a zero weight. (Not before S is
-                // there: only then are the products that read what the stage held
-                // before complete, and the wait below is for this step's V.)
-                if (vz0 < vz1) {
-                    const Pos v_at = stage(i, 1);
-                    if (!(ok = wait_warp(bar(C::B_KF + v_at.st), v_at.times & 1, ctl))) break;
-                    uint8_t *v = smem + C::ST_OFF + v_at.st * C::TILE;
-                    for (int c = tid; c < (vz1 - vz0) * 8 * C::DC; c += 128) {
-                        const int r = vz0 + c / (8 * C::DC), q = c % (8 * C::DC);
-                        *reinterpret_cast<uint4 *>(v + (q >> 3) * kRegion + r * 128 + (q & 7) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                }
-                if (busy) {
-                    tc_fence_after();
-                    // 32 keys that no row of the warp sees need no exponentials,
-                    // those that all see need no masks
-                    int some = 15, full = 15;
-                    if (!all) {
-                        some = full = 0;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (__any_sync(kAllLanes, w[c] != 0u)) some |= 1 << c;
-                            if (__all_sync(kAllLanes, w[c] == ~0u || !row.valid)) full |= 1 << c;
-                        }
-                    }
-                    float s[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, s[c]);
-                    tmem_wait_ld();
-                    float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                    if (full == 15) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) mx4[c] = fmax3(mx4[c], s[c][k], s[c][k + 1]);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (!((some >> c) & 1)) continue;
-                            if (!((full >> c) & 1)) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) s[c][k] = (w[c] >> k) & 1u ? s[c][k] : -CUDART_INF_F;
-                            }
-                            float m0 = -CUDART_INF_F, m1 = m0;
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                m0 = fmax3(m0, s[c][k], s[c][k + 1]);
-                                m1 = fmax3(m1, s[c][k + 2], s[c][k + 3]);
-                            }
-                            mx4[c] = fmaxf(m0, m1);
-                        }
-                    }
-                    float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
-                    mx = row.valid ? mx * sl2 : -CUDART_INF_F;
-                    const bool grow = mx > mref + kGrow || (mref == -CUDART_INF_F && mx > mref);
-                    if (__any_sync(kAllLanes, grow)) {
-                        const float ref = grow ? mx : mref;
-                        const float f = grow ? ex2(mref - ref) : 1.f;  // 0 the first time
-                        l *= f;
-                        mref = ref;
-                        if (had) {
+                // The step's two 64-key halves: while one half's weights are worked
+                // out, the other's product and the next scores run. (Not unrolled:
+                // a loop body that the instruction caches of the schedulers hold
+                // is worth more than anything else here. Unrolled, the warps
+                // waited for instructions 3.9 clocks per issue.)
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                float o[32];
-                                tmem_ld32(o_addr + c * 32, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= f;
-                                tmem_st32(o_addr + c * 32, o);
-                            }
-                            tmem_wait_st();
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w0 = h ? w[2] : w[0], w1 = h ? w[3] : w[1];
+                    if (!(ok = wait_warp(bar(C::B_SF + 2 * x + h), sc & 1, ctl))) break;
+                    // Unwritten memory: no NaN may meet a zero weight. (Not before S
+                    // is there: only then are the fills of what the stage held before
+                    // complete, and the wait below is for this step's V.)
+                    if (h == 0 && vz0 < vz1) {
+                        const Pos v_at = stage(i, 1);
+                        if (!(ok = wait_warp(bar(C::B_KF + v_at.st), v_at.times & 1, ctl))) break;
+                        uint8_t *v = smem + C::ST_OFF + v_at.st * C::TILE;
+                        for (int c = tid; c < (vz1 - vz0) * 8 * C::DC; c += 128) {
+                            const int r = vz0 + c / (8 * C::DC), q = c % (8 * C::DC);
+                            *reinterpret_cast<uint4 *>(v + (q >> 3) * kRegion + r * 128 + (q & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
                         }
+                        fence_proxy_async_smem();
                     }
-                    const float nref = mref == -CUDART_INF_F ? 0.f : -mref;
-                    const uint64_t sl2x2 = f2_pack(sl2, sl2), nrefx2 = f2_pack(nref, nref);
-                    uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+                    if (busy) {
+                        tc_fence_after();
+                        // 32 keys that no row of the warp sees need no exponentials,
+                        // those that all see need no masks
+                        int some = 3, full = 3;
+                        if (!all) {
+                            some = full = 0;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t wc = c ? w1 : w0;
+                                if (__any_sync(kAllLanes, wc != 0u)) some |= 1 << c;
+                                if (__all_sync(kAllLanes, wc == ~0u || !row.valid)) full |= 1 << c;
+                            }
+                        }
+                        float s[2][32];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + h * 64 + c * 32, s[c]);
+                        tmem_wait_ld();
+                        if (full != 3) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t wc = c ? w1 : w0;
+                                if (!((full >> c) & 1)) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) s[c][k] = (wc >> k) & 1u ? s[c][k] : -CUDART_INF_F;
+                                }
+                            }
+                        }
+                        float m4[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(s[k >> 1][2 * (k & 1)], s[k >> 1][2 * (k & 1) + 1]);
+#pragma unroll
+                        for (int k = 4; k < 32; k += 4) {
+                            m4[0] = fmax3(m4[0], s[0][k], s[0][k + 1]);
+                            m4[1] = fmax3(m4[1], s[0][k + 2], s[0][k + 3]);
+                            m4[2] = fmax3(m4[2], s[1][k], s[1][k + 1]);
+                            m4[3] = fmax3(m4[3], s[1][k + 2], s[1][k + 3]);
+                        }
+                        float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+                        mx = row.valid ? mx * sl2 : -CUDART_INF_F;
+                        const bool grow = mx > mref + kGrow || (mref == -CUDART_INF_F && mx > mref);
+                        if (__any_sync(kAllLanes, grow)) {
+                            const float ref = grow ? mx : mref;
+                            const float f = grow ? ex2(mref - ref) : 1.f;  // 0 the first time
+                            l *= f;
+                            mref = ref;
+                            if (had) {
+                                // the last product handed over may still be running (S of
+                                // this half shows only the one before it complete)
+                                if (!(ok = wait_warp(bar(C::B_PD + x), (handed - 1) & 1, ctl))) break;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D / 32; ++c) {
+                                    float o[32];
+                                    tmem_ld32(o_addr + c * 32, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) o[k] *= f;
+                                    tmem_st32(o_addr + c * 32, o);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                        const float nref = mref == -CUDART_INF_F ? 0.f : -mref;
+                        const uint64_t sl2x2 = f2_pack(sl2, sl2), nrefx2 = f2_pack(nref, nref);
+                        uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
                         uint32_t pk[32];
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            if (!((some >> (2 * h + c)) & 1)) {
+                            if (!((some >> c) & 1)) {
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) pk[c * 16 + k] = 0u;
                                 continue;
@@ -364,7 +376,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
                                 float a, e;
-                                f2_unpack(f2_fma(f2_pack(s[2 * h + c][k], s[2 * h + c][k + 1]), sl2x2, nrefx2), a, e);
+                                f2_unpack(f2_fma(f2_pack(s[c][k], s[c][k + 1]), sl2x2, nrefx2), a, e);
                                 a = ex2(a);
                                 e = ex2(e);
                                 if (k & 2) sum1 = f2_add(sum1, f2_pack(a, e));
@@ -373,20 +385,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 pk[c * 16 + k / 2] = *reinterpret_cast<const uint32_t *>(&two);
                             }
                         }
-                        tmem_st32u(s_addr + h * 32, pk);
+                        tmem_st32u(s_addr + h * 64, pk);
+                        float a, e;
+                        f2_unpack(f2_add(sum0, sum1), a, e);
+                        l += a + e;
                         tmem_wait_st();
                         tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(C::B_PF + 2 * x + h));
                     }
-                    float a, e;
-                    f2_unpack(f2_add(sum0, sum1), a, e);
-                    l += a + e;
-                } else if (lane == 0) {  // no row of this warp is used: let the others go on
-                    mbar_arrive(bar(C::B_PF + 2 * x));
-                    mbar_arrive(bar(C::B_PF + 2 * x + 1));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_PF + 2 * x + h));
+                    ++handed;
+                    had = true;
                 }
-                had = true;
+                if (!ok) break;
+                ++sc;
             }
             if (!ok) break;
             unit_steps(n);
@@ -438,8 +450,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             bool bad = false;
             const float inv = row.valid && l != 0.f ? 1.f / l : 0.f;
             if (busy || !had) {
-                __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.O) +
-                                      (((size_t)U.b * p.Hq + head) * p.m + (t < p.m ? t : 0)) * D;
+                // where this lane's row goes (-1: nowhere)
+                const long long out_at = in && t < p.m ? (((long long)U.b * p.Hq + head) * p.m + t) * D : -1;
                 const size_t at = (size_t)U.slot * p.rows + prow;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -462,24 +474,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 32; ++k) z[k & 3] = fmaf(o[k], 0.f, z[k & 3]);
                     bad |= z[0] + z[1] + z[2] + z[3] != 0.f;
-                    if (!in || (!row.valid && t >= p.m)) continue;
                     if (U.split) {
+                        if (in) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(p.part_o + at * D + c * 32 + k) =
-                                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                            for (int k = 0; k < 32; k += 4)
+                                *reinterpret_cast<float4 *>(p.part_o + part_at<D>(p, U.slot, c * 8 + k / 4, prow)) =
+                                    make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        }
                     } else {
+                        // Four lanes hold the 64 bytes of four rows each; a 4 x 4
+                        // exchange lets them write one row's 64 bytes together
+                        // instead of 16 bytes of four rows (a quarter of the lines
+                        // per store: the epilogue took 3200 clocks before, of a
+                        // unit's 20000 at window 512).
+                        uint32_t b4[4][4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t b4[4];
+                        for (int q = 0; q < 4; ++q)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const float a = row.valid ? o[q * 8 + 2 * k] * inv : 0.f;
                                 const float e = row.valid ? o[q * 8 + 2 * k + 1] * inv : 0.f;
                                 const __nv_bfloat162 two = __floats2bfloat162_rn(a, e);
-                                b4[k] = *reinterpret_cast<const uint32_t *>(&two);
+                                b4[q][k] = *reinterpret_cast<const uint32_t *>(&two);
                             }
-                            *reinterpret_cast<uint4 *>(orow + c * 32 + q * 8) = make_uint4(b4[0], b4[1], b4[2], b4[3]);
+#pragma unroll
+                        for (int o2 = 1; o2 < 4; o2 <<= 1)  // swap [q][lane] with [lane][q], a bit at a time
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if (q & o2) continue;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const bool up = lane & o2;
+                                    const uint32_t give = up ? b4[q][k] : b4[q | o2][k];
+                                    const uint32_t got = __shfl_xor_sync(kAllLanes, give, o2);
+                                    if (up) b4[q][k] = got; else b4[q | o2][k] = got;
+                                }
+                            }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {  // row (lane & ~3) + q, its 16 bytes number lane & 3
+                            const long long r_at = __shfl_sync(kAllLanes, out_at, (lane & ~3) + q);
+                            if (r_at >= 0)
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.O) + r_at + c * 32 + (lane & 3) * 8) =
+                                    make_uint4(b4[q][0], b4[q][1], b4[q][2], b4[q][3]);
                         }
                     }
                 }
@@ -679,7 +715,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // The whole warp runs the loop and the waits, so descriptors and TMEM
         // addresses stay warp-uniform; one elected lane issues the MMAs and the
         // commits that track them.
-        constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false);
+        constexpr uint32_t idesc_qk = idesc_bf16(128, 64, false);
         constexpr uint32_t idesc_pv = idesc_bf16(128, D, true);
         const int x = (warp - 9) >> 1;
         const bool leader = elect_one();
@@ -687,7 +723,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint64_t dK0 = desc_sw128(sbase + C::ST_OFF, 16);
         const uint64_t dV0 = desc_sw128(sbase + C::ST_OFF, kRegion);
         const uint32_t s_col = tmem + x * 128, o_col = tmem + C::O_COL + x * D;
-        const uint32_t b_sf = bar(C::B_SF + x), b_pf = bar(C::B_PF + 2 * x);
+        const uint32_t b_sf = bar(C::B_SF + 2 * x), b_pf = bar(C::B_PF + 2 * x);
         uint32_t qc = 0, pc = 0, oc = 0;
         auto filled = [&](Pos at) { return wait_warp(bar(C::B_KF + at.st), at.times & 1, ctl); };
         while (ok) {
@@ -699,28 +735,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++qc;
             bool started = false;
             int pend = -1;  // step whose weights are to be used
-            // O (+)= P V of the pending step: 64 keys as soon as their weights are there
-            auto weigh = [&]() -> bool {
-                const Pos vx = stage(pend, 1);
-                if (!started && oc > 0 && !wait_warp(bar(C::B_OE + x), (oc - 1) & 1, ctl)) return false;
-                if (!filled(vx)) return false;
+            // By halves of 64 keys: O (+)= P V of the pending step (`pend`) as soon
+            // as the half's weights are there, then the scores of step i, whose S
+            // takes their place. So a tile's softmax finds the next scores ready.
+            auto halves = [&](int i, bool scores) -> bool {
+                Pos vx = {0, 0}, kx = {0, 0};
+                if (scores) {
+                    kx = stage(i, 0);
+                    if (!filled(kx)) return false;
+                }
+                if (pend >= 0) {
+                    vx = stage(pend, 1);
+                    if (!started && oc > 0 && !wait_warp(bar(C::B_OE + x), (oc - 1) & 1, ctl)) return false;
+                    if (!filled(vx)) return false;
+                }
                 const uint64_t dV = dV0 + (uint64_t)((vx.st * C::TILE) >> 4);
-#pragma unroll
+                const uint64_t dK = dK0 + (uint64_t)((kx.st * C::TILE) >> 4);
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    if (!wait_warp(b_pf + 8 * h, pc & 1, ctl)) return false;
+                    if (pend >= 0 && !wait_warp(b_pf + 8 * h, pc & 1, ctl)) return false;
                     tc_fence_after();
                     if (leader) {
+                        if (pend >= 0) {
 #pragma unroll
-                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                            mma_bf16_ts(o_col, s_col + kk * 8, dV + (uint64_t)((kk * 2048) >> 4), idesc_pv,
-                                        (!started && kk == 0) ? 0u : 1u);
-                        if (h == 1) mma_commit(bar(C::B_KE + vx.st));
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_bf16_ts(o_col, s_col + h * 64 + kk * 8, dV + (uint64_t)(((4 * h + kk) * 2048) >> 4),
+                                            idesc_pv, (!started && h == 0 && kk == 0) ? 0u : 1u);
+                            mma_commit(bar(C::B_PD + x));
+                            if (h == 1) mma_commit(bar(C::B_KE + vx.st));
+                        }
+                        if (scores) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint64_t off = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
+                                mma_bf16_ss(s_col + h * 64, dQ + off, dK + off + (uint64_t)((h * 8192) >> 4), idesc_qk,
+                                            kk > 0 ? 1u : 0u);
+                            }
+                            mma_commit(b_sf + 8 * h);
+                            if (h == 1) mma_commit(bar(C::B_KE + kx.st));
+                        }
                     }
                     __syncwarp();
                 }
-                ++pc;
-                started = true;
-                pend = -1;
+                if (pend >= 0) {
+                    ++pc;
+                    started = true;
+                }
+                pend = scores ? i : -1;
                 return true;
             };
             const int step = one ? 2 : 1;
@@ -733,38 +794,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_IE + slot));
                 }
-                if (pend >= 0 && !(ok = weigh())) break;
-                const Pos kx = stage(i, 0);
-                if (!(ok = filled(kx))) break;
+                if ((use || pend >= 0) && !(ok = halves(i, use))) break;
                 if (!use) {  // the other tile's alone. (Its stages are filled: an arrival
                              // cannot be taken for one of the time before.)
-                    const Pos vx = stage(i, 1);
-                    if (!(ok = filled(vx))) break;
+                    const Pos kx = stage(i, 0), vx = stage(i, 1);
+                    if (!(ok = filled(kx)) || !(ok = filled(vx))) break;
                     if (lane == 0) {
                         mbar_arrive(bar(C::B_KE + kx.st));
                         mbar_arrive(bar(C::B_KE + vx.st));
                     }
                     __syncwarp();
-                    continue;
                 }
-                tc_fence_after();
-                if (leader) {
-                    const uint64_t dK = dK0 + (uint64_t)((kx.st * C::TILE) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = (uint64_t)(((kk >> 2) * kRegion + (kk & 3) * 32) >> 4);
-                        mma_bf16_ss(s_col, dQ + off, dK + off, idesc_qk, kk > 0 ? 1u : 0u);
-                    }
-                    mma_commit(b_sf);
-                    mma_commit(bar(C::B_KE + kx.st));
-                }
-                __syncwarp();
-                pend = i;
             }
             if (!ok) break;
             if (leader) mma_commit(bar(C::B_QE));
             __syncwarp();
-            if (pend >= 0 && !(ok = weigh())) break;
+            if (pend >= 0 && !(ok = halves(n, false))) break;
             if (started) {
                 if (leader) mma_commit(bar(C::B_OF + x));
                 __syncwarp();

@@ -201,12 +201,11 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
             for (int x = 0; x < 4 * ND; ++x) bad |= not_finite(acc[r][x]);
             if (bad && valid) flags[rr] = 1;
             if (U.split) {
-                const size_t slot = (size_t)U.slot * p.rows + rr;
 #pragma unroll
                 for (int h = 0; h < ND; ++h)
-                    *reinterpret_cast<float4 *>(p.part_o + slot * D + h * 64 + tx * 4) =
+                    *reinterpret_cast<float4 *>(p.part_o + part_at<D>(p, U.slot, h * 16 + tx, rr)) =
                         make_float4(acc[r][h * 4], acc[r][h * 4 + 1], acc[r][h * 4 + 2], acc[r][h * 4 + 3]);
-                if (tx == 0) p.part_ml[slot] = make_float2(m[r], l[r]);
+                if (tx == 0) p.part_ml[(size_t)U.slot * p.rows + rr] = make_float2(m[r], l[r]);
             } else if (t < p.m) {
                 T *o = static_cast<T *>(p.O) + (((size_t)U.b * p.Hq + head) * p.m + t) * D;
                 const float inv = valid && l[r] != 0.f ? 1.f / l[r] : 0.f;
