@@ -54,7 +54,7 @@ enum PagedKernel { kPagedRows = 0, kPagedTc = 1, kPagedTile = 2 };
 // Fills the launcher's fields of `p` and says which kernel runs it.
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms);
 // CTAs of the streaming kernel that fit an SM, by the rows of a unit.
-inline int paged_rows_ctas(int rows) { return rows <= 1 ? 3 : rows <= 4 ? 2 : 1; }
+inline int paged_rows_ctas(int rows) { return rows <= 4 ? 2 : 1; }
 // Scratch of one call: partial results of split tiles (0: nothing is split).
 size_t paged_workspace_bytes(const PagedProblem &p);
 cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream);

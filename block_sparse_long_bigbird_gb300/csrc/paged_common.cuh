@@ -53,27 +53,27 @@ __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.402
 
 // The plan in shared memory. Arrays over sequences, then the global list.
 struct Plan {
-    long long *vbase;  // [B + 1] where a sequence's tiles begin on the common axis
+    long long *vbase;  // [B + 1] where a sequence's tiles begin on the common axis, then the share
     uint64_t *gbit;    // [ngb] global keys of those blocks
     int *q, *s;        // [B] new tokens and tokens in the cache (q = 0 for a refused sequence)
     int *gpos;         // [ng] global positions
     int *gblk;         // [ngb] 64-key blocks that hold one, ascending
     int *hstride;      // [Hkv] longest stride of a key head's query heads (with dilation)
-    int *misc;         // [0] ngb, [1] tiles
+    int *misc;         // [0] ngb, [1] CTAs, [2] remainder of the shares
     int ngb;
     int ctas;          // CTAs that share the axis
-    long long total;   // its length
+    long long share;   // its length divided by them: share * ctas + rest
+    int rest;
 };
 
-__host__ __device__ inline size_t plan_bytes(int B, int ng, int Hkv) {
-    const size_t ints = 2 * (size_t)B + 2 * (size_t)ng + Hkv + 2;
-    return 8 * (size_t)(B + 1 + ng) + ((ints * 4 + 15) & ~(size_t)15);
+__host__ __device__ constexpr size_t plan_bytes(int B, int ng, int Hkv) {
+    return 8 * (size_t)(B + 2 + ng) + (((2 * (size_t)B + 2 * (size_t)ng + Hkv + 4) * 4 + 15) & ~(size_t)15);
 }
 
 __device__ __forceinline__ Plan plan_at(void *smem, int B, int ng, int Hkv) {
     Plan P;
     P.vbase = reinterpret_cast<long long *>(smem);
-    P.gbit = reinterpret_cast<uint64_t *>(P.vbase + B + 1);
+    P.gbit = reinterpret_cast<uint64_t *>(P.vbase + B + 2);
     P.q = reinterpret_cast<int *>(P.gbit + ng);
     P.s = P.q + B;
     P.gpos = P.s + B;
@@ -82,7 +82,8 @@ __device__ __forceinline__ Plan plan_at(void *smem, int B, int ng, int Hkv) {
     P.misc = P.hstride + Hkv;
     P.ngb = 0;
     P.ctas = 1;
-    P.total = 0;
+    P.share = 0;
+    P.rest = 0;
     return P;
 }
 
@@ -113,20 +114,43 @@ __device__ __forceinline__ int lower_bound(const int *a, int n, int v) {
     return lo;
 }
 
+// a / b for numbers that mostly fit 32 bits.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if (((unsigned long long)a | (unsigned long long)b) >> 32) return a / b;
+    return (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // Length on the common axis of one tile of a sequence for a key head of that
-// stride: an upper estimate of the blocks it walks, and its fixed cost.
+// stride: an estimate of the blocks it walks (a sixteenth of the global
+// positions have a block of their own: most lie together), and its fixed cost.
+// It decides how evenly the work is spread, nothing else.
 __device__ __forceinline__ int tile_length(const PagedProblem &p, const Plan &P, int q, int s, int stride) {
     const int all = (s + 63) >> 6;
     const long long span = (long long)head_reach(p, stride) + min(q, p.tpt);
-    const long long band = (span >> 6) + 2 + P.ngb;
+    const long long band = (span >> 6) + 2 + ((p.ng + 15) >> 4);
     return (band < all ? (int)band : all) + p.cost;
 }
 
-// Computed by the whole CTA. Ends with a barrier.
+// Computed by the whole CTA. Ends with a barrier. All loads are issued before
+// the first is used, and warp 0 does what follows on its own: the plan stands
+// before every call's first load of a key, so its latency counts.
 __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     const int tid = threadIdx.x, lane = tid & 31, nthr = blockDim.x;
+    int q0 = p.m, s0 = 0, g0 = -1, g1 = -1;
+    if (tid < p.B) {
+        if (p.qlens) q0 = __ldg(p.qlens + tid);
+        s0 = __ldg(p.lens + tid);
+    }
+    if (tid < p.ng) {
+        g0 = __ldg(p.gidx + tid);
+        if (tid > 0) g1 = __ldg(p.gidx + tid - 1);
+    }
     for (int b = tid; b < p.B; b += nthr) {
-        int q = p.qlens ? __ldg(p.qlens + b) : p.m, s = __ldg(p.lens + b);
+        int q = q0, s = s0;
+        if (b != tid) {
+            q = p.qlens ? __ldg(p.qlens + b) : p.m;
+            s = __ldg(p.lens + b);
+        }
         if (q < 0 || q > p.m || s < q || (long long)s > ((long long)p.max_pages << p.log_page)) {
             atomicOr(p.status, kDevBadIndex);
             q = s = 0;
@@ -137,8 +161,9 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     // the global list: a block starts where the block number changes; entries
     // that break the order are skipped (the call's result is then unspecified)
     for (int i = tid; i < p.ng; i += nthr) {
-        int v = __ldg(p.gidx + i);
-        if (v < 0 || v >= kPagedMaxLen || (i > 0 && __ldg(p.gidx + i - 1) >= v)) {
+        int v = i == tid ? g0 : __ldg(p.gidx + i);
+        const int before = i == tid ? g1 : __ldg(p.gidx + i - 1);
+        if (v < 0 || v >= kPagedMaxLen || (i > 0 && before >= v)) {
             atomicOr(p.status, kDevBadIndex);
             v = -1;
         }
@@ -151,7 +176,8 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
             P.hstride[h] = st;
         }
     __syncthreads();
-    if (tid < 32) {
+    const int all_tiles = (p.m + p.tpt - 1) / p.tpt;
+    if (p.ng > 0 && tid >= nthr - 32) {  // the last warp: the blocks of the global list
         int n = 0, kept = 0, last = -1;  // blocks and entries so far, the last entry's block
         for (int i0 = 0; i0 < p.ng; i0 += 32) {
             const int v = i0 + lane < p.ng ? P.gpos[i0 + lane] : -1;
@@ -178,25 +204,20 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
         for (int i = kept + lane; i < p.ng; i += 32) P.gpos[i] = 0x7fffffff;
         if (lane == 0) P.misc[0] = n;
     }
-    __syncthreads();
-    P.ngb = P.misc[0];
-    const int all_tiles = (p.m + p.tpt - 1) / p.tpt;
-    for (int b = tid; b < p.B; b += nthr) {  // each sequence's length on the axis
-        const int q = P.q[b], tiles = (q + p.tpt - 1) / p.tpt;
-        long long n = (long long)p.Hkv * (all_tiles - tiles);  // tiles without tokens: one each
-        if (!p.dilation) {
-            n += (long long)p.Hkv * tiles * tile_length(p, P, q, P.s[b], 1);
-        } else {
-            for (int h = 0; h < p.Hkv; ++h) n += (long long)tiles * tile_length(p, P, q, P.s[b], P.hstride[h]);
-        }
-        P.vbase[b + 1] = n;
-    }
-    __syncthreads();
     if (tid < 32) {
         long long base = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
+        for (int b0 = 0; b0 < p.B; b0 += 32) {  // each sequence's length on the axis, summed up
             const int b = b0 + lane;
-            long long v = b < p.B ? P.vbase[b + 1] : 0;
+            long long v = 0;
+            if (b < p.B) {
+                const int q = P.q[b], s = P.s[b], tiles = (q + p.tpt - 1) / p.tpt;
+                v = (long long)p.Hkv * (all_tiles - tiles);  // tiles without tokens: one each
+                if (!p.dilation) {
+                    v += (long long)p.Hkv * tiles * tile_length(p, P, q, s, 1);
+                } else {
+                    for (int h = 0; h < p.Hkv; ++h) v += (long long)tiles * tile_length(p, P, q, s, P.hstride[h]);
+                }
+            }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long a = __shfl_up_sync(kAllLanes, v, o);
@@ -205,20 +226,37 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
             if (b < p.B) P.vbase[b + 1] = base + v;
             base += __shfl_sync(kAllLanes, v, 31);
         }
-        if (lane == 0) P.vbase[0] = 0;
+        if (lane == 0) {
+            P.vbase[0] = 0;
+            // as many CTAs as there are tiles, or pieces worth having
+            const long long tiles = (long long)p.B * p.Hkv * all_tiles;
+            const long long pieces = p.cut ? divide(base, p.min_piece) : 0;
+            const long long want = pieces > tiles ? pieces : tiles;
+            const int ctas = want < p.slots ? (int)want : p.slots;
+            const long long share = divide(base, ctas);
+            P.misc[1] = ctas;
+            P.misc[2] = (int)(base - share * ctas);
+            P.vbase[p.B + 1] = share;
+        }
     }
     __syncthreads();
-    P.total = P.vbase[p.B];
-    // as many CTAs as there are tiles, or pieces worth having
-    const long long tiles = (long long)p.B * p.Hkv * all_tiles;
-    const long long pieces = p.cut ? P.total / p.min_piece : 0;
-    const long long want = pieces > tiles ? pieces : tiles;
-    P.ctas = want < p.slots ? (int)want : p.slots;
+    P.ngb = p.ng > 0 ? P.misc[0] : 0;
+    P.ctas = P.misc[1];
+    P.rest = P.misc[2];
+    P.share = P.vbase[p.B + 1];
 }
 
-// Where CTA c's stretch begins, and the CTA whose stretch holds x.
-__device__ __forceinline__ long long cta_begin(const Plan &P, int c) { return P.total * c / P.ctas; }
-__device__ __forceinline__ int cta_of(const Plan &P, long long x) { return (int)(((x + 1) * P.ctas - 1) / P.total); }
+// Where CTA c's stretch begins: floor(length * c / ctas).
+__device__ __forceinline__ long long cta_begin(const Plan &P, int c) {
+    return P.share * c + (long long)((uint32_t)(c * P.rest) / (uint32_t)P.ctas);
+}
+// The CTA whose stretch holds x, at or after CTA c.
+__device__ __forceinline__ int cta_of(const Plan &P, long long x, int c) {
+    const long long guess = divide(x, P.share + 1);  // no stretch is longer
+    if (guess > c) c = (int)guess;
+    while (c + 1 < P.ctas && cta_begin(P, c + 1) <= x) ++c;
+    return c;
+}
 
 // A tile on the axis, and how to get to the next one. `live` false: its rows are
 // only zeroed (past q of their sequence).
@@ -273,7 +311,7 @@ __device__ __forceinline__ Tile find_tile(const PagedProblem &p, const Plan &P, 
     if (T.tiles > 0) {
         if (!p.dilation) {
             const long long per = (long long)T.len * T.tiles;
-            T.hk = (int)min(off / per, (long long)p.Hkv);
+            T.hk = (int)min(divide(off, per), (long long)p.Hkv);
             T.begin += T.hk * per;
             off -= T.hk * per;
         } else {
@@ -286,7 +324,7 @@ __device__ __forceinline__ Tile find_tile(const PagedProblem &p, const Plan &P, 
             }
         }
     }
-    T.i = (int)(T.hk < p.Hkv ? off / T.len : off);
+    T.i = (int)(T.hk < p.Hkv ? divide(off, T.len) : off);
     T.begin += T.hk < p.Hkv ? (long long)T.i * T.len : off;
     T.place(p);
     return T;
@@ -314,7 +352,9 @@ struct Units {
     Tile T;
     long long v, end;
     int c;
-    __device__ __forceinline__ Units(const PagedProblem &p, const Plan &P, int cta) : v(0), end(0), c(cta) {
+    __device__ __forceinline__ void begin(const PagedProblem &p, const Plan &P, int cta) {
+        v = end = 0;
+        c = cta;
         if (cta >= P.ctas) return;
         v = cta_begin(P, cta);
         end = cta_begin(P, cta + 1);
@@ -334,9 +374,9 @@ struct Units {
         U.s = T.s;
         U.live = T.live;
         U.lo_blk = U.n_glob = U.e0 = U.e1 = 0;
-        const long long begin = v, stop = p.cut && T.end > end ? end : T.end;
-        U.split = begin > T.begin || stop < T.end;
-        U.slot = 2 * c + (begin == T.begin);
+        const long long from = v, stop = p.cut && T.end > end ? end : T.end;
+        U.split = from > T.begin || stop < T.end;
+        U.slot = 2 * c + (from == T.begin);
         v = stop;
         if (!T.live) return true;
         const int p0 = U.s - U.q + U.t0, p1 = U.s - U.q + min(U.t0 + p.tpt, U.q) - 1;
@@ -351,12 +391,25 @@ struct Units {
         U.e1 = n;
         if (U.split) {
             const long long len = T.end - T.begin;
-            U.e0 = (int)(n * (begin - T.begin) / len);
-            U.e1 = (int)(n * (stop - T.begin) / len);
+            U.e0 = (int)divide(n * (from - T.begin), len);
+            U.e1 = (int)divide(n * (stop - T.begin), len);
         }
         return true;
     }
 };
+
+// The units of a CTA that works on one at a time: thread 0 finds the next one
+// while the others work and leaves it in shared memory, where it costs no
+// registers. Two rooms: the one being filled is not the one being read.
+struct alignas(16) UnitRoom {
+    Units units;
+    Unit U[2];
+    int more[2];
+};
+
+__device__ __noinline__ void fill_room(const PagedProblem &p, const Plan &P, UnitRoom *room, int k) {
+    room->more[k] = room->units.next(p, P, room->U[k]);
+}
 
 __device__ __forceinline__ int entry_block(const Plan &P, const Unit &U, int e) {
     return e < U.n_glob ? P.gblk[e] : U.lo_blk + e - U.n_glob;
@@ -432,10 +485,45 @@ __device__ __forceinline__ float from_float<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Element x of a 16-byte piece, as fp32 (exact). x is a constant wherever this is
+// used. By bits, not through a pointer of another type.
+template <typename T>
+__device__ __forceinline__ float element(const uint4 &v, int x) {
+    constexpr bool half = sizeof(T) == 2;
+    const int i = half ? x >> 1 : x;
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    if (!half) return __uint_as_float(w);
+    return __uint_as_float(x & 1 ? w & 0xffff0000u : w << 16);
+}
+
+// Two values rounded to bf16 (to nearest, ties to even), a in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Sixteen consecutive elements, rounded and written (16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void store16(T *at, const float (&v)[16]) {
+    uint4 *out = reinterpret_cast<uint4 *>(at);
+    if (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            out[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            out[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                __float_as_uint(v[4 * i + 3]));
+    }
+}
+
 // Row `row` of a unit: which token and head it is. Rows go head by head, so
 // that one tensor copy fetches a tile's queries.
 __device__ __forceinline__ void row_token(const PagedProblem &p, const Unit &U, int row, int tpt, int &t, int &head) {
-    const int g = row / tpt;
+    const int g = tpt == 1 ? row : row / tpt;
     t = U.t0 + row - g * tpt;
     head = U.hk * p.group + g;
 }

@@ -24,28 +24,34 @@ constexpr int kRowsWarps = 8;
 constexpr int kItem = 16;  // keys a warp takes at a time
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) paged_rows(const PagedProblem p) {
+__global__ void __launch_bounds__(kRowsWarps * 32, R == 8 ? 1 : 2)
+    paged_rows(const __grid_constant__ PagedProblem p) {
     constexpr int VE = 16 / sizeof(T);  // elements of a 16-byte load
     constexpr int LPK = D / VE;         // lanes per key
     constexpr int KPL = 32 / LPK;       // keys per warp-wide load
     constexpr int NIT = kItem / KPL;    // loads per item
-    constexpr int MOST = R >= 4 || (sizeof(T) == 2 && D == 128) ? 4 : 8;
-    constexpr int CH = NIT < MOST ? NIT : MOST;  // of which this many are in flight together
+    constexpr int CH = 4;               // of which this many are in flight together
+    static_assert(NIT % CH == 0, "whole chunks");
     extern __shared__ __align__(16) uint8_t smem[];
     // joining the warps' results: [warp][R] maxima and sums, [warp][R][D] sums
     float *jm = reinterpret_cast<float *>(smem);
     float *jl = jm + kRowsWarps * R;
     float *ja = jl + kRowsWarps * R;
-    Plan P = plan_at(ja + kRowsWarps * R * D, p.B, p.ng, p.Hkv);
+    UnitRoom *room = reinterpret_cast<UnitRoom *>(ja + kRowsWarps * R * D);
+    Plan P = plan_at(room + 1, p.B, p.ng, p.Hkv);
     make_plan(p, P);
     asm volatile("griddepcontrol.launch_dependents;");  // the join may start planning
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int grp = lane / LPK, sub = lane % LPK;
     const T *Kp = static_cast<const T *>(p.K), *Vp = static_cast<const T *>(p.V);
 
-    Units units(p, P, blockIdx.x);
-    Unit U;
-    while (units.next(p, P, U)) {
+    if (tid == 0) {
+        room->units.begin(p, P, blockIdx.x);
+        fill_room(p, P, room, 0);
+    }
+    __syncthreads();
+    for (int k = 0; room->more[k]; k ^= 1) {
+        const Unit &U = room->U[k];
         float q[R][VE], acc[R][VE], m[R], l[R];
         // lane r masks for row r; the warp reads the masks from there
         Row mine;
@@ -67,125 +73,155 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) 
             if ((rows_in >> r) & 1u) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(
                     static_cast<const T *>(p.Q) + (((size_t)U.b * p.Hq + head) * p.m + t) * D + sub * VE);
-                const T *x = reinterpret_cast<const T *>(&w);
 #pragma unroll
-                for (int i = 0; i < VE; ++i) q[r][i] = to_float<T>(x[i]) * p.scale_log2;
+                for (int i = 0; i < VE; ++i) q[r][i] = element<T>(w, i) * p.scale_log2;
             }
         }
-        // items of this unit: four per 64-key block, dealt to the warps in turn
+        // Items of this unit: four per 64-key block, dealt to the warps in turn, in
+        // chunks of CH loads. The next chunk's keys and values (R <= 2: registers
+        // allow it) and the page of the item after next are on their way while a
+        // chunk is worked on.
+        constexpr int NCH = NIT / CH;
+        constexpr bool AHEAD = R <= 2;
         const int i_end = 4 * U.e1;
-        int item = 4 * U.e0 + warp;
-        int blk = 0, pg = -1;
-        if (item < i_end) {
-            blk = entry_block(P, U, item >> 2);
-            pg = page_of(p, U.b, (blk << 6) + (item & 3) * kItem);
-        }
-        while (item < i_end) {
-            const int next = item + kRowsWarps;
-            int nblk = 0, npg = -1;
-            if (next < i_end) {  // the next table entry is on its way while this item is worked on
-                nblk = entry_block(P, U, next >> 2);
-                npg = page_of(p, U.b, (nblk << 6) + (next & 3) * kItem);
+        struct Item {
+            int i, blk, pg;
+        };
+        auto item_at = [&](int i) -> Item {
+            Item x = {i, 0, -1};
+            if (i < i_end) {
+                x.blk = entry_block(P, U, i >> 2);
+                x.pg = page_of(p, U.b, (x.blk << 6) + (i & 3) * kItem);
             }
-            const int j0 = (blk << 6) + (item & 3) * kItem;
-            uint32_t mask[R], any = 0u, all = 0xffffu;
-            if (pg >= 0) {
-                const uint32_t w =
-                    (uint32_t)(row_mask(mine, blk, global_bits(P, p, blk), ~0ull) >> ((item & 3) * kItem)) & 0xffffu;
+            return x;
+        };
+        struct Masks {
+            uint32_t m[R], any;
+            bool same;
+        };
+        auto masks_of = [&](const Item &x) -> Masks {
+            Masks k;
+            k.any = 0u;
+            uint32_t all = 0xffffu, w = 0u;
+            if (x.pg >= 0)
+                w = (uint32_t)(row_mask(mine, x.blk, global_bits(P, p, x.blk), ~0ull) >> ((x.i & 3) * kItem)) & 0xffffu;
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    mask[r] = __shfl_sync(kAllLanes, w, r);
-                    any |= mask[r];
-                    if ((rows_in >> r) & 1u) all &= mask[r];
+            for (int r = 0; r < R; ++r) {
+                k.m[r] = __shfl_sync(kAllLanes, w, r);
+                k.any |= k.m[r];
+                if ((rows_in >> r) & 1u) all &= k.m[r];
+            }
+            k.same = all == k.any;  // every row sees the same keys
+            return k;
+        };
+        // keys [c CH KPL, ...) of the item; what no row sees is not loaded
+        auto load = [&](const Item &x, uint32_t any, int c, uint4 (&kw)[CH], uint4 (&vw)[CH]) {
+            const int j0 = (x.blk << 6) + (x.i & 3) * kItem;
+            const size_t at = any ? ((((size_t)x.pg * p.Hkv + U.hk) << p.log_page) + (j0 & (p.page - 1))) * D + sub * VE : 0;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int kk = (c * CH + i) * KPL + grp;
+                kw[i] = make_uint4(0u, 0u, 0u, 0u);
+                if ((any >> kk) & 1u) kw[i] = __ldg(reinterpret_cast<const uint4 *>(Kp + at + (size_t)kk * D));
+            }
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int kk = (c * CH + i) * KPL + grp;
+                vw[i] = make_uint4(0u, 0u, 0u, 0u);
+                if ((any >> kk) & 1u) vw[i] = __ldg(reinterpret_cast<const uint4 *>(Vp + at + (size_t)kk * D));
+            }
+        };
+        auto work = [&](const Masks &k, int c, const uint4 (&kw)[CH], const uint4 (&vw)[CH]) {
+            float s[R][CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) s[r][i] = 0.f;
+#pragma unroll
+                for (int x = 0; x < VE; ++x) {
+                    const float kf = element<T>(kw[i], x);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) s[r][i] = fmaf(q[r][x], kf, s[r][i]);
                 }
             }
-            if (any) {
-                const size_t at = ((((size_t)pg * p.Hkv + U.hk) << p.log_page) + (j0 & (p.page - 1))) * D + sub * VE;
-                const bool same = all == any;  // every row sees the same keys
 #pragma unroll
-                for (int c = 0; c < NIT / CH; ++c) {
-                    uint4 kw[CH], vw[CH];
-                    if (KPL > 1 || any >> (c * CH)) {
+            for (int o = LPK / 2; o; o >>= 1)
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) {
-                            const int kk = (c * CH + i) * KPL + grp;
-                            kw[i] = vw[i] = make_uint4(0u, 0u, 0u, 0u);
-                            if ((any >> kk) & 1u) kw[i] = __ldg(reinterpret_cast<const uint4 *>(Kp + at + (size_t)kk * D));
-                        }
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) {
-                            const int kk = (c * CH + i) * KPL + grp;
-                            if ((any >> kk) & 1u) vw[i] = __ldg(reinterpret_cast<const uint4 *>(Vp + at + (size_t)kk * D));
-                        }
-                        float s[R][CH];
+                    for (int i = 0; i < CH; ++i) s[r][i] += __shfl_xor_sync(kAllLanes, s[r][i], o);
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) {
-                            const T *k = reinterpret_cast<const T *>(&kw[i]);
+            for (int r = 0; r < R; ++r) {
+                float mn = m[r];
 #pragma unroll
-                            for (int r = 0; r < R; ++r) s[r][i] = 0.f;
+                for (int i = 0; i < CH; ++i) {
+                    if (!((k.m[r] >> ((c * CH + i) * KPL + grp)) & 1u)) s[r][i] = -CUDART_INF_F;
+                    mn = fmaxf(mn, s[r][i]);
+                }
+                const float ref = mn == -CUDART_INF_F ? 0.f : mn;
+                const float f = ptx::ex2(m[r] - ref);  // 0 from the initial -inf
+                m[r] = mn;
+                l[r] *= f;
 #pragma unroll
-                            for (int x = 0; x < VE; ++x) {
-                                const float kx = to_float<T>(k[x]);
+                for (int i = 0; i < CH; ++i) {
+                    s[r][i] = ptx::ex2(s[r][i] - ref);
+                    l[r] += s[r][i];
+                }
 #pragma unroll
-                                for (int r = 0; r < R; ++r) s[r][i] = fmaf(q[r][x], kx, s[r][i]);
-                            }
-                        }
+                for (int x = 0; x < VE; ++x) acc[r][x] *= f;
+            }
+            if (k.same) {
 #pragma unroll
-                        for (int o = LPK / 2; o; o >>= 1)
+                for (int i = 0; i < CH; ++i) {
 #pragma unroll
-                            for (int r = 0; r < R; ++r)
+                    for (int x = 0; x < VE; ++x) {
+                        const float vx = element<T>(vw[i], x);
 #pragma unroll
-                                for (int i = 0; i < CH; ++i) s[r][i] += __shfl_xor_sync(kAllLanes, s[r][i], o);
+                        for (int r = 0; r < R; ++r) acc[r][x] = fmaf(s[r][i], vx, acc[r][x]);
+                    }
+                }
+            } else {  // a value that some row does not see may be anything: keep 0 x NaN out of that row
 #pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            float mn = m[r];
+                for (int i = 0; i < CH; ++i) {
 #pragma unroll
-                            for (int i = 0; i < CH; ++i) {
-                                if (!((mask[r] >> ((c * CH + i) * KPL + grp)) & 1u)) s[r][i] = -CUDART_INF_F;
-                                mn = fmaxf(mn, s[r][i]);
-                            }
-                            const float ref = mn == -CUDART_INF_F ? 0.f : mn;
-                            const float f = ptx::ex2(m[r] - ref);  // 0 from the initial -inf
-                            m[r] = mn;
-                            l[r] *= f;
+                    for (int r = 0; r < R; ++r) {
+                        const bool sees = (k.m[r] >> ((c * CH + i) * KPL + grp)) & 1u;
 #pragma unroll
-                            for (int i = 0; i < CH; ++i) {
-                                s[r][i] = ptx::ex2(s[r][i] - ref);
-                                l[r] += s[r][i];
-                            }
-#pragma unroll
-                            for (int x = 0; x < VE; ++x) acc[r][x] *= f;
-                        }
-                        if (same) {
-#pragma unroll
-                            for (int i = 0; i < CH; ++i) {
-                                const T *v = reinterpret_cast<const T *>(&vw[i]);
-#pragma unroll
-                                for (int x = 0; x < VE; ++x) {
-                                    const float vx = to_float<T>(v[x]);
-#pragma unroll
-                                    for (int r = 0; r < R; ++r) acc[r][x] = fmaf(s[r][i], vx, acc[r][x]);
-                                }
-                            }
-                        } else {  // a value that some row does not see may be anything: keep 0 x NaN out of that row
-#pragma unroll
-                            for (int i = 0; i < CH; ++i) {
-                                const T *v = reinterpret_cast<const T *>(&vw[i]);
-#pragma unroll
-                                for (int r = 0; r < R; ++r) {
-                                    const bool sees = (mask[r] >> ((c * CH + i) * KPL + grp)) & 1u;
-#pragma unroll
-                                    for (int x = 0; x < VE; ++x)
-                                        acc[r][x] = sees ? fmaf(s[r][i], to_float<T>(v[x]), acc[r][x]) : acc[r][x];
-                                }
-                            }
-                        }
+                        for (int x = 0; x < VE; ++x)
+                            acc[r][x] = sees ? fmaf(s[r][i], element<T>(vw[i], x), acc[r][x]) : acc[r][x];
                     }
                 }
             }
-            item = next;
-            blk = nblk;
-            pg = npg;
+        };
+        Item now = item_at(4 * U.e0 + warp), after = item_at(4 * U.e0 + warp + kRowsWarps);
+        Masks km = masks_of(now);
+        uint4 kw[CH], vw[CH];
+        if (AHEAD && now.i < i_end) load(now, km.any, 0, kw, vw);
+        while (now.i < i_end) {
+            const Item third = item_at(after.i + kRowsWarps);
+            Masks kn = km;
+#pragma unroll 1
+            for (int c = 0; c < NCH; ++c) {
+                if constexpr (AHEAD) {
+                    uint4 kw2[CH], vw2[CH];
+                    const bool last = c == NCH - 1;
+                    if (last) kn = masks_of(after);
+                    load(last ? after : now, last ? kn.any : km.any, last ? 0 : c + 1, kw2, vw2);
+                    if (km.any) work(km, c, kw, vw);
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        kw[i] = kw2[i];
+                        vw[i] = vw2[i];
+                    }
+                } else if (km.any) {
+                    load(now, km.any, c, kw, vw);
+                    work(km, c, kw, vw);
+                }
+            }
+            if constexpr (!AHEAD) kn = masks_of(after);
+            now = after;
+            after = third;
+            km = kn;
         }
         // join the groups of lanes of a warp
 #pragma unroll
@@ -212,6 +248,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 1 ? 3 : R == 8 ? 1 : 2) 
                 jl[warp * R + r] = l[r];
             }
         }
+        if (tid == 0) fill_room(p, P, room, k ^ 1);
         __syncthreads();
         // and the warps, in order
         for (int idx = tid; idx < p.rows * D; idx += kRowsWarps * 32) {
@@ -263,7 +300,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const PagedProblem 
         const long long at = cta_begin(P, c);
         const Tile tile = find_tile(p, P, at);
         if (!tile.live || tile.begin == at || tile.begin < cta_begin(P, c - 1)) continue;
-        const int ns = cta_of(P, tile.end - 1) - c + 2;  // pieces: slot 2 c - 1, then 2 c, 2 c + 2, ...
+        const int ns = cta_of(P, tile.end - 1, c) - c + 2;  // pieces: slot 2 c - 1, then 2 c, 2 c + 2, ...
         const int share = ns > kMergeMany ? kMergeShare : 1;
         auto slot = [&](int k) { return k == 0 ? 2 * c - 1 : 2 * (c + k - 1); };
         for (int idx = chunk * kMergeThreads + (int)threadIdx.x; idx - (int)threadIdx.x < groups * share;
@@ -311,20 +348,16 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const PagedProblem 
             row_token(p, U, row - x * half_rows, p.tpt_half, t, head);
             if (t >= p.m) continue;
             const bool zero = t >= tile.q || l == 0.f;
-            __align__(16) T o[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = from_float<T>(zero ? 0.f : acc[i] / l);
-            uint4 *O = reinterpret_cast<uint4 *>(static_cast<T *>(p.O) +
-                                                 (((size_t)tile.b * p.Hq + head) * p.m + t) * D + 16 * k16);
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T); ++i) O[i] = reinterpret_cast<const uint4 *>(o)[i];
+            for (int i = 0; i < 16; ++i) acc[i] = zero ? 0.f : acc[i] / l;
+            store16<T>(static_cast<T *>(p.O) + (((size_t)tile.b * p.Hq + head) * p.m + t) * D + 16 * k16, acc);
         }
     }
 }
 
 template <typename T, int D, int R>
 cudaError_t launch_rows(const PagedProblem &p, cudaStream_t stream) {
-    const size_t smem = (size_t)kRowsWarps * R * (D + 2) * 4 + plan_bytes(p.B, p.ng, p.Hkv);
+    const size_t smem = (size_t)kRowsWarps * R * (D + 2) * 4 + sizeof(UnitRoom) + plan_bytes(p.B, p.ng, p.Hkv);
     static std::atomic<bool> done[64];
     auto kern = paged_rows<T, D, R>;
     cudaError_t e = allow_smem(kern, done, smem);

@@ -381,8 +381,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 e = ex2(e);
                                 if (k & 2) sum1 = f2_add(sum1, f2_pack(a, e));
                                 else sum0 = f2_add(sum0, f2_pack(a, e));
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(a, e);
-                                pk[c * 16 + k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                                pk[c * 16 + k / 2] = pack_bf16(a, e);
                             }
                         }
                         tmem_st32u(s_addr + h * 64, pk);
@@ -494,8 +493,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             for (int k = 0; k < 4; ++k) {
                                 const float a = row.valid ? o[q * 8 + 2 * k] * inv : 0.f;
                                 const float e = row.valid ? o[q * 8 + 2 * k + 1] * inv : 0.f;
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(a, e);
-                                b4[q][k] = *reinterpret_cast<const uint32_t *>(&two);
+                                b4[q][k] = pack_bf16(a, e);
                             }
 #pragma unroll
                         for (int o2 = 1; o2 < 4; o2 <<= 1)  // swap [q][lane] with [lane][q], a bit at a time
@@ -638,7 +636,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // What each step holds for the tiles, ahead of their use. Lane l looks
         // up piece l % ppb of entry l / ppb.
         const int log_bp = min(p.log_page, 6), log_ppb = 6 - log_bp, ppb = 1 << log_ppb;
-        Units units(p, P, blockIdx.x);
+        Units units;
+        units.begin(p, P, blockIdx.x);
         Unit U;
         for (bool more = true; ok && more; ++uc) {
             more = units.next(p, P, U);
@@ -885,8 +884,7 @@ cudaError_t launch_paged_tc(const PagedProblem &p, cudaStream_t stream) {
     return p.d == 64 ? launch_tc_d<64>(p, stream) : launch_tc_d<128>(p, stream);
 }
 
-static_assert(TcCfg<128>::PLAN_OFF + 1024 + (2 * kPagedMaxBatch + 2 * kPagedMaxGlobal + kPagedMaxHeads + 2) * 4 + 16 +
-                      (kPagedMaxBatch + 1 + kPagedMaxGlobal) * 8 <= 232448,
+static_assert(TcCfg<128>::PLAN_OFF + 1024 + plan_bytes(kPagedMaxBatch, kPagedMaxGlobal, kPagedMaxHeads) <= 232448,
               "the largest plan fits beside the tiles");
 
 }  // namespace sa

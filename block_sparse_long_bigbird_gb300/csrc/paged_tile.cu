@@ -24,11 +24,12 @@ struct TileSmem {
     static constexpr int S = KV + (D * kPad > kTR * D ? D * kPad : kTR * D) * 4;
     static constexpr int MASK = S + kTR * kPad * 4;
     static constexpr int FLAG = MASK + kTR * 8;
-    static constexpr int PLAN = FLAG + kTR * 4;
+    static constexpr int ROOM = FLAG + kTR * 4;
+    static constexpr int PLAN = ROOM + (int)sizeof(UnitRoom);
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
+__global__ void __launch_bounds__(kTT) paged_tile(const __grid_constant__ PagedProblem p) {
     using L = TileSmem<T, D>;
     constexpr int VE = 16 / sizeof(T);
     constexpr int ND = D / 64;  // 4-wide output columns per thread
@@ -45,9 +46,14 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
     const int ty = tid >> 4, tx = tid & 15;  // rows ty * 8 ..., keys and columns tx * 4 ...
     const T *Kp = static_cast<const T *>(p.K), *Vp = static_cast<const T *>(p.V);
 
-    Units units(p, P, blockIdx.x);
-    Unit U;
-    while (units.next(p, P, U)) {
+    UnitRoom *room = reinterpret_cast<UnitRoom *>(smem + L::ROOM);
+    if (tid == 0) {
+        room->units.begin(p, P, blockIdx.x);
+        fill_room(p, P, room, 0);
+    }
+    __syncthreads();
+    for (int room_k = 0; room->more[room_k]; room_k ^= 1) {
+        const Unit &U = room->U[room_k];
         // threads 0..63: one row each, for the masks
         Row row = {};
         if (tid < kTR) {
@@ -67,9 +73,8 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
             if (ok)
                 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.Q) +
                                                           (((size_t)U.b * p.Hq + head) * p.m + t) * D + c * VE));
-            const T *x = reinterpret_cast<const T *>(&w);
 #pragma unroll
-            for (int k = 0; k < VE; ++k) Qs[(c * VE + k) * kTR + r] = to_float<T>(x[k]) * p.scale_log2;
+            for (int k = 0; k < VE; ++k) Qs[(c * VE + k) * kTR + r] = element<T>(w, k) * p.scale_log2;
         }
         float acc[8][4 * ND], m[8], l[8];
 #pragma unroll
@@ -92,9 +97,8 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
             for (int c = tid >> 6; c < D / VE; c += kTT / 64) {
                 uint4 w = make_uint4(0u, 0u, 0u, 0u);
                 if (pg >= 0) w = __ldg(reinterpret_cast<const uint4 *>(Kp + at + c * VE));
-                const T *x = reinterpret_cast<const T *>(&w);
-#pragma unroll
-                for (int k = 0; k < VE; ++k) KV[(c * VE + k) * kPad + key] = to_float<T>(x[k]);
+    #pragma unroll
+                for (int k = 0; k < VE; ++k) KV[(c * VE + k) * kPad + key] = element<T>(w, k);
             }
             const unsigned there = __ballot_sync(kAllLanes, pg >= 0);  // of keys 32 (warp & 1) ...
             if (warp < 2 && lane == 0) flags[kTR - 2 + warp] = (int)there;
@@ -130,9 +134,8 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
                         w = __ldg(reinterpret_cast<const uint4 *>(
                             Vp + ((((size_t)vpg * p.Hkv + U.hk) << p.log_page) + (vpos & (p.page - 1))) * D + c * VE));
                     }
-                    const T *x = reinterpret_cast<const T *>(&w);
-#pragma unroll
-                    for (int k = 0; k < VE; ++k) KV[vk * D + c * VE + k] = to_float<T>(x[k]);
+        #pragma unroll
+                    for (int k = 0; k < VE; ++k) KV[vk * D + c * VE + k] = element<T>(w, k);
                 }
             }
 #pragma unroll
@@ -184,6 +187,7 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
                 }
             }
         }
+        if (tid == 0) fill_room(p, P, room, room_k ^ 1);
         __syncthreads();
         if (tid < kTR) flags[tid] = 0;
         __syncthreads();
@@ -225,6 +229,7 @@ __global__ void __launch_bounds__(kTT) paged_tile(const PagedProblem p) {
                 const float2 ml = exact_row<T, D>(p, P, U, t, head, a);
                 store_exact_row<T, D>(p, U, t, head, rr, ml, a);
             }
+        __syncthreads();  // every warp is done with the unit
     }
 }
 
