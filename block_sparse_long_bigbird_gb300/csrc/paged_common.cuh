@@ -131,13 +131,23 @@ __device__ __forceinline__ int tile_length(const PagedProblem &p, const Plan &P,
     return (band < all ? (int)band : all) + p.cost;
 }
 
+// New tokens and tokens in the cache of a sequence; none of either if they break
+// the contract.
+__device__ __forceinline__ void lengths(const PagedProblem &p, int q, int s, int &q_out, int &s_out) {
+    const bool bad = q < 0 || q > p.m || s < q || (long long)s > ((long long)p.max_pages << p.log_page);
+    if (bad) atomicOr(p.status, kDevBadIndex);
+    q_out = bad ? 0 : q;
+    s_out = bad ? 0 : s;
+}
+
 // Computed by the whole CTA. Ends with a barrier. All loads are issued before
 // the first is used, and warp 0 does what follows on its own: the plan stands
 // before every call's first load of a key, so its latency counts.
 __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     const int tid = threadIdx.x, lane = tid & 31, nthr = blockDim.x;
     int q0 = p.m, s0 = 0, g0 = -1, g1 = -1;
-    if (tid < p.B) {
+    if (!p.cut && p.ng == 0 && !p.dilation) return;  // whole tiles in turn: nothing to plan
+    if (p.cut && tid < p.B) {
         if (p.qlens) q0 = __ldg(p.qlens + tid);
         s0 = __ldg(p.lens + tid);
     }
@@ -145,18 +155,13 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
         g0 = __ldg(p.gidx + tid);
         if (tid > 0) g1 = __ldg(p.gidx + tid - 1);
     }
-    for (int b = tid; b < p.B; b += nthr) {
+    for (int b = tid; p.cut && b < p.B; b += nthr) {
         int q = q0, s = s0;
         if (b != tid) {
             q = p.qlens ? __ldg(p.qlens + b) : p.m;
             s = __ldg(p.lens + b);
         }
-        if (q < 0 || q > p.m || s < q || (long long)s > ((long long)p.max_pages << p.log_page)) {
-            atomicOr(p.status, kDevBadIndex);
-            q = s = 0;
-        }
-        P.q[b] = q;
-        P.s[b] = s;
+        lengths(p, q, s, P.q[b], P.s[b]);
     }
     // the global list: a block starts where the block number changes; entries
     // that break the order are skipped (the call's result is then unspecified)
@@ -204,7 +209,7 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
         for (int i = kept + lane; i < p.ng; i += 32) P.gpos[i] = 0x7fffffff;
         if (lane == 0) P.misc[0] = n;
     }
-    if (tid < 32) {
+    if (p.cut && tid < 32) {
         long long base = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {  // each sequence's length on the axis, summed up
             const int b = b0 + lane;
@@ -241,6 +246,7 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     }
     __syncthreads();
     P.ngb = p.ng > 0 ? P.misc[0] : 0;
+    if (!p.cut) return;
     P.ctas = P.misc[1];
     P.rest = P.misc[2];
     P.share = P.vbase[p.B + 1];
@@ -347,37 +353,57 @@ __device__ __forceinline__ bool is_global(const Plan &P, const PagedProblem &p, 
 }
 
 // The units of a CTA, in order: next() fills the following one and returns
-// whether there is one.
+// whether there is one. Where tiles may not be split (short sweeps), CTAs take
+// whole tiles in turn, which needs no plan.
 struct Units {
     Tile T;
     long long v, end;
     int c;
     __device__ __forceinline__ void begin(const PagedProblem &p, const Plan &P, int cta) {
-        v = end = 0;
         c = cta;
-        if (cta >= P.ctas) return;
-        v = cta_begin(P, cta);
-        end = cta_begin(P, cta + 1);
-        T = find_tile(p, P, v);
-        if (!p.cut && T.begin < v) {  // whole tiles only: those that begin in the stretch
-            v = T.end;
-            if (v < end) T.advance(p, P);
+        v = end = 0;
+        if (!p.cut) {
+            v = cta;
+            end = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt);
+        } else if (cta < P.ctas) {
+            v = cta_begin(P, cta);
+            end = cta_begin(P, cta + 1);
+            T = find_tile(p, P, v);
         }
     }
     __device__ __forceinline__ bool next(const PagedProblem &p, const Plan &P, Unit &U) {
+        U.b = U.hk = U.t0 = U.q = U.s = U.slot = U.lo_blk = U.n_glob = U.e0 = U.e1 = 0;
+        U.live = U.split = false;
         if (v >= end) return false;
-        if (v == T.end) T.advance(p, P);
+        long long from = 0, stop = 0;
+        if (!p.cut) {
+            const int all_tiles = (p.m + p.tpt - 1) / p.tpt;
+            const int u = (int)v, i = u % all_tiles, bh = u / all_tiles;
+            T.b = bh / p.Hkv;
+            T.hk = bh - T.b * p.Hkv;
+            lengths(p, p.qlens ? __ldg(p.qlens + T.b) : p.m, __ldg(p.lens + T.b), T.q, T.s);
+            T.tiles = (T.q + p.tpt - 1) / p.tpt;
+            T.live = i < T.tiles;
+            T.t0 = i * p.tpt;
+            v += gridDim.x;
+            U.hk = T.hk;
+            U.split = false;
+            U.slot = 0;
+        } else {
+            if (v == T.end) T.advance(p, P);
+            from = v;
+            stop = T.end > end ? end : T.end;
+            U.hk = T.head(p);
+            U.split = from > T.begin || stop < T.end;
+            U.slot = 2 * c + (from == T.begin);
+            v = stop;
+        }
         U.b = T.b;
-        U.hk = T.head(p);
         U.t0 = T.t0;
         U.q = T.q;
         U.s = T.s;
         U.live = T.live;
         U.lo_blk = U.n_glob = U.e0 = U.e1 = 0;
-        const long long from = v, stop = p.cut && T.end > end ? end : T.end;
-        U.split = from > T.begin || stop < T.end;
-        U.slot = 2 * c + (from == T.begin);
-        v = stop;
         if (!T.live) return true;
         const int p0 = U.s - U.q + U.t0, p1 = U.s - U.q + min(U.t0 + p.tpt, U.q) - 1;
         int first = max(0, p0 - head_reach(p, p.dilation ? P.hstride[U.hk] : 1));
@@ -407,8 +433,13 @@ struct alignas(16) UnitRoom {
     int more[2];
 };
 
-__device__ __noinline__ void fill_room(const PagedProblem &p, const Plan &P, UnitRoom *room, int k) {
-    room->more[k] = room->units.next(p, P, room->U[k]);
+__device__ __forceinline__ void fill_room(const PagedProblem &p, const Plan &P, UnitRoom *room, int k) {
+    Units u = room->units;  // in registers: what follows would be a chain of shared-memory accesses
+    Unit next;
+    const bool more = u.next(p, P, next);
+    room->units = u;
+    room->U[k] = next;
+    room->more[k] = more;
 }
 
 __device__ __forceinline__ int entry_block(const Plan &P, const Unit &U, int e) {

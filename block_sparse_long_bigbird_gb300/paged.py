@@ -56,9 +56,9 @@ def _ptr(t):
 
 def _ints(name, t, device, *shape):
     """`t` must be a contiguous int32 tensor on `device` of `shape` (-1: any size there)."""
-    if t.dtype is _INT and t.device == device and t.is_contiguous():
-        got = t.shape
-        if got == shape or (len(got) == len(shape) and all(n < 0 or n == m for n, m in zip(shape, got))):
+    got = t.shape
+    if t.dtype is _INT and t.device == device and t.is_contiguous() and len(got) == len(shape):
+        if got == shape or (got[0] == shape[0] or shape[0] < 0) and (len(got) == 1 or got[1] == shape[1] or shape[1] < 0):
             return
     raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device} (-1: any size)")
 
