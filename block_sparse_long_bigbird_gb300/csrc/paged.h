@@ -37,27 +37,31 @@ struct PagedProblem {
     int tpt;         // tokens per unit
     int tpt_half;    // tokens per half of a unit (tpt: units of one half)
     int rows;        // rows per unit: tpt * group
-    int cut;         // whether tiles may be split (then paged_merge is launched)
+    int cut;         // whether tiles may be split (then there is a plan, and paged_merge is launched)
     int slots;       // CTAs that share the work
     int min_piece;   // fewest 64-key blocks worth a CTA of their own
     int cost;        // what a tile costs beside its blocks, in blocks
+    int whole;       // blocks that a CTA may walk beyond an even share before splitting tiles pays
     float scale_log2;
     unsigned long long wait_ns;
     float *part_o;   // [2 slots][d / 4][rows][4] partial sums of split tiles
     float2 *part_ml; // [2 slots][rows] (running maximum, sum)
 };
 
-// Which kernel serves a call: few rows per key head, many rows in bf16 on the
-// tensor cores, or many rows on the ordinary units.
-enum PagedKernel { kPagedRows = 0, kPagedTc = 1, kPagedTile = 2 };
+// Which kernel serves a call: few rows per key head on the ordinary units or, in
+// bf16, on warp-level matrix instructions; many rows in bf16 on the tensor cores;
+// many rows on the ordinary units.
+enum PagedKernel { kPagedRows = 0, kPagedFew = 1, kPagedTc = 2, kPagedTile = 3 };
 
 // Fills the launcher's fields of `p` and says which kernel runs it.
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms);
-// CTAs of the streaming kernel that fit an SM, by the rows of a unit.
-inline int paged_rows_ctas(int rows) { return rows <= 4 ? 2 : 1; }
+// CTAs of the streaming kernels that fit an SM, by the rows of a unit.
+constexpr int paged_rows_ctas(int rows) { return rows <= 4 ? 2 : 1; }
+constexpr int paged_few_ctas(int d, int rows) { return d == 64 && rows <= 16 ? 2 : 1; }
 // Scratch of one call: partial results of split tiles (0: nothing is split).
 size_t paged_workspace_bytes(const PagedProblem &p);
 cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream);
+cudaError_t launch_paged_few(const PagedProblem &p, cudaStream_t stream);
 cudaError_t launch_paged_tile(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream);
 cudaError_t launch_paged_tc(const PagedProblem &p, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sms, cudaStream_t stream);

@@ -8,10 +8,15 @@
 
 namespace sa {
 
-// At most this many query rows of a key head go to the kernel that streams the
-// cache with the ordinary units.
-constexpr int kNoCutBlocks = 17;
-static int rows_limit(sa_dtype dtype) { return dtype == SA_FP32 ? 8 : 4; }
+// The most query rows per key head of the kernels that stream the cache. On the
+// ordinary units: one in bf16 (from two on the matrix instructions of paged_few
+// are ahead: 64 sequences of 4096 tokens, 8 key heads, d = 64, take 96 us for one
+// row on either, 102 against 96 us for two, 174 against 97 us for three), and
+// eight in fp32. With warp-level matrix instructions up to 24 rows, 128-row tiles
+// beyond: the same batch with 24 rows takes 137 against 168 us, 16 sequences of
+// 32768 tokens 237 against 241 us (d = 128: 341 and 358); 32 rows would take 160
+// and 167, 271 and 240, 481 and 356 us.
+constexpr int kRowsBf16 = 1, kRowsFp32 = 8, kFewRows = 24;
 
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms) {
     p.group = p.Hq / p.Hkv;
@@ -20,13 +25,26 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     const long long rows = (long long)p.m * p.group;
     PagedKernel kind;
     int per_sm = 1;
-    if (rows <= rows_limit(dtype)) {
+    // ns: a 64-key block in a CTA that has the SM to itself (or its usual share),
+    // and what splitting tiles adds to a call (more units, and the join)
+    int block_ns, split_ns = 8000;
+    if (rows <= (dtype == SA_FP32 ? kRowsFp32 : kRowsBf16)) {
         kind = kPagedRows;
         p.tpt = p.tpt_half = p.m;
         p.rows = (int)rows;
         per_sm = paged_rows_ctas(p.rows);
         p.min_piece = 4;
         p.cost = 1;
+        block_ns = dtype == SA_FP32 ? p.d / 64 * (450 + 130 * p.rows) : p.d == 64 ? 450 : 550;
+    } else if (dtype == SA_BF16 && !force_simt && rows <= kFewRows) {
+        kind = kPagedFew;
+        p.tpt = p.tpt_half = p.m;
+        p.rows = (int)rows;
+        per_sm = paged_few_ctas(p.d, p.rows);
+        p.min_piece = 4;
+        p.cost = 1;
+        block_ns = p.d == 64 ? 450 : 650;
+        split_ns = 14000;
     } else if (dtype == SA_BF16 && !force_simt) {
         kind = kPagedTc;
         const int most = 128 / p.group;
@@ -36,6 +54,8 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
         p.rows = halves * p.tpt_half * p.group;
         p.min_piece = 8;
         p.cost = 3;
+        block_ns = halves == 2 ? 1000 : 550;
+        split_ns = 28000;
     } else {
         kind = kPagedTile;
         const int most = 64 / p.group;
@@ -44,14 +64,32 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
         per_sm = p.d == 64 ? 4 : 2;
         p.min_piece = 2;
         p.cost = 1;
+        block_ns = p.d == 64 ? 7200 : 13000;
+        split_ns = 20000;
     }
-    // No tile walks more than its table row. Short walks are not split, which
-    // saves the launch that joins the pieces.
+    // Whole tiles take as many rounds of the GPU's CTAs as there are tiles to a CTA,
+    // rounded up; split ones share the blocks evenly, also with CTAs that had no
+    // tile. One token, 8 key heads, d = 128, one sequence: 900 keys take 15.4 us whole
+    // and 15.6 split, 4000 keys 46 and 18; 8 sequences of 900 keys 15.8 and 20; in
+    // fp32 with four rows 900 keys 34 and 21. 1000 tokens with a window of 512 over
+    // 8192 keys, 12 heads, four sequences: 34 and 62.
+    // The device decides by the lengths. The host leaves plan and join out where
+    // splitting would not pay with the longest walks: no tile walks more than its table
+    // row or, without dilation, its window and the blocks of the global positions
+    // (some 16 to a block).
+    p.whole = split_ns / block_ns;
     const long long tiles = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt);
-    const long long longest = ((((long long)p.max_pages << p.log_page) + 63) >> 6) + p.cost;
-    p.cut = longest > kNoCutBlocks;
-    const long long most = p.cut ? tiles * (longest / p.min_piece + 1) : tiles;
-    p.slots = (int)(most < (long long)num_sms * per_sm ? most : (long long)num_sms * per_sm);
+    long long longest = (((long long)p.max_pages << p.log_page) + 63) >> 6;
+    if (!p.dilation && p.half < longest << 6) {
+        const long long band = (((long long)p.half + p.tpt) >> 6) + 2 + ((p.ng + 15) >> 4);
+        longest = band < longest ? band : longest;
+    }
+    longest += p.cost;
+    const long long ctas = (long long)num_sms * per_sm;
+    const long long pieces = tiles * (longest / p.min_piece + 1);
+    const long long most = pieces < ctas ? pieces : ctas;
+    p.cut = (tiles + ctas - 1) / ctas * longest - tiles * longest / most > p.whole;
+    p.slots = (int)(p.cut ? most : tiles < ctas ? tiles : ctas);
     return kind;
 }
 
@@ -140,15 +178,21 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
     p.gidx = n_global > 0 ? global_idx : nullptr;
     p.ng = n_global;
     p.wait_ns = sa::api_wait_ns();
+    // the scratch that any window needs, then what this one makes of it (not more)
+    sa::PagedProblem any = p;
+    any.half = (int)sa::kPagedMaxLen;
+    sa::paged_shape(any, dtype, sa::api_force_simt(), sms);
+    const size_t room = sa::paged_workspace_bytes(any);
+    if (room && ws_ok(workspace, workspace_bytes, room) != SA_OK) return SA_ERR_INVALID_ARG;
     const sa::PagedKernel kind = sa::paged_shape(p, dtype, sa::api_force_simt(), sms);
     const size_t need = sa::paged_workspace_bytes(p);
     if (need) {
-        if (ws_ok(workspace, workspace_bytes, need) != SA_OK) return SA_ERR_INVALID_ARG;
         p.part_o = static_cast<float *>(workspace);
         p.part_ml = reinterpret_cast<float2 *>(p.part_o + 2 * (size_t)p.slots * p.rows * p.d);
     }
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = kind == sa::kPagedRows ? sa::launch_paged_rows(p, dtype, cs)
+                    : kind == sa::kPagedFew ? sa::launch_paged_few(p, cs)
                     : kind == sa::kPagedTc ? sa::launch_paged_tc(p, cs)
                                            : sa::launch_paged_tile(p, dtype, cs);
     if (e == cudaSuccess && need) e = sa::launch_paged_merge(p, dtype, sms, cs);
@@ -165,6 +209,7 @@ size_t sa_longformer_paged_workspace_bytes(int B, int Hq, int Hkv, int m, int d,
     if (sa::api_device(&status, &sms) != SA_OK) return 0;
     sa::PagedProblem p = {};
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.m = m; p.d = d; p.page = page; p.max_pages = max_pages;
+    p.half = (int)sa::kPagedMaxLen;
     sa::paged_shape(p, dtype, sa::api_force_simt(), sms);
     return sa::paged_workspace_bytes(p);
 }

@@ -9,7 +9,8 @@
 // stretch [T c / n, T (c + 1) / n): every CTA gets the same amount of work
 // whatever the lengths of the sequences, and a tile is split only where a
 // boundary falls into it, so there are fewer than 2 n partial results. The part
-// of a tile that one CTA takes is a unit. The lengths live on the device, so no
+// of a tile that one CTA takes is a unit. Where splitting would add more than
+// it evens out, CTAs take whole tiles in turn. The lengths live on the device, so no
 // host code can do this: every CTA reads them (at most kPagedMaxBatch) and
 // computes the same plan in shared memory, which costs one or two microseconds
 // where a planning kernel would cost a launch.
@@ -59,11 +60,12 @@ struct Plan {
     int *gpos;         // [ng] global positions
     int *gblk;         // [ngb] 64-key blocks that hold one, ascending
     int *hstride;      // [Hkv] longest stride of a key head's query heads (with dilation)
-    int *misc;         // [0] ngb, [1] CTAs, [2] remainder of the shares
+    int *misc;         // [0] ngb, [1] CTAs (0: whole tiles in turn), [2] remainder of the shares
     int ngb;
     int ctas;          // CTAs that share the axis
     long long share;   // its length divided by them: share * ctas + rest
     int rest;
+    bool cut;          // whether tiles are split
 };
 
 __host__ __device__ constexpr size_t plan_bytes(int B, int ng, int Hkv) {
@@ -84,6 +86,7 @@ __device__ __forceinline__ Plan plan_at(void *smem, int B, int ng, int Hkv) {
     P.ctas = 1;
     P.share = 0;
     P.rest = 0;
+    P.cut = false;
     return P;
 }
 
@@ -211,6 +214,7 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     }
     if (p.cut && tid < 32) {
         long long base = 0;
+        int longest = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {  // each sequence's length on the axis, summed up
             const int b = b0 + lane;
             long long v = 0;
@@ -218,9 +222,15 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
                 const int q = P.q[b], s = P.s[b], tiles = (q + p.tpt - 1) / p.tpt;
                 v = (long long)p.Hkv * (all_tiles - tiles);  // tiles without tokens: one each
                 if (!p.dilation) {
-                    v += (long long)p.Hkv * tiles * tile_length(p, P, q, s, 1);
-                } else {
-                    for (int h = 0; h < p.Hkv; ++h) v += (long long)tiles * tile_length(p, P, q, s, P.hstride[h]);
+                    const int len = tiles > 0 ? tile_length(p, P, q, s, 1) : 0;
+                    v += (long long)p.Hkv * tiles * len;
+                    longest = max(longest, len);
+                } else if (tiles > 0) {
+                    for (int h = 0; h < p.Hkv; ++h) {
+                        const int len = tile_length(p, P, q, s, P.hstride[h]);
+                        v += (long long)tiles * len;
+                        longest = max(longest, len);
+                    }
                 }
             }
 #pragma unroll
@@ -231,6 +241,7 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
             if (b < p.B) P.vbase[b + 1] = base + v;
             base += __shfl_sync(kAllLanes, v, 31);
         }
+        longest = __reduce_max_sync(kAllLanes, longest);
         if (lane == 0) {
             P.vbase[0] = 0;
             // as many CTAs as there are tiles, or pieces worth having
@@ -239,7 +250,9 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
             const long long want = pieces > tiles ? pieces : tiles;
             const int ctas = want < p.slots ? (int)want : p.slots;
             const long long share = divide(base, ctas);
-            P.misc[1] = ctas;
+            // what the last CTA would walk beyond an even share with whole tiles
+            const long long over = divide(tiles + p.slots - 1, p.slots) * longest - share;
+            P.misc[1] = over > p.whole ? ctas : 0;
             P.misc[2] = (int)(base - share * ctas);
             P.vbase[p.B + 1] = share;
         }
@@ -247,7 +260,8 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     __syncthreads();
     P.ngb = p.ng > 0 ? P.misc[0] : 0;
     if (!p.cut) return;
-    P.ctas = P.misc[1];
+    P.cut = P.misc[1] > 0;
+    P.ctas = P.cut ? P.misc[1] : 1;
     P.rest = P.misc[2];
     P.share = P.vbase[p.B + 1];
 }
@@ -353,8 +367,7 @@ __device__ __forceinline__ bool is_global(const Plan &P, const PagedProblem &p, 
 }
 
 // The units of a CTA, in order: next() fills the following one and returns
-// whether there is one. Where tiles may not be split (short sweeps), CTAs take
-// whole tiles in turn, which needs no plan.
+// whether there is one.
 struct Units {
     Tile T;
     long long v, end;
@@ -362,7 +375,7 @@ struct Units {
     __device__ __forceinline__ void begin(const PagedProblem &p, const Plan &P, int cta) {
         c = cta;
         v = end = 0;
-        if (!p.cut) {
+        if (!P.cut) {
             v = cta;
             end = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt);
         } else if (cta < P.ctas) {
@@ -376,7 +389,7 @@ struct Units {
         U.live = U.split = false;
         if (v >= end) return false;
         long long from = 0, stop = 0;
-        if (!p.cut) {
+        if (!P.cut) {
             const int all_tiles = (p.m + p.tpt - 1) / p.tpt;
             const int u = (int)v, i = u % all_tiles, bh = u / all_tiles;
             T.b = bh / p.Hkv;

@@ -4,8 +4,8 @@
 //     O_r = sum_j w_rj V_j / sum_j w_rj,   w_rj = 2^(s_rj - max_j s_rj),   s = q . k log2(e) / sqrt(d)
 //
 // A call reads each visible key and value row once per key head and does a few
-// flops per byte: the memory bounds it as long as a key head has at most R = 8
-// rows (rows = tokens x query heads of the key head). One warp takes 16 keys
+// flops per byte: the memory bounds it as long as a key head has few rows: one in
+// bf16, up to R = 8 in fp32 (tokens x query heads of the key head). One warp takes 16 keys
 // at a time (one page, one table entry): each key's row is spread over
 // D / 8 (bf16) or D / 4 (fp32) lanes, 16 bytes each, so all loads are full
 // lines; K and V of the 16 keys are requested together before either is used.
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const PagedProblem 
     Plan P = plan_at(smem, p.B, p.ng, p.Hkv);
     make_plan(p, P);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the sweeps' results are visible from here on
+    if (!P.cut) return;
     const int groups = p.rows * (D / 16);
     const int half_rows = p.tpt_half * p.group;
     const long long n_items = (long long)(P.ctas - 1) * per_tile;
@@ -368,12 +369,12 @@ cudaError_t launch_rows(const PagedProblem &p, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t launch_rows_r(const PagedProblem &p, cudaStream_t stream) {
-    if (p.rows <= 1) return launch_rows<T, D, 1>(p, stream);
-    if (p.rows <= 2) return launch_rows<T, D, 2>(p, stream);
     if constexpr (sizeof(T) == 4) {
         if (p.rows > 4) return launch_rows<T, D, 8>(p, stream);
+        if (p.rows > 2) return launch_rows<T, D, 4>(p, stream);
+        if (p.rows > 1) return launch_rows<T, D, 2>(p, stream);
     }
-    return launch_rows<T, D, 4>(p, stream);
+    return launch_rows<T, D, 1>(p, stream);
 }
 
 }  // namespace
@@ -392,8 +393,10 @@ cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sm
                          : (p.d == 64 ? paged_merge<__nv_bfloat16, 64> : paged_merge<__nv_bfloat16, 128>);
     // no more shared memory than a kernel has without asking: the largest plan takes 29 KB
     // CTAs per tile: as many as its groups keep busy, within what fits the GPU at a time
-    const long long busy = ((long long)p.rows * (p.d / 16) + kMergeThreads - 1) / kMergeThreads;
-    long long per_tile = 8ll * num_sms / p.slots;
+    const long long tiles = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt);
+    const int share = p.slots / tiles >= kMergeMany ? kMergeShare : 1;
+    const long long busy = ((long long)p.rows * (p.d / 16) * share + kMergeThreads - 1) / kMergeThreads;
+    long long per_tile = 16ll * num_sms / p.slots;
     per_tile = per_tile > busy ? busy : per_tile < 1 ? 1 : per_tile;
     const long long items = per_tile * p.slots, grid = 8ll * num_sms;
     cudaLaunchConfig_t cfg = {};
