@@ -41,6 +41,7 @@ struct PagedProblem {
     int slots;       // CTAs that share the work
     int min_piece;   // fewest 64-key blocks worth a CTA of their own
     int cost;        // what a tile costs beside its blocks, in blocks
+    int warps;       // warps of a CTA (paged_few)
     int whole;       // blocks that a CTA may walk beyond an even share before splitting tiles pays
     float scale_log2;
     unsigned long long wait_ns;
@@ -57,7 +58,9 @@ enum PagedKernel { kPagedRows = 0, kPagedFew = 1, kPagedTc = 2, kPagedTile = 3 }
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms);
 // CTAs of the streaming kernels that fit an SM, by the rows of a unit.
 constexpr int paged_rows_ctas(int rows) { return rows <= 4 ? 2 : 1; }
-constexpr int paged_few_ctas(int d, int rows) { return d == 64 && rows <= 16 ? 2 : 1; }
+constexpr int paged_few_ctas(int d, int rows, int warps) {
+    return (d == 64 ? rows <= 16 ? 16 : 12 : 8) / warps;
+}
 // Scratch of one call: partial results of split tiles (0: nothing is split).
 size_t paged_workspace_bytes(const PagedProblem &p);
 cudaError_t launch_paged_rows(const PagedProblem &p, sa_dtype dtype, cudaStream_t stream);

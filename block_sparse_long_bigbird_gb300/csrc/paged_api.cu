@@ -34,15 +34,19 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
         p.rows = (int)rows;
         per_sm = paged_rows_ctas(p.rows);
         p.min_piece = 4;
-        p.cost = 1;
+        p.cost = 4;
         block_ns = dtype == SA_FP32 ? p.d / 64 * (450 + 130 * p.rows) : p.d == 64 ? 450 : 550;
     } else if (dtype == SA_BF16 && !force_simt && rows <= kFewRows) {
         kind = kPagedFew;
         p.tpt = p.tpt_half = p.m;
         p.rows = (int)rows;
-        per_sm = paged_few_ctas(p.d, p.rows);
+        // CTAs of four warps where there are tiles for all of them, so that others stream
+        // while one starts or joins its unit, and of as many as registers allow else: 64 sequences of 900 tokens, 8 key heads, 4
+        // rows, d = 128, take 50 us, 58 with eight warps; one sequence 17.8 and 15.1.
+        p.warps = (long long)p.B * p.Hkv >= 2ll * num_sms ? 4 : p.d == 64 && rows > 16 ? 12 : 8;
+        per_sm = paged_few_ctas(p.d, p.rows, p.warps);
         p.min_piece = 4;
-        p.cost = 1;
+        p.cost = 4;
         block_ns = p.d == 64 ? 450 : 650;
         split_ns = 14000;
     } else if (dtype == SA_BF16 && !force_simt) {
@@ -74,7 +78,8 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     // fp32 with four rows 900 keys 34 and 21. 1000 tokens with a window of 512 over
     // 8192 keys, 12 heads, four sequences: 34 and 62.
     // The device decides by the lengths. The host leaves plan and join out where
-    // splitting would not pay with the longest walks: no tile walks more than its table
+    // splitting would not pay if every tile took the longest walk, and that is not so
+    // long that uneven lengths would make up for it. No tile walks more than its table
     // row or, without dilation, its window and the blocks of the global positions
     // (some 16 to a block).
     p.whole = split_ns / block_ns;
@@ -88,7 +93,7 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     const long long ctas = (long long)num_sms * per_sm;
     const long long pieces = tiles * (longest / p.min_piece + 1);
     const long long most = pieces < ctas ? pieces : ctas;
-    p.cut = (tiles + ctas - 1) / ctas * longest - tiles * longest / most > p.whole;
+    p.cut = (tiles + ctas - 1) / ctas * longest - tiles * longest / most > p.whole || longest > 3ll * p.whole;
     p.slots = (int)(p.cut ? most : tiles < ctas ? tiles : ctas);
     return kind;
 }

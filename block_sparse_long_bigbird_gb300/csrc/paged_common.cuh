@@ -220,7 +220,7 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
             long long v = 0;
             if (b < p.B) {
                 const int q = P.q[b], s = P.s[b], tiles = (q + p.tpt - 1) / p.tpt;
-                v = (long long)p.Hkv * (all_tiles - tiles);  // tiles without tokens: one each
+                v = (long long)p.Hkv * (all_tiles - tiles) * p.cost;  // tiles without tokens
                 if (!p.dilation) {
                     const int len = tiles > 0 ? tile_length(p, P, q, s, 1) : 0;
                     v += (long long)p.Hkv * tiles * len;
@@ -289,7 +289,7 @@ struct Tile {
 
     __device__ __forceinline__ void place(const PagedProblem &p) {
         live = hk < p.Hkv;
-        end = begin + (live ? len : 1);
+        end = begin + (live ? len : p.cost);
         // the longest sweeps first
         t0 = (live ? tiles - 1 - i : tiles + i % ((p.m + p.tpt - 1) / p.tpt - tiles)) * p.tpt;
     }
@@ -344,8 +344,9 @@ __device__ __forceinline__ Tile find_tile(const PagedProblem &p, const Plan &P, 
             }
         }
     }
-    T.i = (int)(T.hk < p.Hkv ? divide(off, T.len) : off);
-    T.begin += T.hk < p.Hkv ? (long long)T.i * T.len : off;
+    const int len = T.hk < p.Hkv ? T.len : p.cost;
+    T.i = (int)divide(off, len);
+    T.begin += (long long)T.i * len;
     T.place(p);
     return T;
 }
@@ -407,7 +408,7 @@ struct Units {
             from = v;
             stop = T.end > end ? end : T.end;
             U.hk = T.head(p);
-            U.split = from > T.begin || stop < T.end;
+            U.split = T.live && (from > T.begin || stop < T.end);
             U.slot = 2 * c + (from == T.begin);
             v = stop;
         }

@@ -33,7 +33,6 @@
 namespace sa {
 namespace {
 
-constexpr int kFewWarps = 8;
 constexpr int kItem = 16;    // keys a warp takes at a time
 constexpr float kGrow = 8.f;  // growth of a maximum (log2) that rescales the sums
 constexpr int kStages = 2;   // items in flight per warp
@@ -63,26 +62,26 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <int D, int NT>
+template <int D, int NT, int W>
 struct Few {
-    static constexpr int ctas = paged_few_ctas(D, 8 * NT);  // per SM
+    static constexpr int ctas = paged_few_ctas(D, 8 * NT, W);  // per SM
     static constexpr int pieces = kItem * D * 2 * 2 / 512;  // a lane's 16-byte pieces of an item: K, then V
     static constexpr int f4 = NT * D / 16;                  // float4 of a lane's sums
     static constexpr int stages = kStages * pieces * 512, results = f4 * 512 + NT * 64;
     static constexpr int ring = stages > results ? stages : results;  // bytes per warp
     static size_t smem(const PagedProblem &p) {
-        return (size_t)kFewWarps * ring + sizeof(UnitRoom) + 16 + plan_bytes(p.B, p.ng, p.Hkv);
+        return (size_t)W * ring + sizeof(UnitRoom) + 16 + plan_bytes(p.B, p.ng, p.Hkv);
     }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(const __grid_constant__ PagedProblem p) {
-    using C = Few<D, NT>;
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32, Few<D, NT, W>::ctas) paged_few(const __grid_constant__ PagedProblem p) {
+    using C = Few<D, NT, W>;
     using bf16 = __nv_bfloat16;
     constexpr int SETS = D / 64, CH = D / 32;
     constexpr int PK = D / 8;  // 16-byte pieces of a key
     extern __shared__ __align__(16) uint8_t smem[];
-    UnitRoom *room = reinterpret_cast<UnitRoom *>(smem + kFewWarps * C::ring);
+    UnitRoom *room = reinterpret_cast<UnitRoom *>(smem + W * C::ring);
     uint32_t *bad = reinterpret_cast<uint32_t *>(room + 1);  // rows to be computed again: of this unit, of the next
     Plan P = plan_at(bad + 4, p.B, p.ng, p.Hkv);
     make_plan(p, P);
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
             Item x[kStages + 1];
             x[0] = next;
 #pragma unroll
-            for (int s = 1; s <= kStages; ++s) x[s] = item_at(4 * U.e0 + warp + s * kFewWarps);
+            for (int s = 1; s <= kStages; ++s) x[s] = item_at(4 * U.e0 + warp + s * W);
 #pragma unroll
             for (int s = 0; s < kStages; ++s) w[s] = fetch(x[s], s);
             next = x[kStages];
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
         }
         int st = 0;
 #pragma unroll 1
-        for (int i = 4 * U.e0 + warp; i < i_end; i += kFewWarps) {
+        for (int i = 4 * U.e0 + warp; i < i_end; i += W) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             __syncwarp();
             const uint4 *at = ring + st * (C::pieces * 32);
@@ -227,9 +226,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
                     for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], k0.z, k1.z, k0.w, k1.w, q[nt][c].z, q[nt][c].w);
                 }
                 uint32_t hi[NT][2], lo[2];  // weights as the right operand
+                bool up = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    bool up = false;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t sees =
@@ -238,7 +237,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
                         s[nt][2 + x] = (sees >> (n + 8)) & 1u ? s[nt][2 + x] * p.scale_log2 : -CUDART_INF_F;
                         up |= fmaxf(s[nt][x], s[nt][2 + x]) > m[nt][x] + kGrow;
                     }
-                    if (__any_sync(kAllLanes, up)) {
+                }
+                if (__any_sync(kAllLanes, up)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
                         float f[2];
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
@@ -253,6 +255,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
 #pragma unroll
                         for (int i = 0; i < SETS * 16; ++i) acc[nt][i / 16][(i / 4) % 4][i % 4] *= f[i & 1];
                     }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const float ref = m[nt][x] == -CUDART_INF_F ? 0.f : m[nt][x];
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
 #pragma unroll
             for (int s = 0; s + 1 < kStages; ++s) w[s] = w[s + 1];
             const Item x = next;
-            next = item_at(i + (kStages + 1) * kFewWarps);
+            next = item_at(i + (kStages + 1) * W);
             w[kStages - 1] = fetch(x, st);
             st = st + 1 == kStages ? 0 : st + 1;
         }
@@ -319,19 +324,19 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
         if (tid == 0) fill_room(p, P, room, k ^ 1);
         __syncthreads();
         if (tid == 0) bad[k ^ 1] = 0u;
-        for (int idx = tid; idx < C::f4 * 32; idx += kFewWarps * 32) {
+        for (int idx = tid; idx < C::f4 * 32; idx += W * 32) {
             const int ln = idx & 31, i = idx >> 5, f = i & 1, set = (i >> 1) % SETS, part = (i >> 1) / SETS;
             const int row = 8 * (part >> 1) + 2 * (ln & 3) + (part & 1), col = set * 64 + (ln >> 2) * 8 + 4 * f;
             if (row >= p.rows) continue;
             float mx = -CUDART_INF_F;
 #pragma unroll
-            for (int v = 0; v < kFewWarps; ++v)
+            for (int v = 0; v < W; ++v)
                 mx = fmaxf(mx, reinterpret_cast<const float *>(smem + v * C::ring + C::f4 * 512)[row]);
             const float ref = mx == -CUDART_INF_F ? 0.f : mx;
             float ls = 0.f;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int v = 0; v < kFewWarps; ++v) {
+            for (int v = 0; v < W; ++v) {
                 const float *jw = reinterpret_cast<const float *>(smem + v * C::ring + C::f4 * 512);
                 const float4 y = reinterpret_cast<const float4 *>(smem + v * C::ring)[idx];
                 const float g = ptx::ex2(jw[row] - ref);
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
         __syncthreads();
         const uint32_t again = bad[k];
         if (again) {
-            for (int r = warp; r < p.rows; r += kFewWarps) {
+            for (int r = warp; r < p.rows; r += W) {
                 if (!((again >> r) & 1u)) continue;
                 int t, head;
                 row_token(p, U, r, p.tpt, t, head);
@@ -373,28 +378,32 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<D, NT>::ctas) paged_few(co
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, int W>
 cudaError_t launch_few(const PagedProblem &p, cudaStream_t stream) {
-    const size_t smem = Few<D, NT>::smem(p);
+    const size_t smem = Few<D, NT, W>::smem(p);
     static std::atomic<bool> done[64];
-    auto kern = paged_few<D, NT>;
+    auto kern = paged_few<D, NT, W>;
     cudaError_t e = allow_smem(kern, done, smem);
     if (e != cudaSuccess) return e;
-    kern<<<p.slots, kFewWarps * 32, smem, stream>>>(p);
+    kern<<<p.slots, W * 32, smem, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int D, int NT, int W>
+cudaError_t launch_few_w(const PagedProblem &p, cudaStream_t stream) {
+    return p.warps == 4 ? launch_few<D, NT, 4>(p, stream) : launch_few<D, NT, W>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_few(const PagedProblem &p, cudaStream_t stream) {
-    const int nt = (p.rows + 7) / 8;
     if (p.d == 64)
-        return nt == 1   ? launch_few<64, 1>(p, stream)
-               : nt == 2 ? launch_few<64, 2>(p, stream)
-                         : launch_few<64, 3>(p, stream);
-    return nt == 1   ? launch_few<128, 1>(p, stream)
-           : nt == 2 ? launch_few<128, 2>(p, stream)
-                     : launch_few<128, 3>(p, stream);
+        return p.rows <= 8    ? launch_few_w<64, 1, 8>(p, stream)
+               : p.rows <= 16 ? launch_few_w<64, 2, 8>(p, stream)
+                              : launch_few_w<64, 3, 12>(p, stream);
+    return p.rows <= 8    ? launch_few_w<128, 1, 8>(p, stream)
+           : p.rows <= 16 ? launch_few_w<128, 2, 8>(p, stream)
+                          : launch_few_w<128, 3, 8>(p, stream);
 }
 
 }  // namespace sa
