@@ -27,7 +27,7 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     int per_sm = 1;
     // ns: a 64-key block in a CTA that has the SM to itself (or its usual share),
     // and what splitting tiles adds to a call (more units, and the join)
-    int block_ns, split_ns = 8000;
+    int block_ns, split_ns = 12000;
     if (rows <= (dtype == SA_FP32 ? kRowsFp32 : kRowsBf16)) {
         kind = kPagedRows;
         p.tpt = p.tpt_half = p.m;
@@ -215,8 +215,13 @@ size_t sa_longformer_paged_workspace_bytes(int B, int Hq, int Hkv, int m, int d,
     sa::PagedProblem p = {};
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.m = m; p.d = d; p.page = page; p.max_pages = max_pages;
     p.half = (int)sa::kPagedMaxLen;
-    sa::paged_shape(p, dtype, sa::api_force_simt(), sms);
-    return sa::paged_workspace_bytes(p);
+    size_t most = 0;  // whichever kernel SA_OPT_FORCE_SIMT chooses by then
+    for (int simt = 0; simt < 2; ++simt) {
+        sa::paged_shape(p, dtype, simt != 0, sms);
+        const size_t n = sa::paged_workspace_bytes(p);
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 sa_status sa_cache_append(const void *K_new, const void *V_new, void *K_pages, void *V_pages, int B, int Hkv, int m,

@@ -29,7 +29,7 @@ struct TileSmem {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kTT) paged_tile(const __grid_constant__ PagedProblem p) {
+__global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_constant__ PagedProblem p) {
     using L = TileSmem<T, D>;
     constexpr int VE = 16 / sizeof(T);
     constexpr int ND = D / 64;  // 4-wide output columns per thread

@@ -11,9 +11,14 @@ are always changed in place. Nothing here waits for the device: what a kernel
 finds wrong in a table or a list is reported by ``get_last_device_status``.
 """
 
+import functools
+
 import torch
 
 from . import _lib
+
+# torch's allocation without its dispatcher, which costs 4 us of a call of 16; on the current device only
+_new_cuda = getattr(torch._C._dynamo.guards, "_empty_strided_cuda", None)
 
 _DTYPE = {torch.bfloat16: _lib.SA_BF16, torch.float32: _lib.SA_FP32}
 _INT = torch.int32
@@ -33,21 +38,24 @@ def _call(name, device, stream, *args):
         raise _lib.SparseAttnError(st, name)
 
 
-def _scratch(n_bytes, device, stream):
-    """Workspace of one call, from torch's allocator; kept from reuse until `stream` is done with it."""
-    if n_bytes == 0:
-        return None
-    ws = torch.empty(n_bytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
-
-
-def _fresh(like, stream):
-    t = torch.empty_like(like)
+def _new(shape, strides, dtype, device, stream):
+    """An uninitialised tensor, kept from reuse until `stream` is done with it."""
+    if _new_cuda is not None and torch._C._cuda_getDevice() == device.index:
+        t = _new_cuda(shape, strides, dtype)
+    else:
+        t = torch.empty_strided(shape, strides, dtype=dtype, device=device)
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _scratch(n_bytes, device, stream):
+    """Workspace of one call."""
+    return None if n_bytes == 0 else _new((n_bytes,), (1,), torch.uint8, device, stream)
+
+
+def _fresh(like, stream):
+    return _new(tuple(like.shape), like.stride(), like.dtype, like.device, stream)
 
 
 def _ptr(t):
@@ -109,7 +117,7 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     max_pages = block_table.shape[1]
     dt = _DTYPE[Q.dtype]
     if workspace is None:
-        workspace = _scratch(_workspace_bytes(dev, B, Hq, Hkv, m, d, page, max_pages, dt), dev, stream)
+        workspace = _scratch(_workspace_bytes(dev.index, B, Hq, Hkv, m, d, page, max_pages, dt), dev, stream)
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on Q's device")
     if out is None:
@@ -123,12 +131,10 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     return out
 
 
-def _workspace_bytes(device, *sizes):
-    fn = _lib.lib().sa_longformer_paged_workspace_bytes
-    if torch._C._cuda_getDevice() == device.index:
-        return fn(*sizes)
-    with torch.cuda.device(device):
-        return fn(*sizes)
+@functools.lru_cache(maxsize=1024)  # the sizes and the device's number of SMs are all it depends on
+def _workspace_bytes(index, *sizes):
+    with torch.cuda.device(index):
+        return _lib.lib().sa_longformer_paged_workspace_bytes(*sizes)
 
 
 def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None):
@@ -136,7 +142,7 @@ def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None)
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    return _workspace_bytes(dev, B, Hq, Hkv, m, d, page, max_pages, _DTYPE[dtype])
+    return _workspace_bytes(dev.index, B, Hq, Hkv, m, d, page, max_pages, _DTYPE[dtype])
 
 
 def cache_append(K_new, V_new, K_pages, V_pages, block_table, seq_lens, q_lens=None, stream=None):
@@ -144,11 +150,11 @@ def cache_append(K_new, V_new, K_pages, V_pages, block_table, seq_lens, q_lens=N
     _pools(K_pages, V_pages, (4,))
     num_pages, Hkv, page, d = K_pages.shape
     _new_rows("K_new", K_new, K_pages, Hkv)
-    _new_rows("V_new", V_new, K_pages, Hkv)
     B, _, m, _ = K_new.shape
-    if V_new.shape != K_new.shape:
-        raise ValueError("K_new and V_new must share shape")
     dev = K_pages.device
+    if V_new.shape != K_new.shape or V_new.dtype is not K_new.dtype or V_new.device != dev \
+            or not V_new.is_contiguous():
+        raise ValueError("V_new must be contiguous and match K_new in shape, dtype and device")
     _ints("block_table", block_table, dev, B, -1)
     _ints("seq_lens", seq_lens, dev, B)
     if q_lens is not None:

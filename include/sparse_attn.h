@@ -506,9 +506,10 @@ sa_status bigbird_attn_fwd_noalloc(const void *Q, const void *K, const void *V, 
  *   longformer_attn_fwd_ex. global_idx: DEVICE int32 [n_global], strictly
  *   increasing positions, the same for every sequence; positions past a
  *   sequence's end do not matter. n_global <= 512.
- * Numerics: bf16 inputs: fp32 scores, softmax and sums; with more than 4 query
+ * Numerics: bf16 inputs: fp32 scores, softmax and sums; with more than 8 query
  *   rows per key head (m * Hq / Hkv) the weights are rounded to bf16 for the
- *   tensor cores, as in the calls above. fp32: fp32 throughout.
+ *   matrix instructions, as in the calls above, and with 2 to 8 rows to the sum
+ *   of two bf16 numbers (relative 2^-17). fp32: fp32 throughout.
  *   Deterministic: no atomics on values; splits are joined in a fixed order.
  * workspace: sa_longformer_paged_workspace_bytes bytes (0: none needed), for
  *   the partial results of long sweeps cut into pieces.
@@ -524,8 +525,8 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
                                     const int32_t *global_idx, int n_global,
                                     void *workspace, size_t workspace_bytes,
                                     sa_dtype dtype, sa_stream_t stream);
-/* Scratch bytes of such a call on the current device (0 also for invalid
- * sizes). The option SA_OPT_FORCE_SIMT must be the same for both calls. */
+/* Scratch bytes of such a call on the current device, whatever its other
+ * arguments and options (0 also for invalid sizes). */
 size_t sa_longformer_paged_workspace_bytes(int B, int Hq, int Hkv, int m, int d, int page, int max_pages,
                                            sa_dtype dtype);
 
