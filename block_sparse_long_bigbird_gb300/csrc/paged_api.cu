@@ -93,7 +93,7 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     const long long ctas = (long long)num_sms * per_sm;
     const long long pieces = tiles * (longest / p.min_piece + 1);
     const long long most = pieces < ctas ? pieces : ctas;
-    p.cut = (tiles + ctas - 1) / ctas * longest - tiles * longest / most > p.whole || longest > 3ll * p.whole;
+    p.cut = (tiles + ctas - 1) / ctas * longest - tiles * longest / most > p.whole || longest > 2ll * p.whole;
     p.slots = (int)(p.cut ? most : tiles < ctas ? tiles : ctas);
     return kind;
 }

@@ -204,6 +204,8 @@ __global__ void __launch_bounds__(W * 32, Few<D, NT, W>::ctas) paged_few(const _
 #pragma unroll
             for (int i = 0; i < SETS * 16; ++i) acc[nt][i / 16][(i / 4) % 4][i % 4] = 0.f;
         }
+        if (tid == 0) fill_room(p, P, room, k ^ 1);  // while the first items are on their way
+        __syncwarp();
         int st = 0;
 #pragma unroll 1
         for (int i = 4 * U.e0 + warp; i < i_end; i += W) {
@@ -321,7 +323,6 @@ __global__ void __launch_bounds__(W * 32, Few<D, NT, W>::ctas) paged_few(const _
                     jm[8 * NT + 8 * nt + 2 * quad + x] = sum;
                 }
             }
-        if (tid == 0) fill_room(p, P, room, k ^ 1);
         __syncthreads();
         if (tid == 0) bad[k ^ 1] = 0u;
         for (int idx = tid; idx < C::f4 * 32; idx += W * 32) {

@@ -197,6 +197,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 8 ? 1 : 2)
         Masks km = masks_of(now);
         uint4 kw[CH], vw[CH];
         if (AHEAD && now.i < i_end) load(now, km.any, 0, kw, vw);
+        if (tid == 0) fill_room(p, P, room, k ^ 1);  // while the first items are on their way
+        __syncwarp();
         while (now.i < i_end) {
             const Item third = item_at(after.i + kRowsWarps);
             Masks kn = km;
@@ -248,7 +250,6 @@ __global__ void __launch_bounds__(kRowsWarps * 32, R == 8 ? 1 : 2)
                 jl[warp * R + r] = l[r];
             }
         }
-        if (tid == 0) fill_room(p, P, room, k ^ 1);
         __syncthreads();
         // and the warps, in order
         for (int idx = tid; idx < p.rows * D; idx += kRowsWarps * 32) {
@@ -291,18 +292,17 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const PagedProblem 
     extern __shared__ __align__(16) uint8_t smem[];
     Plan P = plan_at(smem, p.B, p.ng, p.Hkv);
     make_plan(p, P);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the sweeps' results are visible from here on
-    if (!P.cut) return;
     const int groups = p.rows * (D / 16);
     const int half_rows = p.tpt_half * p.group;
     const long long n_items = (long long)(P.ctas - 1) * per_tile;
-    for (long long w = blockIdx.x; w < n_items; w += gridDim.x) {
+    for (long long w = blockIdx.x; w < n_items && P.cut; w += gridDim.x) {
         const int c = 1 + (int)(w / per_tile), chunk = (int)(w % per_tile);
         const long long at = cta_begin(P, c);
         const Tile tile = find_tile(p, P, at);
         if (!tile.live || tile.begin == at || tile.begin < cta_begin(P, c - 1)) continue;
         const int ns = cta_of(P, tile.end - 1, c) - c + 2;  // pieces: slot 2 c - 1, then 2 c, 2 c + 2, ...
         const int share = ns > kMergeMany ? kMergeShare : 1;
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the sweeps' results are visible from here on
         auto slot = [&](int k) { return k == 0 ? 2 * c - 1 : 2 * (c + k - 1); };
         for (int idx = chunk * kMergeThreads + (int)threadIdx.x; idx - (int)threadIdx.x < groups * share;
              idx += per_tile * kMergeThreads) {
@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge(const PagedProblem 
             store16<T>(static_cast<T *>(p.O) + (((size_t)tile.b * p.Hq + head) * p.m + t) * D + 16 * k16, acc);
         }
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // whatever follows this launch follows the sweeps too
 }
 
 template <typename T, int D, int R>

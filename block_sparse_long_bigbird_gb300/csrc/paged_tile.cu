@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
 #pragma unroll
             for (int x = 0; x < 4 * ND; ++x) acc[r][x] = 0.f;
         }
+        if (tid == kTT - 1) fill_room(p, P, room, room_k ^ 1);  // a warp without masks to work out
         for (int e = U.e0; e < U.e1; ++e) {
             const int blk = entry_block(P, U, e), j0 = blk << 6;
             __syncthreads();  // the previous step is done with KV, Ps and masks
@@ -187,7 +188,6 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
                 }
             }
         }
-        if (tid == 0) fill_room(p, P, room, room_k ^ 1);
         __syncthreads();
         if (tid < kTR) flags[tid] = 0;
         __syncthreads();
