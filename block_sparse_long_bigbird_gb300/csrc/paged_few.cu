@@ -24,8 +24,8 @@
 // clocks and SM), so their number counts: with rows down instead of across, one
 // tile is 16 rows and takes twice as many.
 // Up to 8 rows P V is computed with P as the sum of two bf16 numbers (relative
-// 2^-17); with more, P is rounded to bf16 (2^-9 of each weight), as in the
-// kernel for many rows.
+// 2^-16), which the rate allows; with more, P is rounded to bf16 (2^-8 of each
+// weight), as in the kernel for many rows.
 // A row that does not see a key multiplies its value by 0; where that value is
 // infinite or NaN the row's sums come out so, and exact_row computes it again.
 #include "paged_common.cuh"

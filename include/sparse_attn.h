@@ -509,7 +509,7 @@ sa_status bigbird_attn_fwd_noalloc(const void *Q, const void *K, const void *V, 
  * Numerics: bf16 inputs: fp32 scores, softmax and sums; with more than 8 query
  *   rows per key head (m * Hq / Hkv) the weights are rounded to bf16 for the
  *   matrix instructions, as in the calls above, and with 2 to 8 rows to the sum
- *   of two bf16 numbers (relative 2^-17). fp32: fp32 throughout.
+ *   of two bf16 numbers (relative 2^-16). fp32: fp32 throughout.
  *   Deterministic: no atomics on values; splits are joined in a fixed order.
  * workspace: sa_longformer_paged_workspace_bytes bytes (0: none needed), for
  *   the partial results of long sweeps cut into pieces.

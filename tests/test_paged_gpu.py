@@ -67,6 +67,49 @@ def test_long_sweeps_are_split_and_joined(m, Hq, Hkv, dtype):
     attend_and_check(Q, K, V, table, lens, None, 8000, None, None, dtype)
 
 
+# B, Hkv: few tiles (large CTAs) and many (small ones)
+@pytest.mark.parametrize("B,Hkv", [(2, 1), (110, 3)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,group", [(1, 2), (7, 1), (2, 4), (1, 9), (4, 4), (1, 17), (23, 1), (3, 8), (5, 5)])
+def test_few_rows_per_key_head(m, group, d, B, Hkv):
+    """2 to 8 rows: weights as the sum of two bf16 numbers; 9 to 24: bf16 weights; one more goes to the 128-row tiles."""
+    lens = [max(m, (37 * i + 5) % 190) for i in range(B)]
+    lens[0], lens[1] = 190, m
+    q = None if m == 1 else [m] + [i % (m + 1) for i in range(1, B)]
+    Q, K, V, table = make_cache(m + group + d, B, Hkv * group, Hkv, m, d, 32, lens, sigma=1.5)
+    attend_and_check(Q, K, V, table, lens, q, 128, [0, 1, 70], None, weights=2.0 ** -8 if m * group > 8 else 2.0 ** -16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("m,Hq,Hkv", [(1, 2, 2), (5, 4, 2), (3, 16, 2), (70, 4, 2)])
+def test_tables_wider_than_the_sequences(m, Hq, Hkv, dtype):
+    """Room for long sequences, but short ones (whole tiles in turn), then one long among short and empty ones."""
+    for lens, q in (([100, m, 77], None), ([5000, 0, m, 333, 40], [m, 0, m, 0, m // 2])):
+        lens = [max(n, 0 if q is None else k) for n, k in zip(lens, q or lens)]
+        Q, K, V, table = make_cache(15, len(lens), Hq, Hkv, m, 64, 64, lens, dtype, width=700)
+        attend_and_check(Q, K, V, table, lens, q, 20000, None, None, dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 4, 12])
+def test_values_beyond_the_largest_number_in_a_split_sweep(group, d):
+    """A row that sees an infinity or NaN has it; rows of the same tile that do not see it are as without it."""
+    lens, m = [4000], 2
+    Q, K, V, table = make_cache(51, 1, group, 1, m, d, 16, lens)
+    clean = attend_and_check(Q, K, V, table, lens, None, 9000)
+    Vc = V.clone()
+    last = lens[0] - 1
+    Vc[int(table[0, last // 16]), 0, last % 16, 0] = float("inf")
+    Vc[int(table[0, last // 16]), 0, last % 16, 1] = float("nan")
+    got = sa.longformer_attn_paged_fwd(*dev(Q, K, Vc, table, ints(lens)), 9000)
+    a, b = f64(got), f64(clean)
+    assert np.isposinf(a[:, :, 1, 0]).all() and np.isnan(a[:, :, 1, 1]).all()
+    # summed again by the definition: the weights' rounding of one (2^-8 of a mean of |v| < 2), the results' of both
+    assert np.allclose(a[:, :, 0], b[:, :, 0], rtol=2.0 ** -7, atol=2.0 ** -7)
+    assert np.allclose(a[:, :, 1, 2:], b[:, :, 1, 2:], rtol=2.0 ** -7, atol=2.0 ** -7)
+    assert sa.get_last_device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("m", [1, 3, 70])
 def test_missing_pages_and_empty_rows(m, dtype):
@@ -191,6 +234,27 @@ def test_offsets_past_32_bits(m, Hq):
     sa.cache_copy_pages(K, V, ints([P - 1]).cuda(), ints([P - 9]).cuda())
     assert torch.equal(V[P - 9].nan_to_num(7.0), V[P - 1].nan_to_num(7.0))
     assert sa.get_last_device_status() == 0
+
+
+@pytest.mark.parametrize("m,Hq", [(40, 2), (300, 4)])
+def test_a_wait_that_runs_out_ends_the_call_and_the_next_one_is_exact(m, Hq):
+    lens = [3000, 700]
+    Q, K, V, table = make_cache(61, 2, Hq, 2, m, 64, 64, lens)
+    Qd, Kd, Vd, T, L = dev(Q, K, V, table, ints(lens))
+    want = sa.longformer_attn_paged_fwd(Qd, Kd, Vd, T, L, 8000)
+    torch.cuda.synchronize()
+    assert sa.get_last_device_status() == 0
+    sa.set_option(sa.SA_OPT_WAIT_LIMIT, 1)  # 1 microsecond: waits on copies and MMAs run out
+    try:
+        for _ in range(3):
+            sa.longformer_attn_paged_fwd(Qd, Kd, Vd, T, L, 8000)
+        torch.cuda.synchronize()  # every wait and every drain is bounded
+    finally:
+        sa.set_option(sa.SA_OPT_WAIT_LIMIT, 0)
+    got = sa.longformer_attn_paged_fwd(Qd, Kd, Vd, T, L, 8000)
+    torch.cuda.synchronize()
+    assert sa.get_last_device_status() in (_lib.SA_OK, _lib.SA_ERR_TIMEOUT)
+    assert sa.get_last_device_status() == 0 and torch.equal(got, want)
 
 
 def test_many_sequences_and_many_globals():
