@@ -39,14 +39,20 @@ def _call(name, device, stream, *args):
 
 
 def _new(shape, strides, dtype, device, stream):
-    """An uninitialised tensor, kept from reuse until `stream` is done with it."""
-    if _new_cuda is not None and torch._C._cuda_getDevice() == device.index:
-        t = _new_cuda(shape, strides, dtype)
-    else:
-        t = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    """An uninitialised tensor for a call on `stream`.
+
+    Memory of that stream, so that nothing that the current one still has to do may touch it; the current one, where
+    the caller goes on, keeps it from reuse too.
+    """
     if stream is not None:
-        t.record_stream(stream)
-    return t
+        caller = torch.cuda.current_stream(device)
+        with torch.cuda.stream(stream):
+            t = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+        t.record_stream(caller)
+        return t
+    if _new_cuda is not None and torch._C._cuda_getDevice() == device.index:
+        return _new_cuda(shape, strides, dtype)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def _scratch(n_bytes, device, stream):
@@ -114,6 +120,8 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     if global_idx is not None:
         _ints("global_idx", global_idx, dev, -1)
     n_global = 0 if global_idx is None else global_idx.numel()
+    if window > 0x7ffffffe:
+        window = 0x7ffffffe  # half of it is more than any position
     max_pages = block_table.shape[1]
     dt = _DTYPE[Q.dtype]
     if workspace is None:
@@ -247,7 +255,7 @@ def cache_trim(block_table, seq_lens, ref_count, page, reach, global_idx=None, o
         _ints("global_idx", global_idx, dev, -1)
     n_global = 0 if global_idx is None else global_idx.numel()
     table, refs = _outputs(out, (block_table, ref_count), stream)
-    _call("sa_cache_trim", dev, stream, num_pages, page, B, max_pages, reach,
+    _call("sa_cache_trim", dev, stream, num_pages, page, B, max_pages, min(reach, 0x7fffffff),
           global_idx.data_ptr() if n_global else None, n_global, block_table.data_ptr(), seq_lens.data_ptr(),
           ref_count.data_ptr(), table.data_ptr(), refs.data_ptr())
     return table, refs

@@ -188,6 +188,50 @@ def test_deterministic_and_independent_of_the_stream(m, Hq):
     assert sa.get_last_device_status() == 0
 
 
+def test_results_on_another_stream_are_not_in_memory_that_this_one_still_writes():
+    lens, m = [3000, 2100], 2100  # outputs of over a megabyte, which torch keeps apart from small ones
+    Q, K, V, table = make_cache(4, 2, 4, 2, m, 64, 64, lens)
+    Qd, Kd, Vd, T, L = dev(Q, K, V, table, ints(lens))
+    want = sa.longformer_attn_paged_fwd(Qd, Kd, Vd, T, L, 6000)
+    wide = torch.full((2, 600_000), -1, dtype=torch.int32, device="cuda")
+    wide[0, :2] = torch.tensor([3, 5], dtype=torch.int32)
+    refs = torch.ones(600_000, dtype=torch.int32, device="cuda")
+    rows, lens2 = ints([0]).cuda(), ints([100, 0]).cuda()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    scratch = sa.paged_workspace_bytes(2, 4, 2, m, 64, 64, T.shape[1], Qd.dtype)
+    old = [torch.empty_like(x) for x in (Qd, wide, refs) for _ in range(3)]
+    old += [torch.empty(scratch, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    for x in old:
+        x.fill_(7)  # (a kernel's first launch would wait for the sleep)
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # some 10 ms
+    for x in old:
+        x.fill_(77)
+    del old, x  # free again for this stream, while its fills are still to come
+    got = sa.longformer_attn_paged_fwd(Qd, Kd, Vd, T, L, 6000, stream=s)
+    new_table, new_lens, new_refs = sa.cache_free(wide, lens2, refs, rows, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert bool((new_table == -1).all()) and new_lens.tolist() == [0, 0]
+    assert int(new_refs.sum()) == 600_000 - 2 and sa.get_last_device_status() == 0
+
+
+def test_the_widest_windows():
+    lens = [300]
+    Q, K, V, table = make_cache(4, 1, 2, 2, 3, 64, 64, lens)
+    args = dev(Q, K, V, table, ints(lens))
+    want = sa.longformer_attn_paged_fwd(*args, 600)
+    for window in (2 ** 31 - 2, 2 ** 31, 2 ** 40):  # what C takes at most, and more
+        assert torch.equal(sa.longformer_attn_paged_fwd(*args, window), want)
+    refs = torch.ones(K.shape[0], dtype=torch.int32, device="cuda")
+    for reach in (2 ** 31 - 1, 2 ** 32 + 1):
+        t, r = sa.cache_trim(args[3], args[4], refs, 64, reach)
+        assert torch.equal(t, args[3]) and torch.equal(r, refs)
+
+
 @pytest.mark.parametrize("m,Hq", [(1, 2), (3, 8), (130, 4)])
 def test_captured_graphs_follow_the_lengths(m, Hq):
     # one graph, replayed while lengths, table and pools move on; two graphs replayed together
