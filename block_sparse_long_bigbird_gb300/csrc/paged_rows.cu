@@ -15,6 +15,11 @@
 // keys, and unwritten memory is never touched. Long sweeps are cut into units
 // by the plan; their partial results are joined by paged_merge in a fixed
 // order, so results do not depend on timing.
+//
+// Measured (16 sequences of 32768 keys, one row per key head): bf16, 8 key heads, d =
+// 64 172 us, 6.2 TB/s; d = 128 316 us, 6.8 TB/s (a plain copy: 6.7); fp32, 4 key heads,
+// 16384 keys, d = 128, 168 us, 6.4 TB/s, two rows 172, four 197, eight 375 (there the
+// multiply-adds bound it). The smallest call takes 5.5 us, half of it launch and plan.
 #include "paged_common.cuh"
 
 namespace sa {

@@ -1,6 +1,7 @@
 // Attention of many new tokens over a paged cache on the tensor cores (bf16):
-// chunks of a prompt, drafts, and single tokens whose query heads share a key
-// head.
+// chunks of a prompt, and whatever gives a key head more than 24 query rows.
+//
+//     O_r = sum_j w_rj V_j / sum_j w_rj,   w_rj = 2^(s_rj - m_r),   s = q . k log2(e) / sqrt(d)
 //
 // A unit's query rows (tokens x the query heads of one key head, up to 2 x 128)
 // are two MMA tiles of 128 rows that share every key and value they load: a
@@ -28,6 +29,15 @@
 // row's O not finite, and exact_row then computes that row again.
 // Roles' waits are bounded; on expiry the CTA latches SA_ERR_TIMEOUT, drains
 // its copies and MMAs, frees TMEM and exits.
+//
+// Measured: 4096 tokens at the end of 32768 keys, 16 query and 4 key heads, d =
+// 128: 805 us, 1280 TFLOP/s (0.65 of the measured bf16 rate); with as many key as
+// query heads, 2 x 2048 tokens over 16384 keys: d = 128 430 us, 1190 TFLOP/s, d = 64
+// 420 us, 615 TFLOP/s. A 64-key block of two tiles takes 1.0 us whatever d is: the
+// softmax bounds it (16384 exponentials per block, one thread per row), not the
+// tensor pipe (48% busy at d = 128) or the memory (3%). A window of 512, 4 x 4096
+// tokens, 12 heads, d = 64: 64 us; a unit of ten blocks costs 12.7 us there, 2.7 of
+// them to start and to finish.
 #include <cuda.h>
 
 #include <type_traits>
