@@ -106,13 +106,21 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     workspace: uint8 CUDA tensor of paged_workspace_bytes(...), or None to allocate it here.
     Rows past q_lens and rows that see no key are zeros.
     """
-    _pools(K_pages, V_pages, (4,))
-    num_pages, Hkv, page, d = K_pages.shape
-    _new_rows("Q", Q, K_pages, None)
-    B, Hq, m, _ = Q.shape
-    dev = Q.device
-    _ints("block_table", block_table, dev, B, -1)
-    _ints("seq_lens", seq_lens, dev, B)
+    dtype, dev, shape, strides = Q.dtype, Q.device, Q.shape, Q.stride()
+    pool, table = K_pages.shape, block_table.shape
+    # every test below in one expression; where it fails, the tests one by one say which
+    if not (len(shape) == len(pool) == 4 and V_pages.shape == pool and shape[3] == pool[3] and dtype in _DTYPE
+            and K_pages.dtype is dtype and V_pages.dtype is dtype and block_table.dtype is _INT and seq_lens.dtype is _INT
+            and K_pages.device == dev and V_pages.device == dev and block_table.device == dev and seq_lens.device == dev
+            and Q.is_cuda and Q.is_contiguous() and K_pages.is_contiguous() and V_pages.is_contiguous()
+            and block_table.is_contiguous() and seq_lens.is_contiguous()
+            and len(table) == 2 and table[0] == shape[0] and seq_lens.shape == shape[:1]):
+        _pools(K_pages, V_pages, (4,))
+        _new_rows("Q", Q, K_pages, None)
+        _ints("block_table", block_table, dev, shape[0], -1)
+        _ints("seq_lens", seq_lens, dev, shape[0])
+    num_pages, Hkv, page, d = pool
+    B, Hq, m, _ = shape
     if q_lens is not None:
         _ints("q_lens", q_lens, dev, B)
     if dilation is not None:
@@ -122,14 +130,14 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     n_global = 0 if global_idx is None else global_idx.numel()
     if window > 0x7ffffffe:
         window = 0x7ffffffe  # half of it is more than any position
-    max_pages = block_table.shape[1]
-    dt = _DTYPE[Q.dtype]
+    max_pages = table[1]
+    dt = _DTYPE[dtype]
     if workspace is None:
         workspace = _scratch(_workspace_bytes(dev.index, B, Hq, Hkv, m, d, page, max_pages, dt), dev, stream)
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on Q's device")
     if out is None:
-        out = _fresh(Q, stream)
+        out = _new(tuple(shape), strides, dtype, dev, stream)
     elif out.shape != Q.shape or out.dtype is not Q.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA tensor shaped and typed like Q")
     _call("longformer_attn_paged_fwd", dev, stream, Q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
@@ -155,21 +163,28 @@ def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None)
 
 def cache_append(K_new, V_new, K_pages, V_pages, block_table, seq_lens, q_lens=None, stream=None):
     """Write the new tokens' keys and values [B, Hkv, m, d] into their pages; returns (K_pages, V_pages)."""
-    _pools(K_pages, V_pages, (4,))
-    num_pages, Hkv, page, d = K_pages.shape
-    _new_rows("K_new", K_new, K_pages, Hkv)
-    B, _, m, _ = K_new.shape
-    dev = K_pages.device
-    if V_new.shape != K_new.shape or V_new.dtype is not K_new.dtype or V_new.device != dev \
-            or not V_new.is_contiguous():
-        raise ValueError("V_new must be contiguous and match K_new in shape, dtype and device")
-    _ints("block_table", block_table, dev, B, -1)
-    _ints("seq_lens", seq_lens, dev, B)
+    dtype, dev, shape = K_new.dtype, K_new.device, K_new.shape
+    pool, table = K_pages.shape, block_table.shape
+    if not (len(shape) == len(pool) == 4 and V_pages.shape == pool and V_new.shape == shape and shape[1] == pool[1]
+            and shape[3] == pool[3] and dtype in _DTYPE and V_new.dtype is dtype and K_pages.dtype is dtype
+            and V_pages.dtype is dtype and block_table.dtype is _INT and seq_lens.dtype is _INT
+            and V_new.device == dev and K_pages.device == dev and V_pages.device == dev and block_table.device == dev
+            and seq_lens.device == dev and K_new.is_cuda and K_new.is_contiguous() and V_new.is_contiguous()
+            and K_pages.is_contiguous() and V_pages.is_contiguous() and block_table.is_contiguous()
+            and seq_lens.is_contiguous() and len(table) == 2 and table[0] == shape[0] and seq_lens.shape == shape[:1]):
+        _pools(K_pages, V_pages, (4,))
+        _new_rows("K_new", K_new, K_pages, pool[1])
+        _new_rows("V_new", V_new, K_pages, pool[1])
+        if V_new.shape != shape:
+            raise ValueError("K_new and V_new must share shape")
+        _ints("block_table", block_table, dev, shape[0], -1)
+        _ints("seq_lens", seq_lens, dev, shape[0])
+    num_pages, Hkv, page, d = pool
+    B, _, m, _ = shape
     if q_lens is not None:
         _ints("q_lens", q_lens, dev, B)
     _call("sa_cache_append", dev, stream, K_new.data_ptr(), V_new.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
-          B, Hkv, m, d, page, num_pages, block_table.shape[1], block_table.data_ptr(), seq_lens.data_ptr(),
-          _ptr(q_lens), _DTYPE[K_pages.dtype])
+          B, Hkv, m, d, page, num_pages, table[1], block_table.data_ptr(), seq_lens.data_ptr(), _ptr(q_lens), _DTYPE[dtype])
     return K_pages, V_pages
 
 
