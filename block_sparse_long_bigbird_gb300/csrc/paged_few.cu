@@ -1,5 +1,5 @@
-// Attention of a few new tokens per sequence over a paged cache in bf16, up to
-// 16 rows per key head (rows = tokens x query heads of the key head).
+// Attention of a few new tokens per sequence over a paged cache in bf16, 2 to
+// 24 rows per key head (rows = tokens x query heads of the key head).
 //
 //     O_r = sum_j w_rj V_j / sum_j w_rj,   w_rj = 2^(s_rj - max_j s_rj),   s = q . k log2(e) / sqrt(d)
 //
@@ -16,13 +16,14 @@
 //   * the rows of O^T may stand in any order, so a lane reads 16-byte pieces of
 //     four value rows and pairs up their elements for four tiles; its sums end
 //     up as 8 neighbouring elements of two rows of O.
-// Copies (cp.async) go to a ring of the warp's own, three items deep: 192 KB in
-// flight per SM, and no barrier. A copy instruction takes whole lines: 64 bytes
-// of eight keys, which each lane would use itself, were fetched from L2 twice.
+// Copies (cp.async) go to a ring of the warp's own, two items deep: 128 KB in
+// flight per SM, and no barrier. (Three items leave L1, which the copies go
+// through, too little room: 64 sequences of 4096 keys, 8 key heads, d = 128, take
+// 207 us instead of 176.) A copy instruction takes whole lines: the 64 bytes of
+// eight keys that the lanes themselves would use were fetched from L2 twice.
 // Masked keys are copied as zeros without being read.
-// These instructions run at a tenth of the rate of the 128-row ones (one per 9.5
-// clocks and SM), so their number counts: with rows down instead of across, one
-// tile is 16 rows and takes twice as many.
+// With rows down instead of across a tile would be 16 rows and take twice the
+// matrix instructions for 8.
 // Up to 8 rows P V is computed with P as the sum of two bf16 numbers (relative
 // 2^-16), which the rate allows; with more, P is rounded to bf16 (2^-8 of each
 // weight), as in the kernel for many rows.
