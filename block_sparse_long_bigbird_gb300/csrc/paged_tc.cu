@@ -36,8 +36,11 @@
 // 420 us, 615 TFLOP/s. A 64-key block of two tiles takes 1.0 us whatever d is: the
 // softmax bounds it (16384 exponentials per block, one thread per row), not the
 // tensor pipe (48% busy at d = 128) or the memory (3%). A window of 512, 4 x 4096
-// tokens, 12 heads, d = 64: 64 us; a unit of ten blocks costs 12.7 us there, 2.7 of
-// them to start and to finish.
+// tokens, 12 heads, d = 64: 62 us; a unit of ten blocks takes 18400 clocks there: 2800 to
+// start (record, rows, first scores), 10500 in its steps, 2000 for the last product
+// and 3100 to write O. Units of one tile that see little pay more: the first chain's
+// warps join both O's and write them (2300 to 6000 clocks). Loading their next
+// queries ahead, into the place of the second tile, changed nothing.
 #include <cuda.h>
 
 #include <type_traits>
