@@ -18,7 +18,7 @@ import torch
 from . import _lib
 
 # torch's allocation without its dispatcher, which costs 4 us of a call of 16; on the current device only
-_new_cuda = getattr(torch._C._dynamo.guards, "_empty_strided_cuda", None)
+_new_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 _DTYPE = {torch.bfloat16: _lib.SA_BF16, torch.float32: _lib.SA_FP32}
 _INT = torch.int32
