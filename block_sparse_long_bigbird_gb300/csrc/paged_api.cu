@@ -41,8 +41,9 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
         p.tpt = p.tpt_half = p.m;
         p.rows = (int)rows;
         // CTAs of four warps where there are tiles for all of them, so that others stream
-        // while one starts or joins its unit, and of as many as registers allow else: 64 sequences of 900 tokens, 8 key heads, 4
-        // rows, d = 128, take 50 us, 58 with eight warps; one sequence 17.8 and 15.1.
+        // while one starts or joins its unit, and of as many as registers allow else: 64
+        // sequences of 900 tokens, 8 key heads, 4 rows, d = 128, take 50 us, 58 with eight
+        // warps; one sequence 17.8 and 15.1.
         p.warps = (long long)p.B * p.Hkv >= 2ll * num_sms ? 4 : p.d == 64 && rows > 16 ? 12 : 8;
         per_sm = paged_few_ctas(p.d, p.rows, p.warps);
         p.min_piece = 4;
@@ -192,6 +193,7 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
     const sa::PagedKernel kind = sa::paged_shape(p, dtype, sa::api_force_simt(), sms);
     const size_t need = sa::paged_workspace_bytes(p);
     if (need) {
+        if (ws_ok(workspace, workspace_bytes, need) != SA_OK) return SA_ERR_INVALID_ARG;
         p.part_o = static_cast<float *>(workspace);
         p.part_ml = reinterpret_cast<float2 *>(p.part_o + 2 * (size_t)p.slots * p.rows * p.d);
     }
