@@ -41,6 +41,7 @@ struct PagedProblem {
     int slots;       // CTAs that share the work
     int min_piece;   // fewest 64-key blocks worth a CTA of their own
     int cost;        // what a tile costs beside its blocks, in blocks
+    int listed;      // whether a tile's far global keys are walked side by side, 64 to an entry (paged_tile)
     int warps;       // warps of a CTA (paged_few)
     int whole;       // blocks that a CTA may walk beyond an even share before splitting tiles pays
     float scale_log2;

@@ -69,6 +69,7 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
         per_sm = p.d == 64 ? 4 : 2;
         p.min_piece = 2;
         p.cost = 1;
+        p.listed = 1;
         block_ns = p.d == 64 ? 7200 : 13000;
         split_ns = 20000;
     }
@@ -82,12 +83,12 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     // splitting would not pay if every tile took the longest walk, and that is not so
     // long that uneven lengths would make up for it. No tile walks more than its table
     // row or, without dilation, its window and the blocks of the global positions
-    // (some 16 to a block).
+    // (some 16 to a block, or listed 64 to an entry).
     p.whole = split_ns / block_ns;
     const long long tiles = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt);
     long long longest = (((long long)p.max_pages << p.log_page) + 63) >> 6;
     if (!p.dilation && p.half < longest << 6) {
-        const long long band = (((long long)p.half + p.tpt) >> 6) + 2 + ((p.ng + 15) >> 4);
+        const long long band = (((long long)p.half + p.tpt) >> 6) + 2 + (p.listed ? (p.ng + 63) >> 6 : (p.ng + 15) >> 4);
         longest = band < longest ? band : longest;
     }
     longest += p.cost;

@@ -125,12 +125,13 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 
 // Length on the common axis of one tile of a sequence for a key head of that
 // stride: an estimate of the blocks it walks (a sixteenth of the global
-// positions have a block of their own: most lie together), and its fixed cost.
+// positions have a block of their own: most lie together; listed ones are 64 to
+// an entry), and its fixed cost.
 // It decides how evenly the work is spread, nothing else.
 __device__ __forceinline__ int tile_length(const PagedProblem &p, const Plan &P, int q, int s, int stride) {
     const int all = (s + 63) >> 6;
     const long long span = (long long)head_reach(p, stride) + min(q, p.tpt);
-    const long long band = (span >> 6) + 2 + ((p.ng + 15) >> 4);
+    const long long band = (span >> 6) + 2 + (p.listed ? (p.ng + 63) >> 6 : (p.ng + 15) >> 4);
     return (band < all ? (int)band : all) + p.cost;
 }
 
@@ -357,7 +358,9 @@ struct Unit {
     int q, s;
     bool live, split;
     int slot;                    // partial-result slot (split)
-    int lo_blk, n_glob, e0, e1;  // entries [e0, e1): first the global blocks before lo_blk, then lo_blk ...
+    // entries [e0, e1): first the global blocks before lo_blk (or, listed, the global
+    // keys before it, 64 to an entry), then lo_blk ...
+    int lo_blk, n_glob, e0, e1;
 };
 
 // Is a position among the global ones?
@@ -365,6 +368,11 @@ __device__ __forceinline__ bool is_global(const Plan &P, const PagedProblem &p, 
     if (p.ng == 0) return false;
     const int i = lower_bound(P.gpos, p.ng, pos);
     return i < p.ng && P.gpos[i] == pos;
+}
+
+// Global positions before a unit's first block.
+__device__ __forceinline__ int far_globals(const PagedProblem &p, const Plan &P, const Unit &U) {
+    return p.ng ? lower_bound(P.gpos, p.ng, U.lo_blk << 6) : 0;
 }
 
 // The units of a CTA, in order: next() fills the following one and returns
@@ -426,7 +434,7 @@ struct Units {
             if (i < p.ng && P.gpos[i] <= p1) first = 0;
         }
         U.lo_blk = first >> 6;
-        U.n_glob = p.ng ? lower_bound(P.gblk, P.ngb, U.lo_blk) : 0;
+        U.n_glob = !p.ng ? 0 : p.listed ? (far_globals(p, P, U) + 63) >> 6 : lower_bound(P.gblk, P.ngb, U.lo_blk);
         const int n = U.n_glob + (p1 >> 6) - U.lo_blk + 1;
         U.e1 = n;
         if (U.split) {
@@ -593,13 +601,15 @@ __device__ __noinline__ float2 exact_row(const PagedProblem &p, const Plan &P, c
     }
     const Row r = make_row(p, P, U, head, t);
     float m = -CUDART_INF_F, l = 0.f;
+    const int far = p.listed ? far_globals(p, P, U) : 0;
     for (int e = U.e0; e < U.e1; ++e) {
-        const int blk = entry_block(P, U, e);
-        uint64_t w = row_mask(r, blk, global_bits(P, p, blk), ~0ull);
+        const bool listed = p.listed && e < U.n_glob;
+        const int blk = listed ? 0 : entry_block(P, U, e);
+        uint64_t w = listed ? low_bits(far - 64 * e) : row_mask(r, blk, global_bits(P, p, blk), ~0ull);
         while (w) {
             const int i = __ffsll((long long)w) - 1;
             w &= w - 1;
-            const int j = (blk << 6) + i;
+            const int j = listed ? P.gpos[64 * e + i] : (blk << 6) + i;
             const int pg = page_of(p, U.b, j);
             if (pg < 0) continue;
             const size_t at = (((size_t)pg * p.Hkv + U.hk) << p.log_page) + (j & (p.page - 1));

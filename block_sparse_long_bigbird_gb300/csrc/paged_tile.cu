@@ -11,6 +11,8 @@
 // with three, 512 tokens over 8192 keys (2 sequences, 16 heads, d = 64, fp32) took 1458
 // us, with four 994 us, 33.5 TFLOP/s of 75 that the multiply-adds allow (d = 128: 2650
 // us, 25 TFLOP/s). Rows in use matter: a unit is 64 rows whatever it holds.
+// Global keys before a tile's window are gathered 64 to a step, wherever they lie;
+// a step per block that holds one was half of all steps with 16 of them spread out.
 #include "paged_common.cuh"
 
 namespace sa {
@@ -88,13 +90,18 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
             for (int x = 0; x < 4 * ND; ++x) acc[r][x] = 0.f;
         }
         if (tid == kTT - 1) fill_room(p, P, room, room_k ^ 1);  // a warp without masks to work out
+        const int far = far_globals(p, P, U);
         for (int e = U.e0; e < U.e1; ++e) {
-            const int blk = entry_block(P, U, e), j0 = blk << 6;
+            const bool listed = e < U.n_glob;  // 64 of the far global keys, which every row sees
+            const int blk = listed ? 0 : entry_block(P, U, e), j0 = blk << 6;
             __syncthreads();  // the previous step is done with KV, Ps and masks
-            if (tid < kTR) masks[tid] = row_mask(row, blk, global_bits(P, p, blk), ~0ull);
+            if (tid < kTR)
+                masks[tid] = !listed ? row_mask(row, blk, global_bits(P, p, blk), ~0ull)
+                             : row.valid ? low_bits(far - 64 * e) : 0ull;
             // one key per lane: keys past the sequence or without a page count as
             // zeros and are masked below
-            const int key = tid & 63, pos = j0 + key;
+            const int key = tid & 63;
+            const int pos = !listed ? j0 + key : 64 * e + key < far ? P.gpos[64 * e + key] : U.s;
             const int pg = pos < U.s ? page_of(p, U.b, pos) : -1;
             const size_t at = ((((size_t)(pg < 0 ? 0 : pg) * p.Hkv + U.hk) << p.log_page) + (pos & (p.page - 1))) * D;
 #pragma unroll 4
@@ -131,9 +138,10 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
             {
                 // V rows as they are: a warp per key row piece
                 for (int i = tid; i < kTR * (D / VE); i += kTT) {
-                    const int vk = i / (D / VE), c = i % (D / VE), vpos = j0 + vk;
+                    const int vk = i / (D / VE), c = i % (D / VE);
                     uint4 w = make_uint4(0u, 0u, 0u, 0u);
                     if ((present >> vk) & 1ull) {
+                        const int vpos = listed ? P.gpos[64 * e + vk] : j0 + vk;
                         const int vpg = page_of(p, U.b, vpos);
                         w = __ldg(reinterpret_cast<const uint4 *>(
                             Vp + ((((size_t)vpg * p.Hkv + U.hk) << p.log_page) + (vpos & (p.page - 1))) * D + c * VE));

@@ -60,10 +60,6 @@ def _scratch(n_bytes, device, stream):
     return None if n_bytes == 0 else _new((n_bytes,), (1,), torch.uint8, device, stream)
 
 
-def _fresh(like, stream):
-    return _new(tuple(like.shape), like.stride(), like.dtype, like.device, stream)
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -198,7 +194,9 @@ def _pool_args(K_pages, V_pages):
 
 def _outputs(out, ins, stream):
     if out is None:
-        return [_fresh(t, stream) for t in ins]
+        if stream is None and _new_cuda is not None and torch._C._cuda_getDevice() == ins[0].get_device():
+            return [_new_cuda(tuple(t.shape), t.stride(), _INT) for t in ins]
+        return [_new(tuple(t.shape), t.stride(), _INT, t.device, stream) for t in ins]
     if len(out) != len(ins):
         raise ValueError(f"out must hold {len(ins)} tensors")
     for o, t in zip(out, ins):

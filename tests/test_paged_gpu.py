@@ -149,6 +149,23 @@ def test_what_a_row_does_not_see_does_not_reach_it(m, Hq, dtype):
     assert sa.get_last_device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("m,Hq,dil", [(1, 2, None), (70, 2, None), (70, 4, [0, 3, 1, 0])])
+def test_many_far_globals(m, Hq, dil, dtype):
+    """More global keys before the window than one step takes, some without a page, some later than the sequence."""
+    lens = [2000, 700]
+    g = sorted(set(range(0, 40)) | set(range(50, 1900, 13)) | {1975, 2600})
+    Q, K, V, table = make_cache(71, 2, Hq, 2, m, 64, 16, lens, dtype)
+    table[0, 20:30] = -1
+    attend_and_check(Q, K, V, table, lens, None, 64, g, dil, dtype)
+    # an infinite value at a far global key: every row has it, computed by the definition
+    Vc = V.clone()
+    Vc[int(table[1, 0]), :, 3, 0] = float("inf")
+    got = f64(sa.longformer_attn_paged_fwd(*dev(Q, K, Vc, table, ints(lens)), 64, ints(g).cuda(), dilation=dev(ints(dil))[0]))
+    assert np.isposinf(got[1, :, :, 0]).all() and np.isfinite(got[1, :, :, 1:]).all() and np.isfinite(got[0]).all()
+    assert sa.get_last_device_status() == 0
+
+
 def test_bad_lengths_and_pages_are_zeroed_and_latched():
     lens = [64, 100, 30]
     Q, K, V, table = make_cache(2, 3, 4, 2, 2, 64, 16, lens, width=7)
