@@ -110,6 +110,27 @@ def test_values_beyond_the_largest_number_in_a_split_sweep(group, d):
     assert sa.get_last_device_status() == 0
 
 
+@pytest.mark.parametrize("m,group,d", [(2, 1, 64), (2, 2, 128), (2, 10, 64), (40, 1, 64)])
+def test_infinities_in_some_of_many_tiles(m, group, d):
+    """CTAs that compute rows again between units that need none of that."""
+    B, Hkv = 120, 3
+    lens = [m + (29 * i) % 90 for i in range(B)]
+    Q, K, V, table = make_cache(52, B, Hkv * group, Hkv, m, d, 16, lens)
+    clean = attend_and_check(Q, K, V, table, lens, None, 300)
+    Vc = V.clone()
+    for b in range(0, B, 2):
+        last = lens[b] - 1
+        Vc[int(table[b, last // 16]), :, last % 16, 5] = float("-inf")
+    got = sa.longformer_attn_paged_fwd(*dev(Q, K, Vc, table, ints(lens)), 300)
+    assert torch.equal(got[1::2], clean[1::2])
+    a, b = f64(got[::2]), f64(clean[::2])
+    assert np.isneginf(a[:, :, -1, 5]).all()
+    a[:, :, -1, 5] = b[:, :, -1, 5]
+    # the weights' rounding of one (2^-8 of a mean of |v| < 4), the results' of both
+    assert np.allclose(a, b, rtol=2.0 ** -7, atol=2.0 ** -6)
+    assert sa.get_last_device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("m", [1, 3, 70])
 def test_missing_pages_and_empty_rows(m, dtype):
