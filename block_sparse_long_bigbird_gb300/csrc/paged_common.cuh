@@ -144,9 +144,11 @@ __device__ __forceinline__ void lengths(const PagedProblem &p, int q, int s, int
     s_out = bad ? 0 : s;
 }
 
-// Computed by the whole CTA. Ends with a barrier. All loads are issued before
-// the first is used, and warp 0 does what follows on its own: the plan stands
-// before every call's first load of a key, so its latency counts.
+// Computed by the whole CTA. Ends with a barrier where there is anything to plan;
+// where there is not it returns at once, and what the caller has set up in shared
+// memory needs a barrier of its own. All loads are issued before the first is
+// used, and warp 0 does what follows on its own: the plan stands before every
+// call's first load of a key, so its latency counts.
 __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
     const int tid = threadIdx.x, lane = tid & 31, nthr = blockDim.x;
     int q0 = p.m, s0 = 0, g0 = -1, g1 = -1;

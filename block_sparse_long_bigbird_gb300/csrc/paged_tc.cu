@@ -186,8 +186,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         prefetch_tmap(&tmV);
     }
     Plan P = plan_at(smem + C::PLAN_OFF, p.B, p.ng, p.Hkv);
-    tc_fence_before();
     make_plan(p, P);
+    // The mbarriers and the TMEM address above are every warp's from here on,
+    // also on calls that need no plan (make_plan has no barrier there).
+    tc_fence_before();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     asm volatile("griddepcontrol.launch_dependents;");  // the join may start planning
