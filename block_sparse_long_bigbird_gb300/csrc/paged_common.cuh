@@ -144,6 +144,24 @@ __device__ __forceinline__ void lengths(const PagedProblem &p, int q, int s, int
     s_out = bad ? 0 : s;
 }
 
+// Marks (-1) the entries of a[0..n) that are not above every one kept before
+// them, so that what the walks search is ascending whatever a list held. One
+// warp; out of line, as lists are hardly ever out of order.
+__device__ __noinline__ void keep_ascending(int *a, int n) {
+    const int lane = threadIdx.x & 31;
+    int top = -1;  // the largest entry so far
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int v = i0 + lane < n ? a[i0 + lane] : -1;
+        int most = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) most = max(most, __shfl_up_sync(kAllLanes, most, o));
+        const int prior = __shfl_up_sync(kAllLanes, most, 1);
+        if (i0 + lane < n && v <= (lane == 0 ? top : max(top, prior))) a[i0 + lane] = -1;
+        top = max(top, __shfl_sync(kAllLanes, most, 31));
+    }
+    __syncwarp();
+}
+
 // Computed by the whole CTA. Ends with a barrier where there is anything to plan;
 // where there is not it returns at once, and what the caller has set up in shared
 // memory needs a barrier of its own. All loads are issued before the first is
@@ -169,16 +187,16 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
         }
         lengths(p, q, s, P.q[b], P.s[b]);
     }
-    // the global list: a block starts where the block number changes; entries
-    // that break the order are skipped (the call's result is then unspecified)
+    // the global list: entries out of range or order are latched and do not count
+    bool unsorted = false;
     for (int i = tid; i < p.ng; i += nthr) {
-        int v = i == tid ? g0 : __ldg(p.gidx + i);
+        const int v = i == tid ? g0 : __ldg(p.gidx + i);
         const int before = i == tid ? g1 : __ldg(p.gidx + i - 1);
         if (v < 0 || v >= kPagedMaxLen || (i > 0 && before >= v)) {
             atomicOr(p.status, kDevBadIndex);
-            v = -1;
+            unsorted = true;
         }
-        P.gpos[i] = v;
+        P.gpos[i] = v >= kPagedMaxLen ? -1 : v;
     }
     if (p.dilation)
         for (int h = tid; h < p.Hkv; h += nthr) {
@@ -186,9 +204,11 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
             for (int g = 0; g < p.group; ++g) st = max(st, head_stride(p, h * p.group + g));
             P.hstride[h] = st;
         }
-    __syncthreads();
+    unsorted = __syncthreads_or(unsorted);
     const int all_tiles = (p.m + p.tpt - 1) / p.tpt;
-    if (p.ng > 0 && tid >= nthr - 32) {  // the last warp: the blocks of the global list
+    // the last warp: the blocks of the global list; one starts where the block number changes
+    if (p.ng > 0 && tid >= nthr - 32) {
+        if (unsorted) keep_ascending(P.gpos, p.ng);
         int n = 0, kept = 0, last = -1;  // blocks and entries so far, the last entry's block
         for (int i0 = 0; i0 < p.ng; i0 += 32) {
             const int v = i0 + lane < p.ng ? P.gpos[i0 + lane] : -1;

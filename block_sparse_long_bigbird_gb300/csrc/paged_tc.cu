@@ -799,6 +799,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 pend = scores ? i : -1;
                 return true;
             };
+            // With one tile every step is used: its blocks lie in the window, or hold
+            // a global key before it (the plan's lists are ascending).
             const int step = one ? 2 : 1;
             for (int i = one ? x : 0; i < n; i += step) {
                 bool use = true;

@@ -505,7 +505,10 @@ sa_status bigbird_attn_fwd_noalloc(const void *Q, const void *K, const void *V, 
  * window: even, >= 0. dilation: DEVICE int32 [Hq] or NULL, as for
  *   longformer_attn_fwd_ex. global_idx: DEVICE int32 [n_global], strictly
  *   increasing positions, the same for every sequence; positions past a
- *   sequence's end do not matter. n_global <= 512.
+ *   sequence's end do not matter. n_global <= 512. An entry outside [0, 2^30)
+ *   or not above every entry that counts before it does not count, and latches
+ *   SA_ERR_BAD_INDEX; an entry of `dilation` outside [0, 63] counts as 0 and
+ *   latches it.
  * Numerics: bf16 inputs: fp32 scores, softmax and sums; with more than 8 query
  *   rows per key head (m * Hq / Hkv) the weights are rounded to bf16 for the
  *   matrix instructions, as in the calls above, and with 2 to 8 rows to the sum

@@ -40,3 +40,43 @@ def test_chunks_with_a_plain_window_right_after_dense_calls(B, Hq, Hkv, m, d):
         _dense_calls()
         assert torch.equal(sa.longformer_attn_paged_fwd(*args, 64), first)
     assert sa.get_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ lists that break the contract
+def _counted(g):
+    """The entries of a list that count: in range and above every one that counts before them."""
+    kept = []
+    for v in g:
+        if 0 <= v < 2 ** 30 and (not kept or v > kept[-1]):
+            kept.append(v)
+    return kept
+
+
+LISTS = [[1000, 1100, 5, 6, 64, 128], [200, 264, 10, 20, 70], [7, 7], [5, -3, 4, 300], [2 ** 30, 7, 8],
+         [-1], list(range(60, 0, -1)) + list(range(100, 170)), [65 * i % 400 for i in range(100)]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("m,Hq", [(1, 2), (3, 8), (40, 2), (40, 4), (150, 4)])
+def test_global_lists_out_of_order_or_range(m, Hq, dtype):
+    lens = [400, 300]
+    Q, K, V, table = make_cache(91, 2, Hq, 2, m, 64, 16, lens, dtype)
+    args = dev(Q, K, V, table, ints(lens))
+    for g in LISTS:
+        want = attend_and_check(Q, K, V, table, lens, None, 64, _counted(g), None, dtype)
+        got = sa.longformer_attn_paged_fwd(*args, 64, ints(g).cuda())
+        assert sa.get_last_device_status() == _lib.SA_ERR_BAD_INDEX
+        torch.testing.assert_close(got, want, rtol=2.0 ** -6 if dtype == "bf16" else 2e-5, atol=2.0 ** -7 if dtype == "bf16" else 2e-6)
+
+
+@pytest.mark.parametrize("m,Hq", [(1, 2), (3, 8), (40, 2), (150, 4)])
+def test_dilations_out_of_range_count_as_none(m, Hq):
+    lens = [400, 300]
+    Q, K, V, table = make_cache(92, 2, Hq, 2, m, 64, 32, lens)
+    for bad in (64, -1, 2 ** 31 - 1):
+        dil = [2] * Hq
+        want = attend_and_check(Q, K, V, table, lens, None, 64, [3], dil[:-1] + [0])
+        got = sa.longformer_attn_paged_fwd(*dev(Q, K, V, table, ints(lens)), 64, ints([3]).cuda(),
+                                           dilation=ints(dil[:-1] + [bad]).cuda())
+        assert sa.get_last_device_status() == _lib.SA_ERR_BAD_INDEX
+        assert torch.equal(got, want)
