@@ -348,11 +348,19 @@ __global__ void __launch_bounds__(256) free_rows(const PoolProblem p) {
 
 // Pages that no later token can see: all their tokens lie more than `reach`
 // before the next one, and none of them is global. A global position still to
-// come will see everything, so its sequence keeps every page.
+// come will see everything, so its sequence keeps every page. So does a sequence
+// whose length breaks the contract, and every one if the list does: pages given
+// up do not come back.
 __global__ void __launch_bounds__(256) trim_rows(const PoolProblem p) {
+    bool unsorted = false;
+    for (int i = threadIdx.x; i < p.ng; i += blockDim.x)
+        unsorted |= __ldg(p.gidx + i) <= (i == 0 ? -1 : __ldg(p.gidx + i - 1));
+    unsorted = __syncthreads_or(unsorted);
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const int len = p.lens_in[b];
-        const bool keep_all = p.ng > 0 && __ldg(p.gidx + p.ng - 1) >= len;
+        const bool bad = unsorted || len < 0 || (long long)len > ((long long)p.max_pages << p.log_page);
+        if (bad && threadIdx.x == 0) atomicOr(p.status, kDevBadIndex);
+        const bool keep_all = bad || (p.ng > 0 && __ldg(p.gidx + p.ng - 1) >= len);
         const long long lowest = (long long)len - p.reach;  // first position the next token's window holds
         for (int c = threadIdx.x; c < p.max_pages; c += blockDim.x) {
             const size_t at = (size_t)b * p.max_pages + c;

@@ -594,7 +594,9 @@ sa_status sa_cache_free(int num_pages, int B, int max_pages, const int32_t *rows
  * position. reach = window / 2 * (largest dilation + 1). A sequence with a
  * global position still to come (global_idx's last >= seq_lens[b]) keeps every
  * page, as that token will see them all. Call it when the tokens so far have
- * been attended to. */
+ * been attended to. A length below 0 or past the table row keeps that row's
+ * pages, and a list that is negative or not strictly increasing keeps every
+ * row's; both latch SA_ERR_BAD_INDEX. */
 sa_status sa_cache_trim(int num_pages, int page, int B, int max_pages, int reach,
                         const int32_t *global_idx, int n_global,
                         const int32_t *table_in, const int32_t *seq_lens, const int32_t *ref_in,

@@ -80,3 +80,30 @@ def test_dilations_out_of_range_count_as_none(m, Hq):
                                            dilation=ints(dil[:-1] + [bad]).cuda())
         assert sa.get_last_device_status() == _lib.SA_ERR_BAD_INDEX
         assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ bookkeeping of values that break the contract
+def _book():
+    """A table [4, 6] of pages of 16 tokens over 30 pages; the third row is empty."""
+    table = np.full((4, 6), -1, np.int32)
+    table[0], table[1, :4], table[3, :2] = [7, 3, 20, 1, 9, 28], [5, 6, 29, 0], [11, 12]
+    refs = np.zeros(30, np.int32)
+    np.add.at(refs, table[table >= 0], 1)
+    return table, [96, 50, 0, 30], refs
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_trim_keeps_the_pages_of_rows_and_lists_that_break_the_contract(in_place):
+    table, lens, refs = _book()
+    for row, n in ((0, 97), (1, -5), (1, 10 ** 6), (3, 2 ** 31 - 1)):
+        T, R = dev(*map(torch.from_numpy, (table, refs)))
+        bad = lens[:row] + [n] + lens[row + 1:]
+        got = sa.cache_trim(T, ints(bad).cuda(), R, 16, 8, ints([1]).cuda(), out=(T, R) if in_place else None)
+        assert sa.get_last_device_status() == _lib.SA_ERR_BAD_INDEX
+        held = lens[:row] + [0] + lens[row + 1:]  # a sequence without tokens gives up nothing
+        assert [x.tolist() for x in got] == list(op.trim(table, held, refs, 16, 8, [1]))
+    for g in ([3, 2], [40, 40], [-1, 5], [1, 70, 20]):
+        T, R = dev(*map(torch.from_numpy, (table, refs)))
+        got = sa.cache_trim(T, ints(lens).cuda(), R, 16, 8, ints(g).cuda(), out=(T, R) if in_place else None)
+        assert sa.get_last_device_status() == _lib.SA_ERR_BAD_INDEX
+        assert got[0].tolist() == table.tolist() and got[1].tolist() == refs.tolist()
