@@ -1,6 +1,6 @@
 // What the kernels of the paged attention share: the plan (how a call's
 // sweeps are cut into units), the walk over a unit's 64-key blocks, the mask
-// of a row against a block, and an exact path for rows that ordinary
+// of a row against a block, and a pass by the definition over rows that ordinary
 // arithmetic spoils.
 //
 // A tile is a few tokens times the query heads of one key head; it walks the
@@ -144,6 +144,16 @@ __device__ __forceinline__ void lengths(const PagedProblem &p, int q, int s, int
     s_out = bad ? 0 : s;
 }
 
+// What make_plan left in shared memory, where it had anything to plan.
+__device__ __forceinline__ void take_plan(const PagedProblem &p, Plan &P) {
+    P.ngb = p.ng > 0 ? P.misc[0] : 0;
+    if (!p.cut) return;
+    P.cut = P.misc[1] > 0;
+    P.ctas = P.cut ? P.misc[1] : 1;
+    P.rest = P.misc[2];
+    P.share = P.vbase[p.B + 1];
+}
+
 // Marks (-1) the entries of a[0..n) that are not above every one kept before
 // them, so that what the walks search is ascending whatever a list held. One
 // warp; out of line, as lists are hardly ever out of order.
@@ -281,12 +291,7 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
         }
     }
     __syncthreads();
-    P.ngb = p.ng > 0 ? P.misc[0] : 0;
-    if (!p.cut) return;
-    P.cut = P.misc[1] > 0;
-    P.ctas = P.cut ? P.misc[1] : 1;
-    P.rest = P.misc[2];
-    P.share = P.vbase[p.B + 1];
+    take_plan(p, P);
 }
 
 // Where CTA c's stretch begins: floor(length * c / ctas).
@@ -603,62 +608,6 @@ __device__ __forceinline__ void row_token(const PagedProblem &p, const Unit &U, 
     head = U.hk * p.group + g;
 }
 
-// One row of a unit by the definition, the whole warp together: only the keys
-// that the row sees are read, so what masked places hold (unwritten memory,
-// infinities, NaN) cannot reach the result. The tiled kernels multiply masked
-// values by zero instead and call this for rows whose sums came out infinite
-// or NaN, which ordinary inputs never cause. Returns the running maximum and
-// sum, and in `acc` the lane's D / 32 sums.
-template <typename T, int D>
-__device__ __noinline__ float2 exact_row(const PagedProblem &p, const Plan &P, const Unit &U, int t, int head,
-                                         float (&acc)[D / 32]) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const T *Q = static_cast<const T *>(p.Q) + (((size_t)U.b * p.Hq + head) * p.m + t) * D + lane * E;
-    float q[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        q[i] = to_float<T>(Q[i]) * p.scale_log2;
-        acc[i] = 0.f;
-    }
-    const Row r = make_row(p, P, U, head, t);
-    float m = -CUDART_INF_F, l = 0.f;
-    const int far = p.listed ? far_globals(p, P, U) : 0;
-    for (int e = U.e0; e < U.e1; ++e) {
-        const bool listed = p.listed && e < U.n_glob;
-        const int blk = listed ? 0 : entry_block(P, U, e);
-        uint64_t w = listed ? low_bits(far - 64 * e) : row_mask(r, blk, global_bits(P, p, blk), ~0ull);
-        while (w) {
-            const int i = __ffsll((long long)w) - 1;
-            w &= w - 1;
-            const int j = listed ? P.gpos[64 * e + i] : (blk << 6) + i;
-            const int pg = page_of(p, U.b, j);
-            if (pg < 0) continue;
-            const size_t at = (((size_t)pg * p.Hkv + U.hk) << p.log_page) + (j & (p.page - 1));
-            const T *k = static_cast<const T *>(p.K) + at * D + lane * E;
-            float s = 0.f;
-#pragma unroll
-            for (int x = 0; x < E; ++x) s = fmaf(q[x], to_float<T>(k[x]), s);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAllLanes, s, o);
-            if (s == -CUDART_INF_F) continue;  // weight 0 whatever the maximum
-            if (not_finite(s)) {  // +inf or NaN: so is every element of the row
-#pragma unroll
-                for (int x = 0; x < E; ++x) acc[x] = CUDART_NAN_F;
-                return make_float2(0.f, CUDART_NAN_F);
-            }
-            const float mn = fmaxf(m, s);
-            const float f = m == -CUDART_INF_F ? 0.f : ptx::ex2(m - mn), w1 = ptx::ex2(s - mn);
-            l = l * f + w1;
-            const T *v = static_cast<const T *>(p.V) + at * D + lane * E;
-#pragma unroll
-            for (int x = 0; x < E; ++x) acc[x] = fmaf(w1, to_float<T>(v[x]), acc[x] * f);
-            m = mn;
-        }
-    }
-    return make_float2(m, l);
-}
-
 // Where elements [4 k, 4 k + 4) of a row's partial sums lie: rows side by side, so
 // that threads that hold a row each write whole lines.
 template <int D>
@@ -666,23 +615,176 @@ __device__ __forceinline__ size_t part_at(const PagedProblem &p, int slot, int k
     return (((size_t)slot * (D / 4) + k) * p.rows + row) * 4;
 }
 
-// Stores what exact_row returned: the finished row, or its split's partial.
-template <typename T, int D>
-__device__ __forceinline__ void store_exact_row(const PagedProblem &p, const Unit &U, int t, int head, int row,
-                                                float2 ml, const float (&acc)[D / 32]) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    if (U.split) {
+// Rows [at0, at0 + R) of a unit by the definition, those of them whose results hold an
+// infinity or NaN, the whole warp together: a key counts for the rows that see it and
+// for no others. 32 keys at a time, a lane each for the scores, then eight values in
+// flight; the rows share what is loaded. (33000 rows that all see an infinity among
+// 16000 keys, d = 64: 66 ms; key by key with the whole warp, a row at a time, 770.)
+template <typename T, int D, int R>
+__device__ __forceinline__ void exact_rows(const PagedProblem &p, const Plan &P, const Unit &U, int at0) {
+    constexpr int E = D / 32, VE = 16 / sizeof(T), AHEAD = 8;
+    struct alignas(E * sizeof(T)) Piece {
+        T x[E];
+    };
+    const int lane = threadIdx.x & 31, half_rows = p.tpt_half * p.group;
+    size_t base[R];  // where the row is in Q and O
+    Row row[R];
+    float acc[R][E], m[R], l[R];
+    unsigned again = 0u, spoiled = 0u;
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            p.part_o[part_at<D>(p, U.slot, (lane * E + i) >> 2, row) + ((lane * E + i) & 3)] = acc[i];
-        if (lane == 0) p.part_ml[(size_t)U.slot * p.rows + row] = ml;
-    } else {
-        T *O = static_cast<T *>(p.O) + (((size_t)U.b * p.Hq + head) * p.m + t) * D + lane * E;
-        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+    for (int r = 0; r < R; ++r) {
+        const int at = min(at0 + r, p.rows - 1), x = at / half_rows;  // the halves of a unit hold different tokens
+        const int k = at - x * half_rows, g = k / p.tpt_half, head = U.hk * p.group + g;
+        const int t = U.t0 + x * p.tpt_half + k - g * p.tpt_half;
+        base[r] = (((size_t)U.b * p.Hq + head) * p.m + t) * D;
+        row[r] = make_row(p, P, U, head, t);
+        row[r].valid = row[r].valid && at0 + r < p.rows;
+        bool bad = false;
+        if (row[r].valid && U.split) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) O[i] = from_float<T>(acc[i] * inv);
+            for (int i = 0; i < E; ++i)
+                bad |= not_finite(p.part_o[part_at<D>(p, U.slot, (lane * E + i) >> 2, at) + ((lane * E + i) & 3)]);
+            bad |= not_finite(p.part_ml[(size_t)U.slot * p.rows + at].y);
+        } else if (row[r].valid) {
+            const Piece o = *reinterpret_cast<const Piece *>(static_cast<const T *>(p.O) + base[r] + lane * E);
+#pragma unroll
+            for (int i = 0; i < E; ++i) bad |= not_finite(to_float<T>(o.x[i]));
+        }
+        if (__any_sync(kAllLanes, bad)) again |= 1u << r;
+        m[r] = -CUDART_INF_F;
+        l[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[r][i] = 0.f;
     }
+    if (!again) return;
+    const int far = p.listed ? far_globals(p, P, U) : 0;
+    for (int e = U.e0; e < U.e1; ++e) {
+        const bool listed = p.listed && e < U.n_glob;
+        const int blk = listed ? 0 : entry_block(P, U, e);
+        const uint64_t gbits = listed ? 0ull : global_bits(P, p, blk);
+        uint64_t w[R], any = 0ull;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            w[r] = 0ull;
+            if (((again & ~spoiled) >> r) & 1u) w[r] = listed ? low_bits(far - 64 * e) : row_mask(row[r], blk, gbits, ~0ull);
+            any |= w[r];
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < 64; i0 += 32) {
+            const uint32_t seen = (uint32_t)(any >> i0);
+            if (!seen) continue;
+            float s[R];  // of the lane's key
+            size_t at = 0;
+            bool there = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r] = 0.f;
+            if ((seen >> lane) & 1u) {
+                const int j = listed ? P.gpos[64 * e + i0 + lane] : (blk << 6) + i0 + lane;
+                const int pg = page_of(p, U.b, j);
+                there = pg >= 0;
+                if (there) {
+                    at = ((((size_t)pg * p.Hkv + U.hk) << p.log_page) + (j & (p.page - 1))) * D;
+                    const uint4 *k = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.K) + at);
+#pragma unroll 4
+                    for (int c = 0; c < D / VE; ++c) {
+                        const uint4 kw = __ldg(k + c);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            if (!((again >> r) & 1u)) continue;
+                            const uint4 qw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.Q) + base[r]) + c);
+#pragma unroll
+                            for (int x = 0; x < VE; ++x)
+                                s[r] = fmaf(element<T>(qw, x) * p.scale_log2, element<T>(kw, x), s[r]);
+                        }
+                    }
+                }
+            }
+            unsigned on[R], all_on = 0u;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (!there || !((uint32_t)(w[r] >> (i0 + lane)) & 1u)) s[r] = -CUDART_INF_F;
+                on[r] = __ballot_sync(kAllLanes, s[r] != -CUDART_INF_F);  // a score of -inf has weight 0 whatever the maximum
+                all_on |= on[r];
+                // +inf or NaN: so is every element of the row
+                if (__any_sync(kAllLanes, !(s[r] <= 3.402823466e38f))) spoiled |= 1u << r;
+                if (!on[r]) continue;
+                float mn = s[r];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(kAllLanes, mn, o));
+                mn = fmaxf(m[r], mn);
+                const float f = ptx::ex2(m[r] - mn);  // 0 from the initial -inf
+                s[r] = ptx::ex2(s[r] - mn);
+                float sum = s[r];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
+                l[r] = l[r] * f + sum;
+                m[r] = mn;
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[r][i] *= f;
+            }
+#pragma unroll 1
+            for (int k0 = 0; k0 < 32; k0 += AHEAD) {
+                Piece v[AHEAD];
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const size_t from = __shfl_sync(kAllLanes, (unsigned long long)at, k0 + k);
+                    if ((all_on >> (k0 + k)) & 1u)
+                        v[k] = *reinterpret_cast<const Piece *>(static_cast<const T *>(p.V) + from + lane * E);
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int k = 0; k < AHEAD; ++k) {
+                        const float wk = __shfl_sync(kAllLanes, s[r], k0 + k);
+                        if ((on[r] >> (k0 + k)) & 1u) {
+#pragma unroll
+                            for (int i = 0; i < E; ++i) acc[r][i] = fmaf(wk, to_float<T>(v[k].x[i]), acc[r][i]);
+                        }
+                    }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (!((again >> r) & 1u)) continue;
+        if ((spoiled >> r) & 1u) {
+            m[r] = 0.f;
+            l[r] = CUDART_NAN_F;
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[r][i] = CUDART_NAN_F;
+        }
+        if (U.split) {  // the split's partial result
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                p.part_o[part_at<D>(p, U.slot, (lane * E + i) >> 2, at0 + r) + ((lane * E + i) & 3)] = acc[r][i];
+            if (lane == 0) p.part_ml[(size_t)U.slot * p.rows + at0 + r] = make_float2(m[r], l[r]);
+        } else {
+            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+            T *O = static_cast<T *>(p.O) + base[r] + lane * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) O[i] = from_float<T>(acc[r][i] * inv);
+        }
+    }
+}
+
+// The tiled kernels multiply masked values by zero, so an infinity or NaN at a key
+// that a row does not see spoils the row's sums; ordinary inputs never do that.
+// A CTA that met such a row goes over its units once more when it is through
+// with them, and takes the rows whose results are not finite again by the
+// definition. (Not between its units: no other warp may wait for rows that
+// take as long as their keys are many.) Called by `warps` whole warps after a
+// barrier; the results are read back from where they were written. (Nothing of the
+// caller's but where its plan lies, which would otherwise have to be in memory.)
+template <typename T, int D, int R>
+__device__ __noinline__ void rows_again(const PagedProblem &p, void *plan, int warp, int warps) {
+    Plan P = plan_at(plan, p.B, p.ng, p.Hkv);
+    take_plan(p, P);
+    Units units;
+    units.begin(p, P, blockIdx.x);
+    Unit U;
+    while (units.next(p, P, U))
+        if (U.live)
+            for (int at = R * warp; at < p.rows; at += R * warps) exact_rows<T, D, R>(p, P, U, at);
 }
 
 }  // namespace

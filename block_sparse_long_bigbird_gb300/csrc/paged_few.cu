@@ -32,7 +32,7 @@
 // 5.8 TB/s. One sequence of 900 keys takes 11.5 us (d = 64), a few hundred
 // clocks per item and warp: latency.
 // A row that does not see a key multiplies its value by 0; where that value is
-// infinite or NaN the row's sums come out so, and exact_row computes it again.
+// infinite or NaN the row's sums come out so, and rows_again takes it again.
 #include "paged_common.cuh"
 
 namespace sa {
@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(W * 32, Few<D, NT, W>::ctas) paged_few(const _
     constexpr int PK = D / 8;  // 16-byte pieces of a key
     extern __shared__ __align__(16) uint8_t smem[];
     UnitRoom *room = reinterpret_cast<UnitRoom *>(smem + W * C::ring);
-    uint32_t *bad = reinterpret_cast<uint32_t *>(room + 1);  // rows to be computed again: of this unit, of the next
-    Plan P = plan_at(bad + 4, p.B, p.ng, p.Hkv);
+    int *again = reinterpret_cast<int *>(room + 1);  // whether a row is to be taken again
+    Plan P = plan_at(again + 4, p.B, p.ng, p.Hkv);
     make_plan(p, P);
     asm volatile("griddepcontrol.launch_dependents;");  // the join may start planning
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(W * 32, Few<D, NT, W>::ctas) paged_few(const _
     const int odd = 4 * (n & 1), own = n * PK + quad - lane;
 
     if (tid == 0) {
-        bad[0] = bad[1] = 0u;
+        *again = 0;
         room->units.begin(p, P, blockIdx.x);
         fill_room(p, P, room, 0);
     }
@@ -329,7 +329,6 @@ __global__ void __launch_bounds__(W * 32, Few<D, NT, W>::ctas) paged_few(const _
                 }
             }
         __syncthreads();
-        if (tid == 0) bad[k ^ 1] = 0u;
         for (int idx = tid; idx < C::f4 * 32; idx += W * 32) {
             const int ln = idx & 31, i = idx >> 5, f = i & 1, set = (i >> 1) % SETS, part = (i >> 1) / SETS;
             const int row = 8 * (part >> 1) + 2 * (ln & 3) + (part & 1), col = set * 64 + (ln >> 2) * 8 + 4 * f;
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(W * 32, Few<D, NT, W>::ctas) paged_few(const _
             int t, head;
             row_token(p, U, row, p.tpt, t, head);
             const bool valid = (rows_in >> row) & 1u;
-            if (valid && (not_finite(ls) || not_finite(a.x + a.y + a.z + a.w))) atomicOr(&bad[k], 1u << row);
+            if (valid && (not_finite(ls) || not_finite(a.x + a.y + a.z + a.w))) *again = 1;
             if (U.split) {
                 *reinterpret_cast<float4 *>(p.part_o + part_at<D>(p, U.slot, col >> 2, row)) = a;
                 if (col == 0) p.part_ml[(size_t)U.slot * p.rows + row] = make_float2(mx, ls);
@@ -369,19 +368,8 @@ __global__ void __launch_bounds__(W * 32, Few<D, NT, W>::ctas) paged_few(const _
             }
         }
         __syncthreads();
-        const uint32_t again = bad[k];
-        if (again) {
-            for (int r = warp; r < p.rows; r += W) {
-                if (!((again >> r) & 1u)) continue;
-                int t, head;
-                row_token(p, U, r, p.tpt, t, head);
-                float a[D / 32];
-                const float2 ml = exact_row<bf16, D>(p, P, U, t, head, a);
-                store_exact_row<bf16, D>(p, U, t, head, r, ml, a);
-            }
-            __syncthreads();
-        }
     }
+    if (*again) rows_again<bf16, D, 1>(p, again + 4, warp, W);
 }
 
 template <int D, int NT, int W>

@@ -26,7 +26,8 @@
 //     the rounding the dense path of this library makes too).
 // Memory where no token was written may hold NaN: those V rows are zeroed in
 // shared memory before the product. Any other masked infinity or NaN makes its
-// row's O not finite, and exact_row then computes that row again.
+// row's O not finite; the softmax warps take such rows again (rows_again) when
+// the CTA is through with its units.
 // Roles' waits are bounded; on expiry the CTA latches SA_ERR_TIMEOUT, drains
 // its copies and MMAs, frees TMEM and exits.
 //
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t sbase = smem_u32(smem);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    volatile int *again = abort_flag + 1;  // whether a row is to be taken again
     StepRec *recs = reinterpret_cast<StepRec *>(smem + C::REC_OFF);
     UnitRec *unit_recs = reinterpret_cast<UnitRec *>(smem + C::UNIT_OFF);
     auto bar = [&](int i) { return sbase + C::BAR_OFF + 8u * (uint32_t)i; };
@@ -147,6 +149,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
+        *again = 0;
         for (int i = 0; i < C::NST; ++i) {
             mbar_init(bar(C::B_KF + i), 1);
             mbar_init(bar(C::B_KE + i), one ? 1 : 2);  // the MMA warps that read the stage
@@ -549,18 +552,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (had2) mbar_arrive(bar(C::B_OE + 1));
                 }
             }
-            unsigned again = __ballot_sync(kAllLanes, row.valid && (had || had2) && (bad || not_finite(l)));
-            while (again) {
-                const int r = __ffs(again) - 1;
-                again &= again - 1;
-                const int rt = __shfl_sync(kAllLanes, t, r), rh = __shfl_sync(kAllLanes, head, r);
-                float a[D / 32];
-                __syncwarp();
-                const float2 ml = exact_row<__nv_bfloat16, D>(p, P, U, rt, rh, a);
-                store_exact_row<__nv_bfloat16, D>(p, U, rt, rh, x * half_rows + (warp & 3) * 32 + r, ml, a);
-            }
+            if (row.valid && (had || had2) && (bad || not_finite(l))) *again = 1;
             unit_done();
         }
+        // All softmax warps get here (their waits are bounded), their results written.
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (*again && !*abort_flag) rows_again<__nv_bfloat16, D, 4>(p, smem + C::PLAN_OFF, warp, 8);
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 8) {

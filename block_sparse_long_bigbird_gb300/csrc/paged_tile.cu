@@ -29,7 +29,7 @@ struct TileSmem {
     static constexpr int S = KV + (D * kPad > kTR * D ? D * kPad : kTR * D) * 4;
     static constexpr int MASK = S + kTR * kPad * 4;
     static constexpr int FLAG = MASK + kTR * 8;
-    static constexpr int ROOM = FLAG + kTR * 4;
+    static constexpr int ROOM = FLAG + 16;
     static constexpr int PLAN = ROOM + (int)sizeof(UnitRoom);
 };
 
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
     float *KV = reinterpret_cast<float *>(smem + L::KV);   // K: [D][kPad], then V: [64][D]
     float *Ps = reinterpret_cast<float *>(smem + L::S);    // [key][kPad rows]
     uint64_t *masks = reinterpret_cast<uint64_t *>(smem + L::MASK);
-    int *flags = reinterpret_cast<int *>(smem + L::FLAG);
+    int *flags = reinterpret_cast<int *>(smem + L::FLAG);  // which keys are there (2), whether a row is to be taken again
     Plan P = plan_at(smem + L::PLAN, p.B, p.ng, p.Hkv);
     make_plan(p, P);
     asm volatile("griddepcontrol.launch_dependents;");
@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
 
     UnitRoom *room = reinterpret_cast<UnitRoom *>(smem + L::ROOM);
     if (tid == 0) {
+        flags[2] = 0;
         room->units.begin(p, P, blockIdx.x);
         fill_room(p, P, room, 0);
     }
@@ -112,9 +113,9 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
                 for (int k = 0; k < VE; ++k) KV[(c * VE + k) * kPad + key] = element<T>(w, k);
             }
             const unsigned there = __ballot_sync(kAllLanes, pg >= 0);  // of keys 32 (warp & 1) ...
-            if (warp < 2 && lane == 0) flags[kTR - 2 + warp] = (int)there;
+            if (warp < 2 && lane == 0) flags[warp] = (int)there;
             __syncthreads();
-            const uint64_t present = (uint32_t)flags[kTR - 2] | ((uint64_t)(uint32_t)flags[kTR - 1] << 32);
+            const uint64_t present = (uint32_t)flags[0] | ((uint64_t)(uint32_t)flags[1] << 32);
             float s[8][4];
 #pragma unroll
             for (int r = 0; r < 8; ++r)
@@ -199,9 +200,6 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
                 }
             }
         }
-        __syncthreads();
-        if (tid < kTR) flags[tid] = 0;
-        __syncthreads();
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
 #pragma unroll
@@ -214,7 +212,7 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
             bool bad = not_finite(l[r]);
 #pragma unroll
             for (int x = 0; x < 4 * ND; ++x) bad |= not_finite(acc[r][x]);
-            if (bad && valid) flags[rr] = 1;
+            if (bad && valid) flags[2] = 1;
             if (U.split) {
 #pragma unroll
                 for (int h = 0; h < ND; ++h)
@@ -231,17 +229,9 @@ __global__ void __launch_bounds__(kTT, D == 64 ? 4 : 2) paged_tile(const __grid_
                         o[h * 64 + tx * 4 + x] = from_float<T>(valid ? acc[r][h * 4 + x] * inv : 0.f);
             }
         }
-        __syncthreads();
-        for (int rr = warp; rr < p.rows; rr += kTT / 32)
-            if (flags[rr]) {
-                int t, head;
-                row_token(p, U, rr, p.tpt_half, t, head);
-                float a[D / 32];
-                const float2 ml = exact_row<T, D>(p, P, U, t, head, a);
-                store_exact_row<T, D>(p, U, t, head, rr, ml, a);
-            }
         __syncthreads();  // every warp is done with the unit
     }
+    if (flags[2]) rows_again<T, D, 4>(p, smem + L::PLAN, warp, kTT / 32);
 }
 
 template <typename T, int D>

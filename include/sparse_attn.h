@@ -498,7 +498,9 @@ sa_status bigbird_attn_fwd_noalloc(const void *Q, const void *K, const void *V, 
  *   head h / (Hq / Hkv).
  * Rows t >= q_lens[b], and rows that see no key, are written as zeros. What
  * memory holds where no token was written, or at keys a row does not see, does
- * not reach that row, infinities and NaN included.
+ * not reach that row, infinities and NaN included. (Rows next to such values
+ * are computed twice, the second time by the definition: right, but slow where
+ * many rows of a long sequence see one.)
  * A sequence whose seq_lens or q_lens break the contract (or do not fit its
  *   table row) gets zeros and latches SA_ERR_BAD_INDEX; a table entry outside
  *   [-1, num_pages) counts as -1 and latches it.

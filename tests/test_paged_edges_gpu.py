@@ -107,3 +107,29 @@ def test_trim_keeps_the_pages_of_rows_and_lists_that_break_the_contract(in_place
         got = sa.cache_trim(T, ints(lens).cuda(), R, 16, 8, ints(g).cuda(), out=(T, R) if in_place else None)
         assert sa.get_last_device_status() == _lib.SA_ERR_BAD_INDEX
         assert got[0].tolist() == table.tolist() and got[1].tolist() == refs.tolist()
+
+
+# ------------------------------------------------------------------ rows computed again by the definition
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,H,G", [(300, 110, 1), (60, 160, 1), (64, 40, 4)])
+def test_an_infinity_that_every_row_sees_of_a_long_history(m, H, G, d):
+    """Every row of every unit is computed again, several units to a CTA, and no wait runs out over it."""
+    n = 16000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    K, V = (torch.randn(n // 128, H, 128, d, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    Q = torch.randn(1, H * G, m, d, generator=gen, device="cuda", dtype=torch.bfloat16)
+    T, L = torch.arange(n // 128, dtype=torch.int32, device="cuda")[None].contiguous(), ints([n]).cuda()
+    clean = sa.longformer_attn_paged_fwd(Q, K, V, T, L, 2 * n)
+    V[0, :, 0, 7] = float("inf")
+    torch.cuda.synchronize()
+    sa.set_option(sa.SA_OPT_WAIT_LIMIT, 10_000)  # a unit's rows take longer than these 10 ms, its waits microseconds
+    try:
+        got = sa.longformer_attn_paged_fwd(Q, K, V, T, L, 2 * n)
+        torch.cuda.synchronize()
+    finally:
+        sa.set_option(sa.SA_OPT_WAIT_LIMIT, 0)
+    assert sa.get_last_device_status() == 0
+    assert bool(torch.isposinf(got[..., 7]).all())
+    got[..., 7] = clean[..., 7]
+    # the weights' rounding of one (2^-8 of a mean of |v| < 2 over 16000 keys), the results' of both
+    torch.testing.assert_close(got.float(), clean.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
