@@ -18,6 +18,9 @@ namespace sa {
 // and 167, 271 and 240, 481 and 356 us.
 constexpr int kRowsBf16 = 1, kRowsFp32 = 8, kFewRows = 24;
 
+// ns: the longest walk of a global token that is left to one CTA (paged_shape).
+constexpr long long kGlobalWalk = 200000;
+
 PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int num_sms) {
     p.group = p.Hq / p.Hkv;
     p.log_page = p.page == 16 ? 4 : p.page == 32 ? 5 : p.page == 64 ? 6 : 7;
@@ -82,21 +85,33 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
     // The device decides by the lengths. The host leaves plan and join out where
     // splitting would not pay if every tile took the longest walk, and that is not so
     // long that uneven lengths would make up for it. No tile walks more than its table
-    // row or, without dilation, its window and the blocks of the global positions
-    // (some 16 to a block, or listed 64 to an entry).
+    // row or, without dilation, its window and a block per global position (listed
+    // ones 64 to an entry); but one with a global token, which only the device can tell,
+    // walks its whole sequence. Such tokens are few, and plan and join cost every call (a
+    // step of one sequence, window 512, 16 global: 10.0 us with, 7.8 without), so they
+    // come in for it where its walk would take kGlobalWalk in one CTA: a global token at
+    // the end of 65536 keys, 12 heads of 64, takes 60 us with them and 536 without.
     p.whole = split_ns / block_ns;
     const long long tiles = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt);
-    long long longest = (((long long)p.max_pages << p.log_page) + 63) >> 6;
+    const long long row = (((long long)p.max_pages << p.log_page) + 63) >> 6;
+    long long longest = row;
     if (!p.dilation && p.half < longest << 6) {
-        const long long band = (((long long)p.half + p.tpt) >> 6) + 2 + (p.listed ? (p.ng + 63) >> 6 : (p.ng + 15) >> 4);
+        const long long band = (((long long)p.half + p.tpt) >> 6) + 2 + (p.listed ? (p.ng + 63) >> 6 : p.ng);
         longest = band < longest ? band : longest;
     }
     longest += p.cost;
     const long long ctas = (long long)num_sms * per_sm;
-    const long long pieces = tiles * (longest / p.min_piece + 1);
-    const long long most = pieces < ctas ? pieces : ctas;
-    p.cut = (tiles + ctas - 1) / ctas * longest - tiles * longest / most > p.whole || longest > 2ll * p.whole;
-    p.slots = (int)(p.cut ? most : tiles < ctas ? tiles : ctas);
+    auto share = [&](long long walk) {  // CTAs that get a piece each
+        const long long pieces = tiles * (walk / p.min_piece + 1);
+        return pieces < ctas ? pieces : ctas;
+    };
+    p.cut = (tiles + ctas - 1) / ctas * longest - tiles * longest / share(longest) > p.whole || longest > 2ll * p.whole ||
+            (p.ng > 0 && row * block_ns > kGlobalWalk);
+    // A global token's walk may be shared by a CTA per SM; more of them, idle on most
+    // calls, would cost those (5 tokens of 8 sequences in fp32: 36 us, 42 with 4 per SM).
+    long long slots = p.cut ? share(longest) : tiles < ctas ? tiles : ctas;
+    if (p.cut && p.ng > 0 && slots < num_sms) slots = share(row + p.cost) < num_sms ? share(row + p.cost) : num_sms;
+    p.slots = (int)slots;
     return kind;
 }
 

@@ -59,8 +59,9 @@ struct Plan {
     int *q, *s;        // [B] new tokens and tokens in the cache (q = 0 for a refused sequence)
     int *gpos;         // [ng] global positions
     int *gblk;         // [ngb] 64-key blocks that hold one, ascending
+    int *far;          // [B] what global positions add to the length of a sequence's tiles (far_blocks)
     int *hstride;      // [Hkv] longest stride of a key head's query heads (with dilation)
-    int *misc;         // [0] ngb, [1] CTAs (0: whole tiles in turn), [2] remainder of the shares
+    int *misc;         // [4] [0] ngb, [1] CTAs (0: whole tiles in turn), [2] remainder of the shares
     int ngb;
     int ctas;          // CTAs that share the axis
     long long share;   // its length divided by them: share * ctas + rest
@@ -69,7 +70,7 @@ struct Plan {
 };
 
 __host__ __device__ constexpr size_t plan_bytes(int B, int ng, int Hkv) {
-    return 8 * (size_t)(B + 2 + ng) + (((2 * (size_t)B + 2 * (size_t)ng + Hkv + 4) * 4 + 15) & ~(size_t)15);
+    return 8 * (size_t)(B + 2 + ng) + (((2 * (size_t)B + 2 * (size_t)ng + (ng > 0 ? B : 0) + Hkv + 4) * 4 + 15) & ~(size_t)15);
 }
 
 __device__ __forceinline__ Plan plan_at(void *smem, int B, int ng, int Hkv) {
@@ -80,7 +81,8 @@ __device__ __forceinline__ Plan plan_at(void *smem, int B, int ng, int Hkv) {
     P.s = P.q + B;
     P.gpos = P.s + B;
     P.gblk = P.gpos + ng;
-    P.hstride = P.gblk + ng;
+    P.far = P.gblk + ng;
+    P.hstride = P.far + (ng > 0 ? B : 0);
     P.misc = P.hstride + Hkv;
     P.ngb = 0;
     P.ctas = 1;
@@ -124,15 +126,26 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 }
 
 // Length on the common axis of one tile of a sequence for a key head of that
-// stride: an estimate of the blocks it walks (a sixteenth of the global
-// positions have a block of their own: most lie together; listed ones are 64 to
-// an entry), and its fixed cost.
+// stride: an estimate of the blocks it walks, and its fixed cost. `far`: what
+// global positions add to the window (far_blocks).
 // It decides how evenly the work is spread, nothing else.
-__device__ __forceinline__ int tile_length(const PagedProblem &p, const Plan &P, int q, int s, int stride) {
+__device__ __forceinline__ int tile_length(const PagedProblem &p, int q, int s, int stride, int far) {
     const int all = (s + 63) >> 6;
     const long long span = (long long)head_reach(p, stride) + min(q, p.tpt);
-    const long long band = (span >> 6) + 2 + (p.listed ? (p.ng + 63) >> 6 : (p.ng + 15) >> 4);
+    const long long band = (span >> 6) + 2 + far;
     return (band < all ? (int)band : all) + p.cost;
+}
+
+// Blocks that a sequence's tiles walk because of global positions: those before the
+// last tile's window that hold one (or, listed, the global keys there, 64 to an
+// entry); any number, if a new token is global and sees its whole sequence. (Then its
+// tile is the only long one, but the axis has one length per sequence and head.)
+__device__ inline int far_blocks(const PagedProblem &p, const Plan &P, int q, int s) {
+    const int i = lower_bound(P.gpos, p.ng, s - q);
+    if (i < p.ng && P.gpos[i] < s) return (int)(kPagedMaxLen >> 6);
+    const long long window = (long long)s - head_reach(p, 1) - min(q, p.tpt);  // where it begins
+    const int first = window > 0 ? (int)(window >> 6) : 0;
+    return p.listed ? (lower_bound(P.gpos, p.ng, first << 6) + 63) >> 6 : lower_bound(P.gblk, P.ngb, first);
 }
 
 // New tokens and tokens in the cache of a sequence; none of either if they break
@@ -245,6 +258,14 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
         for (int i = kept + lane; i < p.ng; i += 32) P.gpos[i] = 0x7fffffff;
         if (lane == 0) P.misc[0] = n;
     }
+    if (p.cut && p.ng > 0) {  // the lengths below go by the list
+        __syncthreads();
+        P.ngb = P.misc[0];
+    }
+    if (p.cut && p.ng > 0) {  // the lengths below go by the list
+        __syncthreads();
+        P.ngb = P.misc[0];
+    }
     if (p.cut && tid < 32) {
         long long base = 0;
         int longest = 0;
@@ -253,14 +274,16 @@ __device__ inline void make_plan(const PagedProblem &p, Plan &P) {
             long long v = 0;
             if (b < p.B) {
                 const int q = P.q[b], s = P.s[b], tiles = (q + p.tpt - 1) / p.tpt;
+                const int far = p.ng > 0 && tiles > 0 ? far_blocks(p, P, q, s) : 0;
+                if (p.ng > 0) P.far[b] = far;
                 v = (long long)p.Hkv * (all_tiles - tiles) * p.cost;  // tiles without tokens
                 if (!p.dilation) {
-                    const int len = tiles > 0 ? tile_length(p, P, q, s, 1) : 0;
+                    const int len = tiles > 0 ? tile_length(p, q, s, 1, far) : 0;
                     v += (long long)p.Hkv * tiles * len;
                     longest = max(longest, len);
                 } else if (tiles > 0) {
                     for (int h = 0; h < p.Hkv; ++h) {
-                        const int len = tile_length(p, P, q, s, P.hstride[h]);
+                        const int len = tile_length(p, q, s, P.hstride[h], far);
                         v += (long long)tiles * len;
                         longest = max(longest, len);
                     }
@@ -321,6 +344,9 @@ struct Tile {
         // the longest sweeps first
         t0 = (live ? tiles - 1 - i : tiles + i % ((p.m + p.tpt - 1) / p.tpt - tiles)) * p.tpt;
     }
+    __device__ __forceinline__ int length(const PagedProblem &p, const Plan &P, int stride) const {
+        return tile_length(p, q, s, stride, p.ng > 0 ? P.far[b] : 0);
+    }
     __device__ __forceinline__ int head(const PagedProblem &p) const {  // key head
         return live ? hk : i / ((p.m + p.tpt - 1) / p.tpt - tiles);
     }
@@ -332,7 +358,7 @@ struct Tile {
         tiles = (q + p.tpt - 1) / p.tpt;
         i = 0;
         hk = tiles > 0 ? 0 : p.Hkv;
-        if (tiles > 0) len = tile_length(p, P, q, s, p.dilation ? P.hstride[0] : 1);
+        if (tiles > 0) len = length(p, P, p.dilation ? P.hstride[0] : 1);
     }
     __device__ __forceinline__ void advance(const PagedProblem &p, const Plan &P) {
         begin = end;
@@ -340,7 +366,7 @@ struct Tile {
             if (b + 1 < p.B) start(p, P, b + 1);
         } else if (++i == tiles && live) {
             i = 0;
-            if (++hk < p.Hkv && p.dilation) len = tile_length(p, P, q, s, P.hstride[hk]);
+            if (++hk < p.Hkv && p.dilation) len = length(p, P, P.hstride[hk]);
         }
         place(p);
     }
@@ -364,7 +390,7 @@ __device__ __forceinline__ Tile find_tile(const PagedProblem &p, const Plan &P, 
             off -= T.hk * per;
         } else {
             for (; T.hk < p.Hkv; ++T.hk) {
-                T.len = tile_length(p, P, T.q, T.s, P.hstride[T.hk]);
+                T.len = T.length(p, P, P.hstride[T.hk]);
                 const long long per = (long long)T.len * T.tiles;
                 if (off < per) break;
                 T.begin += per;

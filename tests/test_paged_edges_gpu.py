@@ -133,3 +133,15 @@ def test_an_infinity_that_every_row_sees_of_a_long_history(m, H, G, d):
     got[..., 7] = clean[..., 7]
     # the weights' rounding of one (2^-8 of a mean of |v| < 2 over 16000 keys), the results' of both
     torch.testing.assert_close(got.float(), clean.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+
+
+# ------------------------------------------------------------------ long walks that few tiles hold
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("m,Hq", [(1, 2), (3, 2), (40, 2), (150, 2)])
+def test_a_global_token_of_a_long_sequence_is_shared_out(m, Hq, dtype):
+    """One token among the new ones is global: its tile walks all keys, which no single CTA should do alone."""
+    lens, g = [30000, 200], [0, 29999 - m // 2]
+    Q, K, V, table = make_cache(95, 2, Hq, 2, m, 64, 64, lens, dtype)
+    attend_and_check(Q, K, V, table, lens, None, 256, g, None, dtype)
+    assert _lib.lib().sa_last_launch_count() == 2  # the sweeps, and the join of their pieces
+    attend_and_check(Q, K, V, table, lens, None, 256, list(range(0, 29000, 64))[:400], None, dtype)  # a block each
