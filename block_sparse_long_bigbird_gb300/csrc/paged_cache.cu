@@ -192,12 +192,18 @@ __device__ inline int list_free_pages(const PoolProblem &p, int32_t *list, int w
 // Scratch of fork and reserve: what each row gets.
 __host__ __device__ inline int up32(int x) { return (x + 31) & ~31; }
 
+// The page that a table entry names, or -1; entries outside [-1, num_pages) count
+// as -1 and are latched.
+__device__ __forceinline__ int page_in(const PoolProblem &p, int v) {
+    if (v < -1 || v >= p.num_pages) {
+        atomicOr(p.status, kDevBadIndex);
+        return -1;
+    }
+    return v;
+}
+
 // One holder of page v lets go of it.
 __device__ __forceinline__ void drop_page(const PoolProblem &p, int v) {
-    if (v >= p.num_pages) {
-        atomicOr(p.status, kDevBadIndex);
-        return;
-    }
     if (atomicSub(p.refs_out + v, 1) <= 0) {  // the table names a page that nobody holds
         atomicAdd(p.refs_out + v, 1);
         atomicOr(p.status, kDevBadIndex);
@@ -295,18 +301,13 @@ __global__ void __launch_bounds__(kMoveThreads) fork_apply(const PoolProblem p) 
         const int len = p.lens_out[b], full = len >> p.log_page;
         for (int c = threadIdx.x; c < p.max_pages; c += blockDim.x) {
             // pages that the empty row had in reserve go back
-            const int old = p.table_in[(size_t)b * p.max_pages + c];
+            const int old = page_in(p, p.table_in[(size_t)b * p.max_pages + c]);
             if (old >= 0) drop_page(p, old);
             int v = -1;
-            if (c < full) {
-                v = p.table_in[(size_t)s * p.max_pages + c];
-                if (v >= p.num_pages) {
-                    atomicOr(p.status, kDevBadIndex);
-                    v = -1;
-                }
-                if (v >= 0) atomicAdd(p.refs_out + v, 1);
-            } else if (c == full && (len & (p.page - 1))) {
-                v = row_new[b];
+            if (c < full || (c == full && (len & (p.page - 1)))) {
+                v = page_in(p, p.table_in[(size_t)s * p.max_pages + c]);
+                if (c == full) v = row_new[b];
+                else if (v >= 0) atomicAdd(p.refs_out + v, 1);
             }
             p.table_out[(size_t)b * p.max_pages + c] = v;
         }
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(256) free_rows(const PoolProblem p) {
             const size_t at = (size_t)b * p.max_pages + c;
             const int v = p.table_in[at];
             if (gone) {
-                if (v >= 0) drop_page(p, v);
+                if (page_in(p, v) >= 0) drop_page(p, v);
                 p.table_out[at] = -1;
             } else if (p.table_out != p.table_in) {
                 p.table_out[at] = v;
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(256) trim_rows(const PoolProblem p) {
             const size_t at = (size_t)b * p.max_pages + c;
             int v = p.table_in[at];
             const long long end = ((long long)c + 1) << p.log_page;
-            if (v >= 0 && !keep_all && end <= lowest) {
+            if (page_in(p, v) >= 0 && !keep_all && end <= lowest) {
                 int lo = 0, hi = p.ng;  // first global position in or after the page
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) reserve_plan(const PoolProble
         int c0, c1, n = 0;
         if (!reserve_range(p, b, c0, c1) && lane == 0) atomicOr(p.status, kDevBadIndex);
         for (int c = c0 + lane; c - lane < c1; c += 32)
-            n += __popc(__ballot_sync(kAll, c < c1 && p.table_in[(size_t)b * p.max_pages + c] < 0));
+            n += __popc(__ballot_sync(kAll, c < c1 && page_in(p, p.table_in[(size_t)b * p.max_pages + c]) < 0));
         if (lane == 0) base[b] = n;
     }
     __syncthreads();
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(256) reserve_apply(const PoolProblem p) {
         for (int c = lane; c - lane < p.max_pages; c += 32) {
             const size_t i = (size_t)b * p.max_pages + c;
             int v = c < p.max_pages ? p.table_in[i] : 0;
-            const bool want = c < p.max_pages && c >= c0 && c < c1 && v < 0;
+            const bool want = c < p.max_pages && c >= c0 && c < c1 && (v < 0 || v >= p.num_pages);
             const unsigned m = __ballot_sync(kAll, want);
             const int k = at + __popc(m & ((1u << lane) - 1u));
             at += __popc(m);
@@ -461,7 +462,12 @@ __global__ void __launch_bounds__(kBookThreads, 1) compact_plan(const PoolProble
     const int lane = threadIdx.x & 31;
     int lo, hi, live, n = 0;
     warp_stretch(p.num_pages, lo, hi);
-    for_counts(p.refs_in, lo, hi, 0, [&](int, int v) { n += __popc(__ballot_sync(kAll, v > 0)); });
+    bool negative = false;
+    for_counts(p.refs_in, lo, hi, 0, [&](int, int v) {
+        n += __popc(__ballot_sync(kAll, v > 0));
+        negative |= v < 0;
+    });
+    if (negative) atomicOr(p.status, kDevBadIndex);
     const int live_before = warp_prefix(n, sh, live);
     // rank of a hole i < L: free pages before it; of a mover i >= L: live pages
     // before it, less the live ones below L
@@ -479,7 +485,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) compact_plan(const PoolProble
         const unsigned m = __ballot_sync(kAll, v > 0);
         if (v > 0 && i >= live) movers[rank + __popc(m & ((1u << lane) - 1u))] = i;
         rank += __popc(m);
-        if (i < hi) to[i] = i;
+        if (i < hi) to[i] = v > 0 ? i : -1;  // what is free has no place
     });
     __syncthreads();
     const int moves = live - live_below;
@@ -500,11 +506,12 @@ __global__ void __launch_bounds__(kMoveThreads) compact_apply(const PoolProblem 
     const long long cells = (long long)p.B * p.max_pages;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < cells;
          i += (long long)gridDim.x * blockDim.x) {
-        const int v = p.table_in[i];
-        int w = v;
-        if (v >= p.num_pages) atomicOr(p.status, kDevBadIndex);
-        else if (v >= 0) w = to[v];
-        p.table_out[i] = w;
+        int v = page_in(p, p.table_in[i]);
+        if (v >= 0) {
+            v = to[v];
+            if (v < 0) atomicOr(p.status, kDevBadIndex);  // the table names a page that nobody holds
+        }
+        p.table_out[i] = v;
     }
     move_pages(p, movers, holes, *n_mv, blockIdx.x, gridDim.x);
 }

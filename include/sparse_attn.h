@@ -555,7 +555,8 @@ sa_status sa_cache_append(const void *K_new, const void *V_new, void *K_pages, v
  * page_bytes = Hkv * page * d * element size (a multiple of 16). The
  * bookkeeping arrays are read from *_in and written whole to *_out; the two may
  * be the same array, and must not overlap otherwise. Page numbers are chosen
- * by the inputs alone: the lowest free pages, in order.
+ * by the inputs alone: the lowest free pages, in order. A table entry outside
+ * [-1, num_pages) that a call uses counts as -1 and latches SA_ERR_BAD_INDEX.
  * workspace: sa_cache_workspace_bytes(num_pages, B) bytes.
  * Errors: SA_ERR_INVALID_ARG for sizes or pointers outside the contract or a
  *   workspace too small; SA_ERR_UNSUPPORTED / SA_ERR_CUDA as above.
@@ -617,7 +618,9 @@ sa_status sa_cache_reserve(int num_pages, int page, int B, int max_pages,
 
 /* sa_cache_compact - leaves the L pages in use (ref_count > 0) at [0, L): the
  * k-th page in use at or past L moves, in every layer of both pools, to the
- * k-th free page before L; table and counts follow. */
+ * k-th free page before L; table and counts follow. An entry that names a page
+ * with the count 0 becomes -1 and latches SA_ERR_BAD_INDEX, as does a count
+ * below 0 (the page is free). */
 sa_status sa_cache_compact(void *K_pages, void *V_pages, int layers, int num_pages, size_t page_bytes,
                            int B, int max_pages, const int32_t *table_in, const int32_t *ref_in,
                            int32_t *table_out, int32_t *ref_out,

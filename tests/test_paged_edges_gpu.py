@@ -109,6 +109,71 @@ def test_trim_keeps_the_pages_of_rows_and_lists_that_break_the_contract(in_place
         assert got[0].tolist() == table.tolist() and got[1].tolist() == refs.tolist()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_table_entries_that_name_no_page_are_latched(in_place):
+    """Entries outside [-1, 30) count as none in every call that uses them."""
+    table, lens, refs = _book()
+
+    def call(f, bad, *more):
+        T, R = dev(*map(torch.from_numpy, (bad, refs)))
+        L = ints(lens).cuda()
+        out = {"out": (T, L, R) if f in (sa.cache_fork, sa.cache_free) else (T, R)} if in_place else {}
+        if f is sa.cache_fork or f is sa.cache_compact:
+            K, V = (torch.arange(30, dtype=torch.float32, device="cuda").view(30, 1, 1, 1).expand(30, 1, 16, 64).contiguous()
+                    for _ in range(2))
+            got = f(K, V, T, L, R, *more, **out) if f is sa.cache_fork else f(K, V, T, R, **out)
+        elif f is sa.cache_free:
+            got = f(T, L, R, *more, **out)
+        elif f is sa.cache_trim:
+            got = f(T, L, R, *more, **out)
+        else:
+            got = f(T, L, more[0], R, *more[1:], **out)
+        return [x.tolist() for x in got], sa.get_last_device_status()
+
+    src, dst, row1 = ints([1]).cuda(), ints([2]).cuda(), ints([1]).cuda()
+    for v in (-2, 30, -2 ** 31, 2 ** 31 - 1):
+        # a page of the middle, the partial last one, and one past the length
+        for col, calls in ((1, ((sa.cache_fork, (src, dst)), (sa.cache_free, (row1,)), (sa.cache_trim, (16, 8)), (sa.cache_compact, ()))),
+                           (3, ((sa.cache_fork, (src, dst)), (sa.cache_free, (row1,)), (sa.cache_compact, ()))),
+                           (2, ((sa.cache_reserve, (ints([0, 20, 0, 0]).cuda(), 16)),))):
+            bad, none = table.copy(), table.copy()
+            bad[1, col], none[1, col] = v, -1
+            for f, more in calls:
+                want, ok = call(f, none, *more)
+                assert ok == 0
+                got, status = call(f, bad, *more)
+                assert status == _lib.SA_ERR_BAD_INDEX, (f.__name__, v, col)
+                if got[0][1][col] == v:  # a call that leaves the row as it is leaves the entry too
+                    got[0][1][col] = -1
+                assert got == want, (f.__name__, v, col)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_does_not_follow_entries_of_free_pages(in_place):
+    """An entry whose page has the count 0 would name another sequence's page after the move: it becomes -1."""
+    table, lens, refs = _book()
+    table[1, 0], table[3, 1] = 2, 25  # free: below and past the pages in use
+    refs = np.zeros(30, np.int32)
+    np.add.at(refs, table[table >= 0], 1)
+    refs[2] = refs[25] = 0
+    want = table.copy()
+    want[1, 0] = want[3, 1] = -1
+    wt, wr, moves = op.compact(want, refs)
+    K = torch.arange(30, dtype=torch.float32, device="cuda").view(30, 1, 1, 1).expand(30, 1, 16, 64).contiguous()
+    V = K + 100
+    T, R = dev(*map(torch.from_numpy, (table, refs)))
+    t, r = sa.cache_compact(K, V, T, R, out=(T, R) if in_place else None)
+    assert sa.get_last_device_status() == _lib.SA_ERR_BAD_INDEX
+    assert t.tolist() == wt and r.tolist() == wr
+    for a, b in moves:
+        assert float(K[b].min()) == float(K[b].max()) == a and float(V[b].min()) == 100 + a
+    negative = refs.copy()
+    negative[2] = -1  # a count below 0 is no count: the page is free
+    T, R = dev(*map(torch.from_numpy, (want, negative)))
+    t, r = sa.cache_compact(K, V, T, R)
+    assert sa.get_last_device_status() == _lib.SA_ERR_BAD_INDEX and t.tolist() == wt and r.tolist() == wr
+
+
 # ------------------------------------------------------------------ rows computed again by the definition
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("m,H,G", [(300, 110, 1), (60, 160, 1), (64, 40, 4)])
