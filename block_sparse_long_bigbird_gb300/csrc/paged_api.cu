@@ -363,6 +363,7 @@ sa_status sa_cache_reserve(int num_pages, int page, int B, int max_pages, const 
     if (s != SA_OK) return s;
     if (!page_ok(page) || !seq_lens || !q_lens || !al4(seq_lens) || !al4(q_lens)) return SA_ERR_INVALID_ARG;
     if ((long long)max_pages * page > sa::kPagedMaxLen) return SA_ERR_UNSUPPORTED;
+    if ((long long)B * max_pages > 0x7fffffffll) return SA_ERR_UNSUPPORTED;  // the pages asked for are counted in 32 bits
     if ((s = ws_ok(workspace, workspace_bytes, sa_cache_workspace_bytes(num_pages, B))) != SA_OK) return s;
     sa::PoolProblem p = {};
     int sms = 0, launches = 0;

@@ -609,7 +609,7 @@ sa_status sa_cache_trim(int num_pages, int page, int B, int max_pages, int reach
  * seq_lens[b]) of every row: each table entry past the old tokens' last page up
  * to the new last page that is -1 gets the lowest free page (ref_count 1), rows
  * in order. With too few free pages the last entries stay -1 and
- * SA_ERR_NO_PAGES is latched. */
+ * SA_ERR_NO_PAGES is latched. Limit: B * max_pages < 2^31. */
 sa_status sa_cache_reserve(int num_pages, int page, int B, int max_pages,
                            const int32_t *seq_lens, const int32_t *q_lens,
                            const int32_t *table_in, const int32_t *ref_in,
