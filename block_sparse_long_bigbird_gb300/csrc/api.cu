@@ -415,7 +415,6 @@ sa_status api_device(unsigned **status, int *num_sms) {
 void api_set_launches(int n) { g_last_launches = n; }
 bool api_force_simt() { return g_force_simt.load() != 0; }
 unsigned long long api_wait_ns() { return (unsigned long long)g_wait_limit.load() * 1000ull; }
-int api_grid_ctas() { return g_grid_ctas.load(); }
 
 }  // namespace sa
 

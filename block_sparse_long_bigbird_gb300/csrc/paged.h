@@ -114,6 +114,5 @@ sa_status api_device(unsigned **status, int *num_sms);
 void api_set_launches(int n);
 bool api_force_simt();
 unsigned long long api_wait_ns();
-int api_grid_ctas();
 
 }  // namespace sa

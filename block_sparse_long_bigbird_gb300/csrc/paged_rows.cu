@@ -397,7 +397,8 @@ cudaError_t launch_paged_merge(const PagedProblem &p, sa_dtype dtype, int num_sm
     void (*kern)(const PagedProblem, int) =
         dtype == SA_FP32 ? (p.d == 64 ? paged_merge<float, 64> : paged_merge<float, 128>)
                          : (p.d == 64 ? paged_merge<__nv_bfloat16, 64> : paged_merge<__nv_bfloat16, 128>);
-    // no more shared memory than a kernel has without asking: the largest plan takes 29 KB
+    static_assert(plan_bytes(kPagedMaxBatch, kPagedMaxGlobal, kPagedMaxHeads) <= 48 * 1024,
+                  "no more shared memory than a kernel has without asking");  // 29 KB
     // CTAs per tile: as many as its groups keep busy, within what fits the GPU at a time
     const long long tiles = (long long)p.B * p.Hkv * ((p.m + p.tpt - 1) / p.tpt);
     const int share = p.slots / tiles >= kMergeMany ? kMergeShare : 1;

@@ -392,6 +392,7 @@ const char *sa_status_string(sa_status status);
  *                      sweeps every key) at the cost of more partial results
  *                      to merge. The output does not depend on it beyond
  *                      rounding order.
+ * The calls of the paged cache follow the first two only.
  * Returns SA_ERR_INVALID_ARG for an unknown option.
  */
 enum { SA_OPT_FORCE_SIMT = 1, SA_OPT_WAIT_LIMIT = 2, SA_OPT_MAX_SPLITS = 3, SA_OPT_GRID_CTAS = 4,
