@@ -151,6 +151,8 @@ def _workspace_bytes(index, *sizes):
 
 def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None):
     """Scratch bytes of a longformer_attn_paged_fwd call of these sizes on `device` (default: the current one)."""
+    if dtype not in _DTYPE:
+        raise TypeError(f"unsupported dtype {dtype}; use bfloat16 or float32")
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
