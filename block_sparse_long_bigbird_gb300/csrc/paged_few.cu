@@ -27,9 +27,9 @@
 // Up to 8 rows P V is computed with P as the sum of two bf16 numbers (relative
 // 2^-16), which the rate allows; with more, P is rounded to bf16 (2^-8 of each
 // weight), as in the kernel for many rows.
-// Measured (16 sequences of 32768 keys, 8 key heads): d = 128, 4 rows 316 us, 6.8 TB/s
-// (a plain copy: 6.7), 16 rows 322, 24 rows 331 us; d = 64 170, 176 and 187 us, 6.3 to
-// 5.8 TB/s. One sequence of 900 keys takes 11.5 us (d = 64), a few hundred
+// Measured (16 sequences of 32768 keys, 8 key heads): d = 128, 4 rows 320 us, 6.7 TB/s
+// (a plain copy: 6.7), 16 rows 324, 24 rows 336 us; d = 64 170, 175 and 190 us, 6.3 to
+// 5.7 TB/s. One sequence of 900 keys takes 10.9 us (d = 64), a few hundred
 // clocks per item and warp: latency.
 // A row that does not see a key multiplies its value by 0; where that value is
 // infinite or NaN the row's sums come out so, and rows_again takes it again.

@@ -17,9 +17,11 @@
 // order, so results do not depend on timing.
 //
 // Measured (16 sequences of 32768 keys, one row per key head): bf16, 8 key heads, d =
-// 64 172 us, 6.2 TB/s; d = 128 316 us, 6.8 TB/s (a plain copy: 6.7); fp32, 4 key heads,
-// 16384 keys, d = 128, 168 us, 6.4 TB/s, two rows 172, four 197, eight 375 (there the
-// multiply-adds bound it). The smallest call takes 5.5 us, half of it launch and plan.
+// 64 173 us, 6.2 TB/s; d = 128 320 us, 6.7 TB/s (a plain copy: 6.7); fp32, 4 key heads,
+// 16384 keys, d = 128, 170 us, 6.3 TB/s, two rows 173, four 199, eight 377. Eight rows
+// leave an SM one CTA of 8 warps at 249 registers, which issues half of the time, much
+// of it the shuffles that sum each score over its lanes; the multiply-adds take 28% of
+// their rate and the memory 31%. The smallest call takes 5.5 us, half of it launch and plan.
 #include "paged_common.cuh"
 
 namespace sa {

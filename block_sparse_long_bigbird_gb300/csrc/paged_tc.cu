@@ -32,12 +32,12 @@
 // its copies and MMAs, frees TMEM and exits.
 //
 // Measured: 4096 tokens at the end of 32768 keys, 16 query and 4 key heads, d =
-// 128: 805 us, 1280 TFLOP/s (0.65 of the measured bf16 rate); with as many key as
-// query heads, 2 x 2048 tokens over 16384 keys: d = 128 430 us, 1190 TFLOP/s, d = 64
-// 420 us, 615 TFLOP/s. A 64-key block of two tiles takes 1.0 us whatever d is: the
+// 128: 826 us, 1250 TFLOP/s (0.63 of the measured bf16 rate); with as many key as
+// query heads, 2 x 2048 tokens over 16384 keys: d = 128 444 us, 1160 TFLOP/s, d = 64
+// 423 us, 610 TFLOP/s. A 64-key block of two tiles takes 1.0 us whatever d is: the
 // softmax bounds it (16384 exponentials per block, one thread per row), not the
-// tensor pipe (48% busy at d = 128) or the memory (3%). A window of 512, 4 x 4096
-// tokens, 12 heads, d = 64: 62 us; a unit of ten blocks takes 18400 clocks there: 2800 to
+// tensor pipe (47% busy at d = 128) or the memory (3%). A window of 512, 4 x 4096
+// tokens, 12 heads, d = 64: 66 us; a unit of ten blocks takes 18400 clocks there: 2800 to
 // start (record, rows, first scores), 10500 in its steps, 2000 for the last product
 // and 3100 to write O. Units of one tile that see little pay more: the first chain's
 // warps join both O's and write them (2300 to 6000 clocks). Loading their next

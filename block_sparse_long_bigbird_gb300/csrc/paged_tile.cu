@@ -9,8 +9,8 @@
 // a time); V takes K's buffer once the scores are done, which leaves room for
 // four CTAs per SM (d = 64; two at d = 128) to hide one another's loads and barriers:
 // with three, 512 tokens over 8192 keys (2 sequences, 16 heads, d = 64, fp32) took 1458
-// us, with four 994 us, 33.5 TFLOP/s of 75 that the multiply-adds allow (d = 128: 2650
-// us, 25 TFLOP/s). Rows in use matter: a unit is 64 rows whatever it holds.
+// us, with four 1000 to 1020 us, 33 TFLOP/s of 75 that the multiply-adds allow (d = 128:
+// 2690 us, 25 TFLOP/s). Rows in use matter: a unit is 64 rows whatever it holds.
 // Global keys before a tile's window are gathered 64 to a step, wherever they lie;
 // a step per block that holds one was half of all steps with 16 of them spread out.
 #include "paged_common.cuh"
