@@ -200,6 +200,43 @@ def test_an_infinity_that_every_row_sees_of_a_long_history(m, H, G, d):
     torch.testing.assert_close(got.float(), clean.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,Hq,Hkv,dtype", [(40, 2, 2, "bf16"), (150, 2, 2, "bf16"), (50, 16, 2, "bf16"), (20, 2, 2, "fp32"), (5, 16, 2, "fp32"),
+                                            (150, 2, 2, "simt")])
+def test_rows_taken_again_in_split_tiles(m, Hq, Hkv, dtype, d):
+    """Infinities and NaN in the last token, which only its own rows see, in tiles cut into many pieces; and
+    an infinite key that some rows' windows hold."""
+    lens, simt, dtype = [4000, 77 + m], dtype == "simt", dtype.replace("simt", "bf16")
+    sa.set_option(sa.SA_OPT_FORCE_SIMT, int(simt))
+    try:
+        Q, K, V, table = make_cache(96, 2, Hq, Hkv, m, d, 16, lens, dtype)
+        clean = f64(attend_and_check(Q, K, V, table, lens, None, 9000, None, None, dtype))
+        Vc = V.clone()
+        for b, n in enumerate(lens):
+            Vc[int(table[b, (n - 1) // 16]), :, (n - 1) % 16, 0] = float("inf")
+            Vc[int(table[b, (n - 1) // 16]), :, (n - 1) % 16, 1] = float("nan")
+        got = f64(sa.longformer_attn_paged_fwd(*dev(Q, K, Vc, table, ints(lens)), 9000))
+        assert np.isposinf(got[:, :, -1, 0]).all() and np.isnan(got[:, :, -1, 1]).all()
+        got[:, :, -1, :2] = clean[:, :, -1, :2]
+        # bf16: the weights' rounding of one (2^-8 of a mean of |v| < 4), the results' of both; fp32: sums in another order
+        assert np.allclose(got, clean, rtol=2.0 ** -7 if dtype == "bf16" else 2e-5, atol=2.0 ** -6 if dtype == "bf16" else 2e-6)
+        Kc = K.clone()  # one row's q k is infinite or NaN where the window holds the key: all of that row is NaN
+        at = lens[0] - m // 2 - 20
+        Kc[int(table[0, at // 16]), :, at % 16, 3] = float("inf")
+        want = f64(attend_and_check(Q, K, V, table, lens, None, 40, None, None, dtype))
+        got = f64(sa.longformer_attn_paged_fwd(*dev(Q, Kc, V, table, ints(lens)), 40))
+        seen = np.array([at <= lens[0] - m + t <= at + 20 for t in range(m)])
+        q3 = f64(Q)[0, :, :, 3]
+        nan = seen[None] & (q3 >= 0)  # +inf or NaN; a score of -inf is a weight of 0
+        assert np.isnan(got[0][nan]).all() and np.isfinite(got[0][~nan]).all() and np.isfinite(got[1]).all()
+        same = ~seen
+        assert np.allclose(got[0][:, same], want[0][:, same], rtol=2.0 ** -7 if dtype == "bf16" else 2e-5,
+                           atol=2.0 ** -6 if dtype == "bf16" else 2e-6)
+    finally:
+        sa.set_option(sa.SA_OPT_FORCE_SIMT, 0)
+    assert sa.get_last_device_status() == 0
+
+
 # ------------------------------------------------------------------ long walks that few tiles hold
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("m,Hq", [(1, 2), (3, 2), (40, 2), (150, 2)])
