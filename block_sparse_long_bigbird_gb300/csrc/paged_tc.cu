@@ -30,8 +30,9 @@
 // the CTA is through with its units.
 // Over pages of 4 bits a stage is filled by four more warps, which load the codes into registers
 // (a warp with nothing else to do looks the pages up) and write the halves they
-// stand for, zeros past the last token. Queries and weights are halves then too (the
-// weights to 2^-11). That bounds such calls: a stage of 128 keys takes the converters some 2700
+// stand for, zeros past the last token. Queries and weights are halves then too: weights to
+// 2^-11 and, as they are 2^7 at the reference, to 2^-32 of the largest (half of a half's smallest
+// number). That bounds such calls: a stage of 128 keys takes the converters some 2700
 // clocks, twice as long as they need alone, as little of their latency is hidden (one
 // such warp per scheduler; registers are out). Where a CTA takes many such steps the pages are
 // converted first instead (paged_unpack; kUnpackStep holds the rule): 4096 tokens over 32768
@@ -69,6 +70,7 @@ constexpr int kTcThreads = 384;   // 8 softmax warps, loader, two MMA issuers, s
 constexpr int kTcThreads4 = 512;  // and, over pages of 4 bits, four that convert
 constexpr int kRegion = 128 * 128;  // 128 rows x 128 B: one 64-column piece of a tile
 constexpr float kGrow = 8.0f;       // growth of the maximum (log2) that rescales O
+constexpr float kAbove = 7.0f;      // 4 bits: weights are 2^kAbove at the reference, as they are halves (up to 2^15)
 constexpr int kSI = 4;              // step records in flight
 constexpr int kNU = 4;              // units in flight
 constexpr int kPR = 8;              // 4 bits: page records in flight
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(P4 ? kTcThreads4 : kTcThreads, 1)
                                 tmem_wait_st();
                             }
                         }
-                        const float nref = mref == -CUDART_INF_F ? 0.f : -mref;
+                        const float nref = mref == -CUDART_INF_F ? 0.f : P4 ? kAbove - mref : -mref;
                         const uint64_t sl2x2 = f2_pack(sl2, sl2), nrefx2 = f2_pack(nref, nref);
                         uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
                         uint32_t pk[32];
@@ -615,6 +617,8 @@ __global__ void __launch_bounds__(P4 ? kTcThreads4 : kTcThreads, 1)
                         }
                     }
                 }
+                // what the sums are relative to: as in parts of this tile that are taken again
+                if (P4) mref -= kAbove;
                 if (U.split && in) p.part_ml[at] = make_float2(row.valid ? mref : -CUDART_INF_F, row.valid ? l : 0.f);
             } else if (U.split && in) {  // no valid row in this warp: the merge writes their zeros
                 p.part_ml[(size_t)U.slot * p.rows + prow] = make_float2(-CUDART_INF_F, 0.f);

@@ -1,0 +1,83 @@
+"""Pages held in 4 bits and the rotation of positions where they could go wrong: weights far below the largest, results of
+split tiles that are taken again."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_long_bigbird_gb300 as sa
+from oracle import paged4 as o4
+from oracle.paged import oracle_paged
+from paged4_util import attend4_and_check, bound4, make_cache4
+from paged_util import dev, f64, ints
+
+pytestmark = pytest.mark.gpu
+
+
+def _converts_first(B, Hq, Hkv, m, d, page, width, window, dilated=False, n_global=0):
+    """Whether a bf16 call turns its pages into scratch of bf16 ones first: only then is its scratch as large as they are."""
+    n = sa.paged_workspace_bytes(B, Hq, Hkv, m, d, page, width, torch.bfloat16, packed=True, window=window, dilated=dilated,
+                                 n_global=n_global)
+    return n >= 2 * B * width * Hkv * page * d * 2
+
+
+def _weights(Q, table, page, Hkv, window, dtype, **kw):
+    """How far off weights are: bf16 numbers (2^-8) only where the pages become bf16 ones first, halves (2^-11) else."""
+    B, Hq, m, d = Q.shape
+    first = dtype == "bf16" and _converts_first(B, Hq, Hkv, m, d, page, table.shape[1], window, **kw)
+    return 2.0 ** -8 if first else None
+
+
+# ------------------------------------------------------------------ weights far below the largest
+def _one_above_many(m, group, d, n, top, dtype):
+    """Every key is zero but the one at position `top`, which is 14 to 30 powers of two above the others, another power for
+    every row; its value is zero, so the others, however small their weights, are all there is of the result."""
+    rng = np.random.default_rng(m + d + n)
+    page = 64
+    pages = -(-n // page)
+    table = torch.from_numpy(rng.permutation(pages).astype(np.int32))[None].contiguous()
+    codes = [np.zeros((pages, 1, page, d // 2), dtype=np.uint8), rng.integers(0, 8, (pages, 1, page, d // 2), dtype=np.uint8)]
+    codes[1] |= rng.integers(0, 8, codes[1].shape, dtype=np.uint8) << 4
+    scales = [np.full((pages, 1, page, d // 16), 120, dtype=np.uint8) for _ in "KV"]  # 1
+    at = (int(table[0, top // page]), 0, top % page)
+    codes[0][at][0] = 7  # 6
+    codes[1][at] = 0
+    rows = np.linspace(14.0, 30.0, m * group).reshape(1, group, m)
+    Q = rng.standard_normal((1, group, m, d))
+    Q[..., 0] = rows * math.log(2.0) * math.sqrt(d) / 6
+    pools = [torch.from_numpy(o4.joined(c, s)) for c, s in zip(codes, scales)]
+    values = [o4.decode(c, s) for c, s in zip(codes, scales)]
+    return torch.from_numpy(Q).to(torch.bfloat16 if dtype == "bf16" else torch.float32), pools[0], pools[1], values, table
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+# few rows; chunks whose pages are converted on the way, of one tile and of two, whole and split
+@pytest.mark.parametrize("m,group,n,late", [(1, 1, 700, False), (1, 8, 5000, True), (24, 1, 3000, True), (100, 1, 1500, False),
+                                            (100, 1, 1500, True), (100, 1, 9000, False), (50, 2, 9000, True),
+                                            (200, 1, 500, False), (200, 1, 6000, True), (100, 2, 6000, False)])
+def test_weights_far_below_the_largest(m, group, n, late, d, dtype):
+    """2^-14 to 2^-30 of the largest: no coarser than 2^-32 of it, in whichever kernel."""
+    Q, K, V, values, table = _one_above_many(m, group, d, n, n - m if late else 0, dtype)
+    attend4_and_check(Q, K, V, values, table, [n], None, 4 * n, dtype=dtype, weights=_weights(Q, table, 64, 1, 4 * n, dtype))
+
+
+@pytest.mark.parametrize("m,group,d,n", [(100, 1, 64, 9000), (50, 2, 128, 9000), (200, 1, 64, 6000), (200, 1, 128, 6000),
+                                         (20, 1, 64, 9000), (4, 4, 128, 9000)])
+def test_parts_that_are_taken_again_join_those_that_are_not(m, group, d, n):
+    """Rows that a NaN at a masked key spoils are taken again in one part of a split tile only; the other parts stay."""
+    Q, K, V, values, table = make_cache4(91, 1, group, 1, m, d, 16, [n])
+    codes, scales = (x.copy() for x in o4.parts(V.numpy(), d))
+    last = n - 1
+    scales[int(table[0, last // 16]), 0, last % 16, 1] = 255
+    bad = torch.from_numpy(o4.joined(codes, scales))
+    args = dev(Q, K, bad, table, ints([n]))
+    got = f64(sa.longformer_attn_paged_fwd(*args, 4 * n))
+    assert sa._lib.lib().sa_last_launch_count() == 2  # split, not converted first
+    ref, A, S = oracle_paged(f64(Q), *values, table.numpy(), [n], None, 4 * n)
+    lim = bound4(ref, A, S, "bf16", n, d, np.nanmax(np.abs(values[1])))
+    assert (np.abs(got - ref)[:, :, :-1] <= lim[:, :, :-1]).all()
+    assert np.isnan(got[:, :, -1, 16:32]).all()
+    assert sa.get_last_device_status() == 0
