@@ -798,7 +798,9 @@ __global__ void __launch_bounds__(P4 ? kTcThreads4 : kTcThreads, 1)
             }
             unit_steps(n);
         }
-        if (!ok && qc) wait_drain(bar(C::B_QF), (qc - 1) & 1);  // abort: wait for the copy still in flight
+        // The copy may still be in flight where another role's wait ran out, also after this loop has
+        // seen the last unit; otherwise its data is long there.
+        if (qc) wait_drain(bar(C::B_QF), (qc - 1) & 1);
     } else if (warp == 8) {
         // ================================================================ loader of Q, K and V
         const int log_bp = min(p.log_page, 6);  // tokens of a box: a page, at most 64
@@ -878,11 +880,11 @@ __global__ void __launch_bounds__(P4 ? kTcThreads4 : kTcThreads, 1)
             }
             unit_steps(n);
         }
-        if (!ok) {  // abort: wait for the copies still in flight
-            for (int i = 0; i < C::NST; ++i)
-                if ((armed >> i) & 1u) wait_drain(bar(C::B_KF + i), (phase >> i) & 1u);
-            if (qc) wait_drain(bar(C::B_QF), (qc - 1) & 1);
-        }
+        // Copies may still be in flight where another role's wait ran out, also after this loop has seen the
+        // last unit; otherwise their data is long there.
+        for (int i = 0; i < C::NST; ++i)
+            if ((armed >> i) & 1u) wait_drain(bar(C::B_KF + i), (phase >> i) & 1u);
+        if (qc) wait_drain(bar(C::B_QF), (qc - 1) & 1);
     } else if (warp == 10) {
         // ================================================================ step records
         // What each step holds for the tiles, ahead of their use. Lane l looks

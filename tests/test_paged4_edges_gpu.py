@@ -81,3 +81,33 @@ def test_parts_that_are_taken_again_join_those_that_are_not(m, group, d, n):
     assert (np.abs(got - ref)[:, :, :-1] <= lim[:, :, :-1]).all()
     assert np.isnan(got[:, :, -1, 16:32]).all()
     assert sa.get_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ waits that run out while the last copies are on their way
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("m,Hq,Hkv,d", [(100, 2, 2, 64), (100, 1, 1, 128), (60, 4, 2, 128), (200, 2, 2, 64), (256, 1, 1, 128)])
+def test_waits_that_run_out_after_the_last_unit_was_seen(m, Hq, Hkv, d, packed):
+    """A unit or less to a CTA: its loader has nothing left to do while its copies, out of cold memory, are still in flight and
+    the other roles give up. No copy may outlive its CTA; the calls that follow are exact."""
+    lens = [m + 100]
+    Q, K, V, values, table = make_cache4(95, 1, Hq, Hkv, m, d, 64, lens)
+    if not packed:
+        K, V = (torch.from_numpy(np.nan_to_num(v)).to(torch.bfloat16) for v in values)
+    args = dev(Q, K, V, table, ints(lens))
+    want = sa.longformer_attn_paged_fwd(*args, 4000)
+    cold = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")  # larger than the L2
+    torch.cuda.synchronize()
+    assert sa.get_last_device_status() == 0 and torch.isfinite(want).all()
+    for _ in range(4):
+        sa.set_option(sa.SA_OPT_WAIT_LIMIT, 1)  # 1 microsecond
+        try:
+            cold.zero_()
+            sa.longformer_attn_paged_fwd(*args, 4000)
+            torch.cuda.synchronize()
+        finally:
+            sa.set_option(sa.SA_OPT_WAIT_LIMIT, 0)
+        got = sa.longformer_attn_paged_fwd(*args, 4000)
+        torch.cuda.synchronize()
+        assert sa.get_last_device_status() in (sa._lib.SA_OK, sa._lib.SA_ERR_TIMEOUT)
+        assert torch.equal(got, want)
+    assert sa.get_last_device_status() == 0
