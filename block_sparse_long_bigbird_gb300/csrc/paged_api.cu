@@ -300,7 +300,7 @@ size_t sa_longformer_paged_workspace_bytes_ex(int B, int Hq, int Hkv, int m, int
     if (sa::api_device(&status, &sms) != SA_OK) return 0;
     sa::PagedProblem p = {};
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.m = m; p.d = d; p.page = page; p.max_pages = max_pages;
-    p.half = window / 2;
+    p.half = pool == SA_POOL_PLAIN ? (int)sa::kPagedMaxLen : window / 2;  // plain pages: what any window needs
     p.dilation = dilated ? reinterpret_cast<const int32_t *>(&dilated) : nullptr;  // only whether there is one counts
     p.ng = n_global;
     p.packed = pool == SA_POOL_4BIT;

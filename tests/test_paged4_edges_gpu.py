@@ -11,7 +11,7 @@ import block_sparse_long_bigbird_gb300 as sa
 from oracle import paged4 as o4
 from oracle.paged import oracle_paged
 from paged4_util import attend4_and_check, bound4, make_cache4
-from paged_util import dev, f64, ints
+from paged_util import DT, dev, f64, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -110,4 +110,35 @@ def test_waits_that_run_out_after_the_last_unit_was_seen(m, Hq, Hkv, d, packed):
         torch.cuda.synchronize()
         assert sa.get_last_device_status() in (sa._lib.SA_OK, sa._lib.SA_ERR_TIMEOUT)
         assert torch.equal(got, want)
+    assert sa.get_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ scratch sizes
+@pytest.mark.parametrize("pool", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,Hq,Hkv,m,d,page,width", [(1, 12, 12, 1, 64, 64, 1024), (1, 4, 2, 7, 128, 16, 2000),
+                                                     (2, 8, 2, 100, 64, 32, 700), (1, 16, 4, 600, 128, 128, 70),
+                                                     (1, 64, 1, 20, 64, 64, 300)])
+def test_exactly_the_scratch_that_is_asked_for_will_do(B, Hq, Hkv, m, d, page, width, dtype, pool):
+    """Through the C entry points, for small and large windows, with and without dilations and global positions: the call takes
+    the scratch that the size function names for the same arguments, and touches nothing behind it."""
+    lib = sa._lib.lib()
+    lens = [width * page, width * page // 2 + m][:B]
+    Q, K, V, values, table = make_cache4(97, B, Hq, Hkv, m, d, page, lens, dtype)
+    if pool == 0:
+        K, V = (torch.from_numpy(np.nan_to_num(v)).to(DT[dtype]) for v in values)
+    Q, K, V, table, L = dev(Q, K, V, table, ints(lens))
+    g, dil = dev(ints([0, 3, 70, 900]), ints([h % 3 for h in range(Hq)]))
+    for window in (0, 64, 512, 4000, 0x7ffffffe):
+        for dilated in (0, 1):
+            for ng in (0, 4):
+                n = lib.sa_longformer_paged_workspace_bytes_ex(B, Hq, Hkv, m, d, page, width, window, dilated, ng, dtype == "fp32", pool)
+                ws = torch.full((n + 64,), 171, dtype=torch.uint8, device="cuda")
+                O = torch.full_like(Q, float("nan"))
+                status = lib.longformer_attn_paged_fwd_ex(
+                    Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), B, Hq, Hkv, m, d, page, K.shape[0], width,
+                    table.data_ptr(), L.data_ptr(), None, window, dil.data_ptr() if dilated else None, g.data_ptr() if ng else None, ng,
+                    ws.data_ptr() if n else None, n, dtype == "fp32", pool, torch.cuda.current_stream().cuda_stream)
+                assert status == 0, (window, dilated, ng, n)
+                assert torch.isfinite(O).all() and (ws[n:] == 171).all(), (window, dilated, ng, n)
     assert sa.get_last_device_status() == 0
