@@ -140,8 +140,8 @@ __device__ __forceinline__ void floats8(const Eight<T> &v, float (&o)[8]) {
     }
 }
 template <typename T>
-__device__ __forceinline__ void store8(void *base, size_t at, const float (&v)[8]) {
-    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(base) + at);
+__device__ __forceinline__ Eight<T> pack8(const float (&v)[8]) {
+    Eight<T> r;
     uint32_t w[sizeof(T) * 2];
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
@@ -149,7 +149,18 @@ __device__ __forceinline__ void store8(void *base, size_t at, const float (&v)[8
         else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[(2 * i + 1) & 7]), "f"(v[(2 * i) & 7]));
     }
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store8(void *base, size_t at, const Eight<T> &v) {
+    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(base) + at);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) out[i] = v.w[i];
+}
+template <typename T>
+__device__ __forceinline__ void store8(void *base, size_t at, const float (&v)[8]) {
+    store8<T>(base, at, pack8<T>(v));
 }
 
 // max |x| of eight numbers, NaN if one is NaN.
@@ -272,7 +283,8 @@ __global__ void __launch_bounds__(kWriteThreads, P4 ? 6 : 7) cache_write(const W
             }
         }
         const int gy = (int)gridDim.y;
-        // Heads h, h + gy, ... before `end` of one kind, rows of `from`; `done` gets each head's number and elements.
+        // Heads h, h + gy, ... before `end` of one kind, rows of `from`; `done` gets each head's number and elements
+        // (as they are: what is not rotated or coded keeps its bits, those of a NaN too).
         auto heads_of = [&](const void *from, int H, int h, int end, bool take, auto done) {
             Eight<T> na = {}, nb = {};
             const T *at = static_cast<const T *>(from) + (((size_t)b * H + h) * p.m + t) * D;
@@ -283,62 +295,74 @@ __global__ void __launch_bounds__(kWriteThreads, P4 ? 6 : 7) cache_write(const W
             }
 #pragma unroll 1
             for (; h < end; h += gy) {
-                float va[8], vb[8];
-                floats8<T>(na, va);
-                floats8<T>(nb, vb);
+                const Eight<T> ea = na, eb = nb;
                 at += step;
                 if (take && h + gy < end) {
                     na = load8<T>(at, pa);
                     nb = load8<T>(at, pb);
                 }
-                done(h, va, vb);
+                done(h, ea, eb);
             }
         };
         const bool there = live && pg >= 0;
         const size_t page_at = there ? (size_t)pg * p.Hkv : 0;
         const int in_page = pos & (p.page - 1);
-        auto put = [&](void *pool, int h, const float (&va)[8], const float (&vb)[8]) {
+        auto put = [&](void *pool, int h, Eight<T> ea, Eight<T> eb, bool turn) {
             const size_t row = ((page_at + h) << p.log_page) + in_page;
+            float va[8], vb[8];
             if constexpr (P4) {
+                floats8<T>(ea, va);
+                floats8<T>(eb, vb);
+                if (turn) turn8_exact<T, INTER>(va, vb, c, sn);
                 const float ta = top8(va), tb = top8(vb);
                 const float a1 = __shfl_sync(kAll, ta, la), a2 = __shfl_sync(kAll, tb, la);
                 const float b1 = __shfl_sync(kAll, ta, lb), b2 = __shfl_sync(kAll, tb, lb);
                 float ga = sa2 ? a2 : a1, gb = sb2 ? b2 : b1;
                 asm("max.NaN.f32 %0, %0, %1;" : "+f"(ga) : "f"(ta));
                 asm("max.NaN.f32 %0, %0, %1;" : "+f"(gb) : "f"(tb));
-                const uint32_t ea = scale_byte(ga), eb = scale_byte(gb);
-                const uint32_t wa = codes8(va, ea), wb = codes8(vb, eb);
+                const uint32_t sa = scale_byte(ga), sb = scale_byte(gb);
+                const uint32_t wa = codes8(va, sa), wb = codes8(vb, sb);
                 if (!there) return;
                 const Q4At at = q4_row<D>(row, p.page, p.log_page);
                 uint8_t *bytes = static_cast<uint8_t *>(pool);
                 *reinterpret_cast<uint32_t *>(bytes + at.codes + pa / 2) = wa;
                 *reinterpret_cast<uint32_t *>(bytes + at.codes + pb / 2) = wb;
-                if (!(pa & 8)) bytes[at.scales + pa / 16] = (uint8_t)ea;
-                if (!(pb & 8)) bytes[at.scales + pb / 16] = (uint8_t)eb;
+                if (!(pa & 8)) bytes[at.scales + pa / 16] = (uint8_t)sa;
+                if (!(pb & 8)) bytes[at.scales + pb / 16] = (uint8_t)sb;
             } else if (there) {
-                store8<T>(pool, row * D + pa, va);
-                store8<T>(pool, row * D + pb, vb);
+                if (turn) {
+                    floats8<T>(ea, va);
+                    floats8<T>(eb, vb);
+                    turn8<T, INTER>(va, vb, c, sn);
+                    ea = pack8<T>(va);
+                    eb = pack8<T>(vb);
+                }
+                store8<T>(pool, row * D + pa, ea);
+                store8<T>(pool, row * D + pb, eb);
             }
         };
         int h = blockIdx.y;
-        heads_of(p.Kn, p.Hkv, h, p.Hkv, there, [&](int k, float (&va)[8], float (&vb)[8]) {
-            if (turned) {
-                if constexpr (P4) turn8_exact<T, INTER>(va, vb, c, sn);
-                else turn8<T, INTER>(va, vb, c, sn);
-            }
-            put(p.K, k, va, vb);
-        });
+        heads_of(p.Kn, p.Hkv, h, p.Hkv, there,
+                 [&](int k, const Eight<T> &ea, const Eight<T> &eb) { put(p.K, k, ea, eb, turned); });
         while (h < p.Hkv) h += gy;
         h -= p.Hkv;
-        heads_of(p.Vn, p.Hkv, h, p.Hkv, there, [&](int k, float (&va)[8], float (&vb)[8]) { put(p.V, k, va, vb); });
+        heads_of(p.Vn, p.Hkv, h, p.Hkv, there,
+                 [&](int k, const Eight<T> &ea, const Eight<T> &eb) { put(p.V, k, ea, eb, false); });
         while (h < p.Hkv) h += gy;
         h -= p.Hkv;
         if (!in) continue;
-        heads_of(p.Qn, p.Hq, h, p.Hq, live, [&](int k, float (&va)[8], float (&vb)[8]) {
-            if (turned) turn8<T, INTER>(va, vb, c, sn);
+        heads_of(p.Qn, p.Hq, h, p.Hq, live, [&](int k, Eight<T> ea, Eight<T> eb) {
+            if (turned) {
+                float va[8], vb[8];
+                floats8<T>(ea, va);
+                floats8<T>(eb, vb);
+                turn8<T, INTER>(va, vb, c, sn);
+                ea = pack8<T>(va);
+                eb = pack8<T>(vb);
+            }
             const size_t dst = (((size_t)b * p.Hq + k) * p.m + t) * D;
-            store8<T>(p.Qo, dst + pa, va);
-            store8<T>(p.Qo, dst + pb, vb);
+            store8<T>(p.Qo, dst + pa, ea);
+            store8<T>(p.Qo, dst + pb, eb);
         });
     }
 }
@@ -399,16 +423,16 @@ __global__ void __launch_bounds__(kReadThreads) cache_read(const WriteProblem p)
                 const long long t = t0 + r * RPB;
                 if (t >= p.m) continue;
                 const size_t dst = ((size_t)bh * p.m + (size_t)t) * D + x * 8;
-                float kf[8], vf[8];
                 if constexpr (P4) {
+                    float kf[8], vf[8];
                     q4_floats(kc[r], ks[r], kf);
                     q4_floats(vc[r], vs[r], vf);
+                    store8<T>(p.Ko, dst, kf);
+                    store8<T>(p.Vo, dst, vf);
                 } else {
-                    floats8<T>(kw[r], kf);
-                    floats8<T>(vw[r], vf);
+                    store8<T>(p.Ko, dst, kw[r]);
+                    store8<T>(p.Vo, dst, vw[r]);
                 }
-                store8<T>(p.Ko, dst, kf);
-                store8<T>(p.Vo, dst, vf);
             }
         }
     }

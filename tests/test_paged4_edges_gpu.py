@@ -142,3 +142,35 @@ def test_exactly_the_scratch_that_is_asked_for_will_do(B, Hq, Hkv, m, d, page, w
                 assert status == 0, (window, dilated, ng, n)
                 assert torch.isfinite(O).all() and (ws[n:] == 171).all(), (window, dilated, ng, n)
     assert sa.get_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ rows that are only moved
+def _any_bits(shape, dtype, seed):
+    """Every pattern of bits as likely: infinities and NaNs of all kinds among them."""
+    g = torch.Generator().manual_seed(seed)
+    of = torch.int16 if dtype == "bf16" else torch.int32
+    return torch.randint(torch.iinfo(of).min, torch.iinfo(of).max + 1, shape, generator=g, dtype=torch.int64).to(of)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d,rot,interleaved", [(64, 32, False), (64, 16, True), (128, 48, False), (128, 128, True), (64, 64, False)])
+def test_what_is_not_rotated_keeps_its_bits(d, rot, interleaved, dtype):
+    """Values, elements from rot on, and rows read from plain pages: a NaN's bits too, as sa_cache_append moves them."""
+    B, Hkv, Hq, m, page, lens, q = 3, 2, 4, 9, 16, [40, 9, 23], [9, 9, 4]
+    bits = [_any_bits((B, h, m, d), dtype, i) for i, h in enumerate((Hkv, Hkv, Hq))]
+    assert all(torch.isnan(x.view(DT[dtype])).any() for x in bits)
+    kn, vn, qn = (x.view(DT[dtype]).cuda() for x in bits)
+    table = torch.arange(9, dtype=torch.int32).reshape(3, 3)
+    T, L, n = dev(table, ints(lens), ints(q))
+    K, V = (torch.zeros(9, Hkv, page, d, dtype=DT[dtype], device="cuda") for _ in "KV")
+    Kp, Vp = torch.zeros_like(K), torch.zeros_like(V)
+    sa.cache_append(kn, vn, Kp, Vp, T, L, q_lens=n)
+    _, _, Q = sa.cache_append(kn, vn, K, V, T, L, q_lens=n, rope=sa.rope_table(64, rot), interleaved=interleaved, Q_new=qn)
+    of = bits[0].dtype
+    assert torch.equal(V.view(of), Vp.view(of)) and torch.equal(K.view(of)[..., rot:], Kp.view(of)[..., rot:])
+    rows = [t.view(of).cpu() for t in sa.cache_read(Kp, Vp, T, L, m, q_lens=n)]
+    for b in range(B):
+        assert torch.equal(Q.view(of).cpu()[b, :, :q[b], rot:], bits[2][b, :, :q[b], rot:])
+        for got, want in zip(rows, bits):
+            assert torch.equal(got[b, :, :q[b]], want[b, :, :q[b]]) and (got[b, :, q[b]:] == 0).all()
+    assert sa.get_last_device_status() == 0
