@@ -25,6 +25,7 @@ _new_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
 _DTYPE = {torch.bfloat16: _lib.SA_BF16, torch.float32: _lib.SA_FP32}
 _INT = torch.int32
 _HEAD_4BIT = {36: 64, 72: 128}  # a token's bytes in a 4-bit page: head size
+_WIDEST = 0x7ffffffe  # a window: half of it is more than any position
 
 
 def _call(name, device, stream, *args):
@@ -153,8 +154,8 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     if global_idx is not None:
         _ints("global_idx", global_idx, dev, -1)
     n_global = 0 if global_idx is None else global_idx.numel()
-    if window > 0x7ffffffe:
-        window = 0x7ffffffe  # half of it is more than any position
+    if not 0 <= window <= _WIDEST:
+        window = _in_32_bits(window)
     max_pages = table[1]
     dt = _DTYPE[dtype]
     if workspace is None:
@@ -174,8 +175,13 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     return out
 
 
+def _in_32_bits(window):
+    """A window as the C calls take it, which see 32 bits of any number: the widest, or one that they refuse."""
+    return _WIDEST if window > 0 else -2
+
+
 @functools.lru_cache(maxsize=1024)  # the sizes and the device's number of SMs are all it depends on
-def _workspace_bytes(index, B, Hq, Hkv, m, d, page, max_pages, dtype, packed=False, window=0x7ffffffe, dilated=False,
+def _workspace_bytes(index, B, Hq, Hkv, m, d, page, max_pages, dtype, packed=False, window=_WIDEST, dilated=False,
                      n_global=0):
     sizes = (B, Hq, Hkv, m, d, page, max_pages)
     with torch.cuda.device(index):
@@ -184,7 +190,7 @@ def _workspace_bytes(index, B, Hq, Hkv, m, d, page, max_pages, dtype, packed=Fal
         return _lib.lib().sa_longformer_paged_workspace_bytes_ex(*sizes, window, dilated, n_global, dtype, packed)
 
 
-def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None, packed=False, window=0x7ffffffe,
+def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None, packed=False, window=_WIDEST,
                           dilated=False, n_global=0):
     """Scratch bytes of a longformer_attn_paged_fwd call of these sizes on `device` (default: the current one).
 
@@ -196,6 +202,8 @@ def paged_workspace_bytes(B, Hq, Hkv, m, d, page, max_pages, dtype, device=None,
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
+    if not 0 <= window <= _WIDEST:
+        window = _in_32_bits(window)
     return _workspace_bytes(dev.index, B, Hq, Hkv, m, d, page, max_pages, _DTYPE[dtype], bool(packed), window, bool(dilated),
                             n_global)
 

@@ -174,3 +174,26 @@ def test_what_is_not_rotated_keeps_its_bits(d, rot, interleaved, dtype):
         for got, want in zip(rows, bits):
             assert torch.equal(got[b, :, :q[b]], want[b, :, :q[b]]) and (got[b, :, q[b]:] == 0).all()
     assert sa.get_last_device_status() == 0
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_windows_past_32_bits(packed):
+    """A window whose lower 32 bits are those of a small or a negative one: all that is seen, and its scratch; or a refusal."""
+    lens, m = [9000], 1100
+    Q, K, V, values, table = make_cache4(98, 1, 2, 2, m, 64, 64, lens)
+    if not packed:
+        K, V = (torch.from_numpy(np.nan_to_num(v)).to(torch.bfloat16) for v in values)
+    args = dev(Q, K, V, table, ints(lens))
+    want = sa.longformer_attn_paged_fwd(*args, 20000)
+    sizes = (1, 2, 2, m, 64, 64, table.shape[1], torch.bfloat16)
+    all_of_it = sa.paged_workspace_bytes(*sizes, packed=packed)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 64, 2 ** 40, 2 ** 63 + 2):
+        n = sa.paged_workspace_bytes(*sizes, packed=packed, window=window)
+        assert n == all_of_it
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        assert torch.equal(sa.longformer_attn_paged_fwd(*args, window, workspace=ws), want)
+    for window in (-2, -2 ** 32, 64 - 2 ** 32, -2 ** 40):
+        with pytest.raises(sa.SparseAttnError):
+            sa.longformer_attn_paged_fwd(*args, window)
+        assert not packed or sa.paged_workspace_bytes(*sizes, packed=True, window=window) == 0
+    assert sa.get_last_device_status() == 0
