@@ -12,21 +12,29 @@ from oracle import paged4 as o4
 from oracle.paged import oracle_paged
 from paged4_util import attend4_and_check, bound4, make_cache4
 from paged_util import DT, dev, f64, ints
+from test_paged4_gpu import CASES
 
 pytestmark = pytest.mark.gpu
 
 
-def _converts_first(B, Hq, Hkv, m, d, page, width, window, dilated=False, n_global=0):
-    """Whether a bf16 call turns its pages into scratch of bf16 ones first: only then is its scratch as large as they are."""
-    n = sa.paged_workspace_bytes(B, Hq, Hkv, m, d, page, width, torch.bfloat16, packed=True, window=window, dilated=dilated,
-                                 n_global=n_global)
-    return n >= 2 * B * width * Hkv * page * d * 2
+def _converts_first(Q, K, V, table, lens, q, window, g=None, dil=None):
+    """Whether a bf16 call turns its pages into bf16 ones first: a launch more than over bf16 pages. (No call of up to three
+    tiles, four at d = 64, of 24 rows per key head does.)"""
+    m, group, d = Q.shape[2], Q.shape[1] // K.shape[1], Q.shape[3]
+    if group <= 24 and -(-m // (24 // group)) <= (4 if d == 64 else 3):
+        return False
+    counts = []
+    shape = K.shape[:3] + (d,)
+    for pools in ((K, V), [torch.zeros(shape, dtype=torch.bfloat16) for _ in "KV"]):
+        sa.longformer_attn_paged_fwd(*dev(Q, *pools, table, ints(lens)), window, *dev(ints(g)), dilation=dev(ints(dil))[0],
+                                     q_lens=dev(ints(q))[0])
+        counts.append(sa._lib.lib().sa_last_launch_count())
+    return counts[0] > counts[1]
 
 
-def _weights(Q, table, page, Hkv, window, dtype, **kw):
-    """How far off weights are: bf16 numbers (2^-8) only where the pages become bf16 ones first, halves (2^-11) else."""
-    B, Hq, m, d = Q.shape
-    first = dtype == "bf16" and _converts_first(B, Hq, Hkv, m, d, page, table.shape[1], window, **kw)
+def _weights(Q, K, V, table, lens, q, window, g=None, dil=None):
+    """How far off weights are: bf16 numbers (2^-8) only where the pages become bf16 ones first, else as the inputs' type says."""
+    first = Q.dtype is torch.bfloat16 and _converts_first(Q, K, V, table, lens, q, window, g, dil)
     return 2.0 ** -8 if first else None
 
 
@@ -61,7 +69,7 @@ def _one_above_many(m, group, d, n, top, dtype):
 def test_weights_far_below_the_largest(m, group, n, late, d, dtype):
     """2^-14 to 2^-30 of the largest: no coarser than 2^-32 of it, in whichever kernel."""
     Q, K, V, values, table = _one_above_many(m, group, d, n, n - m if late else 0, dtype)
-    attend4_and_check(Q, K, V, values, table, [n], None, 4 * n, dtype=dtype, weights=_weights(Q, table, 64, 1, 4 * n, dtype))
+    attend4_and_check(Q, K, V, values, table, [n], None, 4 * n, dtype=dtype, weights=_weights(Q, K, V, table, [n], None, 4 * n))
 
 
 @pytest.mark.parametrize("m,group,d,n", [(100, 1, 64, 9000), (50, 2, 128, 9000), (200, 1, 64, 6000), (200, 1, 128, 6000),
@@ -196,4 +204,144 @@ def test_windows_past_32_bits(packed):
         with pytest.raises(sa.SparseAttnError):
             sa.longformer_attn_paged_fwd(*args, window)
         assert not packed or sa.paged_workspace_bytes(*sizes, packed=True, window=window) == 0
+    assert sa.get_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ weights as fine as each path holds them
+@pytest.mark.parametrize("name", [k for k, c in CASES.items() if c[3] * (c[1] // c[2]) > 24])
+def test_weights_of_more_than_24_rows(name):
+    """Halves (2^-11) wherever the pages are not converted first, in further tiles of few rows and in chunks alike."""
+    B, Hq, Hkv, m, d, page, lens, q, window, g, dil = CASES[name]
+    Q, K, V, values, table = make_cache4(len(name), B, Hq, Hkv, m, d, page, lens)
+    w = _weights(Q, K, V, table, lens, q, window, g, dil)
+    attend4_and_check(Q, K, V, values, table, lens, q, window, g, dil, weights=w)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,group,n", [(30, 1, 2500), (72, 1, 2500), (40, 2, 3100), (100, 1, 2500), (3, 40, 2500), (120, 2, 1900)])
+def test_weights_of_more_than_24_rows_in_long_sweeps(m, group, n, d):
+    Q, K, V, values, table = make_cache4(m + n, 1, group, 1, m, d, 32, [n], sigma=1.0)
+    attend4_and_check(Q, K, V, values, table, [n], None, 2 * n, weights=_weights(Q, K, V, table, [n], None, 2 * n))
+
+
+# ------------------------------------------------------------------ queries
+# few rows; chunks of one tile and of two, which turn their queries into halves in place
+_ROWS = [(2, 2), (20, 1), (100, 1), (50, 2), (200, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,group", _ROWS)
+@pytest.mark.parametrize("above", [12, 24, 30])
+def test_queries_with_elements_far_above_the_others(above, m, group, d, dtype):
+    """In places where every key is zero, so that the ordinary elements, 2^-above of the largest, make the scores: no coarser
+    than 2^-38 of the largest (half of a half's smallest number, the largest being at least 2^13)."""
+    n = 300
+    Q, K, V, values, table = make_cache4(m + d + above, 1, group, 1, m, d, 16, [n], dtype)
+    codes, scales = (x.copy() for x in o4.parts(K.numpy(), d))
+    codes[..., :8] = 0
+    K, values[0] = torch.from_numpy(o4.joined(codes, scales)), o4.decode(codes, scales)
+    Q[..., :16] *= 2.0 ** above
+    O = sa.longformer_attn_paged_fwd(*dev(Q, K, V, table, ints([n])), 4 * n)
+    ref, A, S = oracle_paged(f64(Q), *values, table.numpy(), [n], None, 4 * n)
+    # the scores' error joins the others': of weight and sum alike
+    k = np.nansum(np.abs(values[0]), -1).max()
+    off = 2 * np.expm1(2.0 ** -38 * np.abs(f64(Q)).max(-1) * k / math.sqrt(d))
+    lim = bound4(ref, A, S, dtype, n, d, np.nanmax(np.abs(values[1])))
+    lim += (1 + 2.0 ** -8) * off[..., None] * A
+    assert (np.abs(f64(O) - ref) <= lim).all()
+    assert sa.get_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("m,group", _ROWS)
+@pytest.mark.parametrize("e", [-133, -120, -20, 60, 110, 127])
+def test_queries_of_every_exponent(e, m, group, dtype):
+    """Elements of 2^e: a third of the keys are opposite to them, the others zero where the queries are not. Those of large
+    queries get no weight, and all the others the same; of tiny ones every key does."""
+    n, d = 300, 64
+    Q, K, V, values, table = make_cache4(m + 200 + e, 1, group, 1, m, d, 16, [n], dtype)
+    codes, scales = (x.copy() for x in o4.parts(K.numpy(), d))
+    codes[..., :16] = 0
+    drop = np.arange(n) % 3 == 1
+    for j in np.flatnonzero(drop):
+        codes[int(table[0, j // 16]), 0, j % 16, :16] = 0xff  # -6, twice
+    scales[..., :2] = np.where(scales[..., :2] == 255, 255, 120)  # 1
+    K = torch.from_numpy(o4.joined(codes, scales))
+    g = torch.Generator().manual_seed(e + 200)
+    Q = torch.zeros(Q.shape, dtype=torch.float64)
+    Q[..., :32] = torch.ldexp(1 + torch.rand(1, group, m, 32, generator=g).double(), torch.tensor(e)) * (127 / 128)
+    Q = Q.to(DT[dtype])
+    O = f64(sa.longformer_attn_paged_fwd(*dev(Q, K, V, table, ints([n])), 4 * n))
+    assert torch.isfinite(Q).all() and (Q[..., :32] > 0).all()
+    v = np.stack([values[1][int(table[0, j // 16]), 0, j % 16] for j in range(n)])
+    # a mean of |v| <= 6 * 2^2 by equal weights, which are exact; tiny queries' scores of less than 2^-9 move them by 2^-8
+    tiny = e < 0
+    for t in range(m):
+        take = np.arange(n) <= n - m + t
+        take &= True if tiny else ~drop
+        want, size = v[take].mean(0), np.abs(v[take]).mean(0)
+        off = np.abs(O[0, :, t] - want)
+        assert (off <= 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7) + ((2.0 ** -7 if e == -20 else 0) + 2.0 ** -12) * size).all()
+    assert sa.get_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("m,group", _ROWS)
+def test_queries_that_are_infinite_or_nan_reach_their_own_rows_only(m, group, dtype):
+    n, d = 300, 64
+    Q, K, V, values, table = make_cache4(m + 300, 1, group, 1, m, d, 16, [n], dtype)
+    ref, A, S = oracle_paged(f64(Q), *values, table.numpy(), [n], None, 4 * n)
+    lim = bound4(ref, A, S, dtype, n, d, np.nanmax(np.abs(values[1])))
+    bad = Q.clone()
+    bad[0, 0, 0, 5], bad[0, group - 1, m // 2, 40], bad[0, 0, m - 1, 63] = float("inf"), float("nan"), -float("inf")
+    got = sa.longformer_attn_paged_fwd(*dev(bad, K, V, table, ints([n])), 4 * n)
+    spoiled = ~torch.isfinite(bad).all(-1).numpy()
+    assert np.isnan(f64(got)[spoiled]).all() and (np.abs(f64(got) - ref) <= lim)[~spoiled].all()
+    assert sa.get_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ pools of more than 2^32 bytes
+@pytest.mark.parametrize("d", [64, 128])
+def test_offsets_past_32_bits_everywhere(d):
+    """Tokens behind the first 2^32 bytes of both pools: every kernel of the attention, rows taken again, writing, reading."""
+    page = 128
+    P = (2 ** 32 + 2 ** 29) // (page * 9 * d // 16)
+    K = torch.zeros(sa.pool_shape_4bit(P, 1, page, d), dtype=torch.uint8, device="cuda")
+    V = torch.zeros_like(K)
+    # one row; several; tiles of few rows; chunks of one tile and of two; converted first; on the ordinary units
+    for m, Hq, n, dtype, simt in ((1, 1, 300, "bf16", 0), (1, 16, 300, "bf16", 0), (40, 1, 700, "bf16", 0), (9, 3, 300, "fp32", 0),
+                                  (100, 1, 300, "bf16", 0), (200, 1, 9000, "bf16", 0), (1100, 4, 9000, "bf16", 0),
+                                  (40, 1, 300, "fp32", 1)):
+        Q, Ks, Vs, _, table = make_cache4(8 + m, 1, Hq, 1, m, d, page, [n], dtype, spare=0)
+        codes, scales = (x.copy() for x in o4.parts(Vs.numpy(), d))
+        scales[int(table[0, (n - 1) // page]), 0, (n - 1) % page, 0] = 255  # the last token's: for its own row only
+        Vn = torch.from_numpy(o4.joined(codes, scales))
+        need = Ks.shape[0]
+        Qd, T, L = dev(Q, table, ints([n]))
+        far = T + (P - need)
+        assert (P - need) * Ks[0].numel() > 2 ** 32
+        assert dtype == "fp32" or _converts_first(Q, Ks, Vs, table, [n], None, 2 * n) == (m == 1100)
+        sa.set_option(sa.SA_OPT_FORCE_SIMT, simt)
+        try:
+            for v in (Vs, Vn):
+                K[-need:], V[-need:] = Ks.cuda(), v.cuda()
+                got = sa.longformer_attn_paged_fwd(Qd, K, V, far, L, 2 * n)
+                want = sa.longformer_attn_paged_fwd(Qd, Ks.cuda(), v.cuda(), T, L, 2 * n)
+                assert torch.equal(got.nan_to_num(77.0), want.nan_to_num(77.0))
+                assert torch.isnan(want).any() == (v is Vn) and (want[:, :, 0] != 0).any()
+        finally:
+            sa.set_option(sa.SA_OPT_FORCE_SIMT, 0)
+    for dtype, inter in ((torch.bfloat16, False), (torch.float32, True)):
+        kn, vn, qn = (torch.randn(1, 1, 50, d, device="cuda").to(dtype) for _ in "kvq")
+        rope = sa.rope_table(n, d)
+        small = sa.cache_append(kn, vn, Ks.cuda(), Vs.cuda(), T, L, rope=rope, interleaved=inter, Q_new=qn)
+        K[-need:], V[-need:] = Ks.cuda(), Vs.cuda()
+        large = sa.cache_append(kn, vn, K, V, far, L, rope=rope, interleaved=inter, Q_new=qn)
+        assert torch.equal(K[-need:], small[0]) and torch.equal(V[-need:], small[1]) and torch.equal(large[2], small[2])
+        assert not torch.equal(small[0].cpu(), Ks)
+        a, b = (sa.cache_read(x, y, t, L, n, dtype=dtype) for x, y, t in ((K, V, far), (*small[:2], T)))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and (a[0] != 0).any()
+    sa.cache_copy_pages(K, V, ints([P - 1]).cuda(), ints([P - 9]).cuda())
+    assert torch.equal(V[P - 9], V[P - 1]) and torch.equal(K[P - 9], K[P - 1])
     assert sa.get_last_device_status() == 0
