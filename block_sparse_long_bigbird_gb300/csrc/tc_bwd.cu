@@ -402,9 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
-        // the resident tile copy was issued at start-up; with no steps (or on
-        // abort) nothing else waits for it
-        if (total == 0 || !ok || *abort_flag) wait_drain(bar(C::B_TF), 0);
+        // the resident tile copy was issued at start-up; with no steps, or where
+        // a wait runs out (also after this loop), nothing else waits for it
+        wait_drain(bar(C::B_TF), 0);
     } else if (warp == 2 || warp == 3) {
         // ======================================================== chunk loaders
         // Warp 2 streams B1 (K or Q), warp 3 B2 (V or dO) and, in the key
@@ -436,11 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++arms[st];
         }
-        if (!ok || *abort_flag) {
-            // drain our copies in flight before the CTA leaves
-            for (int i = 0; i < C::NSTG; ++i)
-                if (arms[i]) wait_drain(bar(C::B_F + i), (arms[i] - 1) & 1);
-        }
+        // Our copies may still be in flight where a wait ran out, this role's or another's after this loop.
+        for (int i = 0; i < C::NSTG; ++i)
+            if (arms[i]) wait_drain(bar(C::B_F + i), (arms[i] - 1) & 1);
     } else if (warp == 1) {
         // ======================================================== MMA issuer
         // The whole warp runs the loop and the waits (so the descriptors and

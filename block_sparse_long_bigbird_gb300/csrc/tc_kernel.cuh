@@ -943,14 +943,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             cur = nxt;
             slow_cur = slow_nxt;
         }
-        if (!ok && lane == 0) {  // abort: wait for the copies this tile still has in flight
-            for (uint32_t i = 0; i < (uint32_t)C::KST && i < issued; ++i) {
-                const uint32_t arms = (issued - 1 - i) / C::KST + 1;  // copies into stage i
-                wait_drain(bar(C::B_KF + i), (arms - 1) & 1);
-                wait_drain(bar(C::B_VF + i), (arms - 1) & 1);
-            }
-            if (qcnt && q_tma_last) wait_drain(bar(C::B_QF + (qcnt - 1) % C::NQ), ((qcnt - 1) / C::NQ) & 1);
+        // Copies of this tile may still be in flight where a wait ran out: this role's, or another's after this
+        // one has seen the last unit. Otherwise their data is long there.
+        if (lane < C::KST && (uint32_t)lane < issued) {
+            const uint32_t arms = (issued - 1 - (uint32_t)lane) / C::KST + 1;  // copies into stage `lane`
+            wait_drain(bar(C::B_KF + lane), (arms - 1) & 1);
+            wait_drain(bar(C::B_VF + lane), (arms - 1) & 1);
         }
+        if (qcnt && q_tma_last) wait_drain(bar(C::B_QF + (qcnt - 1) % C::NQ), ((qcnt - 1) / C::NQ) & 1);
     } else if (role == 1) {
         // ================================================================ MMA issuer (tile x)
         // The whole warp runs the loop and the waits, so descriptors and TMEM
@@ -1077,7 +1077,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 ++arms[st];
             }
         }
-        if (!ok && lane == 0)  // abort: wait for the copies still in flight
+        if (lane == 0)  // in flight where a wait ran out, this role's or another's
             for (int i = 0; i < C::KST; ++i)
                 if (arms[i]) wait_drain(bar(bf + i), (arms[i] - 1) & 1);
     } else if (role == 2) {

@@ -118,3 +118,36 @@ def test_calls_on_two_event_ordered_streams_share_the_scratch():
     for k, o in enumerate(outs):
         assert torch.equal(o, alone[k % len(probs)]), f"call {k} differs from the same call made alone"
     assert np.isfinite(outs[0].float().cpu().numpy()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bigbird", "longformer"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_waits_that_run_out_after_the_loader_has_seen_its_last_unit(d, kind):
+    # A unit or less to a CTA: the producer has nothing left to do while its copies, out of cold
+    # memory, are still in flight and the other roles give up. No copy may outlive its CTA.
+    Q, K, V = (t.cuda() for t in make_qkv(1, 2, 512, d, "bf16", cfg_id=121))
+    table = pattern_table(0, 2, 512, 64, 2, 3, 3).cuda()
+
+    def call():
+        if kind == "bigbird":
+            return sa.bigbird_attn_fwd(Q, K, V, 64, 2, 3, 3, table)
+        return sa.longformer_attn_fwd(Q, K, V, 128, None)
+
+    want = call()
+    cold = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")  # larger than the L2
+    torch.cuda.synchronize()
+    assert sa.get_last_device_status() == 0
+    for _ in range(4):
+        sa.set_option(sa.SA_OPT_WAIT_LIMIT, 1)
+        try:
+            cold.zero_()
+            call()
+            torch.cuda.synchronize()
+        finally:
+            sa.set_option(sa.SA_OPT_WAIT_LIMIT, 0)
+        got = call()
+        torch.cuda.synchronize()
+        assert sa.get_last_device_status() in (_lib.SA_OK, _lib.SA_ERR_TIMEOUT)
+        assert torch.equal(got, want)
+    assert sa.get_last_device_status() == 0
