@@ -25,7 +25,8 @@
 //     power of two leaves with the softmax's factor.
 //   * Weights in halves: relative 2^-11, and 2^-32 of the largest; with fp32 queries the sum
 //     of two (2^-22). They are kept up to 2^15, so that small ones are far from a half's
-//     smallest number. Sums of weights and products are fp32.
+//     smallest number. Sums of weights and products are fp32, with fp32
+//     queries rounded to the nearest every 16 keys.
 // A warp takes 64 keys (d = 64) or 32 at a time (page numbers by 16) into a ring of its
 // own by cp.async, whole pieces of 16 bytes, two items ahead. The pieces are
 // stored so that neither the reads of K (a row per four lanes) nor those of V (four rows
@@ -36,7 +37,7 @@
 //
 // Measured (16 sequences of 32768 keys, 8 key heads; the same over bf16 pages in brackets): d =
 // 128, 1 to 4 rows 121 us, 5.0 TB/s (320), 16 rows 175 (324), 24 rows 218 (336); d = 64 74, 105 and
-// 121 us (170, 175, 190), the first at 4.1 TB/s; fp32, 8 rows, d = 128 165 us. A plain copy: 6.8
+// 121 us (170, 175, 190), the first at 4.1 TB/s; fp32, 8 rows, d = 128 172 us. A plain copy: 6.8
 // TB/s. 32 keys of one 8-row tile take 640 instructions at d = 128, 256 of them conversions and
 // scales; two thirds of the issue slots are used, the rest is lost to results that are waited
 // for (1.3 of 7 clocks a warp and issue), the conversions' pipe (1.0) and instructions on their way
@@ -500,11 +501,21 @@ __global__ void __launch_bounds__(W * 32, Few4<T, D, NT, W>::ctas) paged_few4(co
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int z = 0; z < PARTS; ++z)
-                                    mma16816(acc[nt][4 * x + j], a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j],
-                                             wt[u][nt][z][0], wt[u][nt][z][1]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float(&to)[4] = acc[nt][4 * x + j];
+                                if constexpr (PARTS == 2) {
+                                    // Matrix instructions cut off what they do not hold, and long sums in them lean: 32768
+                                    // keys were 75 u off (u = 2^-24; 12 u so, at 4% of the time, 14% for 16 rows at d =
+                                    // 128, which spill). So they sum 16 keys, and those sums are added as floats are.
+                                    float t[4];
+                                    mma16816_0(t, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j], wt[u][nt][0][0], wt[u][nt][0][1]);
+                                    mma16816(t, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j], wt[u][nt][1][0], wt[u][nt][1][1]);
+                                    ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(to[0], to[1]), ptx::f2_pack(t[0], t[1])), to[0], to[1]);
+                                    ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(to[2], to[3]), ptx::f2_pack(t[2], t[3])), to[2], to[3]);
+                                } else {
+                                    mma16816(to, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j], wt[u][nt][0][0], wt[u][nt][0][1]);
+                                }
+                            }
                     }
                 }
             }

@@ -345,3 +345,39 @@ def test_offsets_past_32_bits_everywhere(d):
     sa.cache_copy_pages(K, V, ints([P - 1]).cuda(), ints([P - 9]).cuda())
     assert torch.equal(V[P - 9], V[P - 1]) and torch.equal(K[P - 9], K[P - 1])
     assert sa.get_last_device_status() == 0
+
+
+# ------------------------------------------------------------------ long sums in fp32
+@pytest.mark.parametrize("d,group", [(64, 1), (64, 20), (128, 1), (128, 12)])
+def test_long_sums_in_fp32(d, group):
+    """Relative error of the results' root mean square, over sequences so many and long that a warp sums n / 8 keys.
+
+    u = 2^-24; a rounding to the nearest is off by u / sqrt(3) of its result in the mean square. Values of either sign, so
+    that sums grow as the root of their terms. A result: 256 additions of 16 keys' sums, u sqrt(256 / 6) = 6.5 u. The weights'
+    sum: 512 additions of a lane, growing evenly, u sqrt(512) / 3 = 7.5 u. Scores, of mean square 1.3: each of d = 128 products
+    off by 2 u at most (two halves, the sum's last place) at random, 15 u. The exponential 4 u, weights as two halves 1 u.
+    Together 19 u; as much again, and some for what leans: 45 u. (Sums of all keys in the matrix instructions' own
+    accumulators, which cut off: 74 to 81 u.)
+    """
+    B, Hkv, n, page = 16, 8, 32768, 128
+    g = torch.Generator(device="cuda").manual_seed(d + group)
+    P, codes = B * n // page, page * d // 2
+    K, V = (torch.randint(0, 256, sa.pool_shape_4bit(P, Hkv, page, d), generator=g, dtype=torch.uint8, device="cuda")
+            for _ in "KV")
+    for x in (K, V):  # one scale: the numbers themselves, of mean square 8.6
+        x.view(P, Hkv, -1)[..., codes:] = 120
+    table = torch.randperm(P, generator=g, device="cuda").to(torch.int32).reshape(B, -1).contiguous()
+    Q = torch.randn(B, Hkv * group, 1, d, generator=g, device="cuda") / 6.7 ** 0.5
+    O = sa.longformer_attn_paged_fwd(Q, K, V, table, torch.full((B,), n, dtype=torch.int32, device="cuda"), 2 * n)
+    one = torch.tensor(o4.MAGNITUDES, device="cuda")
+    value = torch.cat([one, -one])
+    off = size = 0.0
+    for b, h in ((0, 0), (7, 3), (B - 1, Hkv - 1)):
+        k, v = (x.view(P, Hkv, -1)[table[b].long(), h, :codes].reshape(-1, d // 2).int() for x in (K, V))
+        k, v = (torch.stack([value[x & 15], value[x >> 4]], -1).reshape(n, d) for x in (k, v))
+        q = Q[b, h * group:(h + 1) * group, 0].double()
+        want = torch.softmax(q @ k.T / math.sqrt(d), -1) @ v
+        off += float(((O[b, h * group:(h + 1) * group, 0] - want) ** 2).sum())
+        size += float((want ** 2).sum())
+    assert math.sqrt(off / size) <= 45 * 2.0 ** -24
+    assert sa.get_last_device_status() == 0
