@@ -24,8 +24,9 @@
 //     ones are the sum of two halves (2^-22 of each, or 2^-38 of the largest). The
 //     power of two leaves with the softmax's factor.
 //   * Weights in halves: relative 2^-11, and 2^-32 of the largest; with fp32 queries the sum
-//     of two (2^-22). They are kept up to 2^15, so that small ones are far from a half's
-//     smallest number. Sums of weights and products are fp32, with fp32
+//     of two (2^-22, and 2^-39). They are kept up to 2^15, so that small ones are far from a half's
+//     smallest number: 2^7 at the reference, or 2^14 in fp32, where sums are rescaled as soon as a maximum
+//     doubles the weights (1% of the time). Sums of weights and products are fp32, with fp32
 //     queries rounded to the nearest every 16 keys.
 // A warp takes 64 keys (d = 64) or 32 at a time (page numbers by 16) into a ring of its
 // own by cp.async, whole pieces of 16 bytes, two items ahead. The pieces are
@@ -37,7 +38,7 @@
 //
 // Measured (16 sequences of 32768 keys, 8 key heads; the same over bf16 pages in brackets): d =
 // 128, 1 to 4 rows 121 us, 5.0 TB/s (320), 16 rows 175 (324), 24 rows 218 (336); d = 64 74, 105 and
-// 121 us (170, 175, 190), the first at 4.1 TB/s; fp32, 8 rows, d = 128 172 us. A plain copy: 6.8
+// 121 us (170, 175, 190), the first at 4.1 TB/s; fp32, 8 rows, d = 128 171 us. A plain copy: 6.8
 // TB/s. 32 keys of one 8-row tile take 640 instructions at d = 128, 256 of them conversions and
 // scales; two thirds of the issue slots are used, the rest is lost to results that are waited
 // for (1.3 of 7 clocks a warp and issue), the conversions' pipe (1.0) and instructions on their way
@@ -54,8 +55,6 @@
 namespace sa {
 namespace {
 
-constexpr float kGrow = 8.f;    // growth of a maximum (log2) that rescales the sums
-constexpr float kAbove = 7.f;   // weights are 2^kAbove at the running maximum
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -94,6 +93,8 @@ __device__ __forceinline__ uint32_t low_of(uint32_t a, uint32_t b) {
 template <typename T, int D, int NT, int W>
 struct Few4 {
     static constexpr int parts = sizeof(T) == 4 ? 2 : 1;     // halves to a query element, and to a weight
+    static constexpr float grow = parts == 2 ? 1.f : 8.f;    // growth of a maximum (log2) that rescales the sums
+    static constexpr float above = 15.f - grow;              // weights are 2^above at the reference, and up to 2^15
     static constexpr int ctas = paged_few4_ctas(D, 8 * NT, sizeof(T) == 4, W);  // per SM
     static constexpr int keys = D == 64 ? 64 : 32;           // a warp takes at a time
     static constexpr int codes = keys * D / 2, scales = keys * D / 16;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(W * 32, Few4<T, D, NT, W>::ctas) paged_few4(co
 #pragma unroll
                         for (int u = 1; u < SUB; ++u) t = ptx::fmax3(t, s[u][nt][x], s[u][nt][2 + x]);
                         top[nt][x] = t * sl[nt][x];
-                        up |= top[nt][x] > m[nt][x] + kGrow;
+                        up |= top[nt][x] > m[nt][x] + C::grow;
                     }
                 if (__any_sync(kAllLanes, up)) {
 #pragma unroll
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(W * 32, Few4<T, D, NT, W>::ctas) paged_few4(co
                 for (int nt = 0; nt < NT; ++nt) {
                     float ref[2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) ref[x] = m[nt][x] == -CUDART_INF_F ? 0.f : kAbove - m[nt][x];
+                    for (int x = 0; x < 2; ++x) ref[x] = m[nt][x] == -CUDART_INF_F ? 0.f : C::above - m[nt][x];
                     const uint64_t sl2 = ptx::f2_pack(sl[nt][0], sl[nt][1]), ref2 = ptx::f2_pack(ref[0], ref[1]);
                     uint64_t sum = ptx::f2_pack(l[nt][0], l[nt][1]);
 #pragma unroll
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(W * 32, Few4<T, D, NT, W>::ctas) paged_few4(co
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
                 if (n == 0) {
-                    jm[8 * nt + 2 * quad + x] = m[nt][x] - kAbove;  // what the weights are relative to
+                    jm[8 * nt + 2 * quad + x] = m[nt][x] - C::above;  // what the weights are relative to
                     jm[8 * NT + 8 * nt + 2 * quad + x] = sum;
                 }
             }

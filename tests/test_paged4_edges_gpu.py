@@ -72,6 +72,18 @@ def test_weights_far_below_the_largest(m, group, n, late, d, dtype):
     attend4_and_check(Q, K, V, values, table, [n], None, 4 * n, dtype=dtype, weights=_weights(Q, K, V, table, [n], None, 4 * n))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,group,n,late", [(1, 1, 700, False), (1, 8, 5000, True), (16, 1, 3000, True), (100, 1, 1500, False),
+                                            (2, 12, 9000, True)])
+def test_weights_far_below_the_largest_in_fp32(m, group, n, late, d):
+    """As above, no coarser than 2^-39 of the largest."""
+    Q, K, V, values, table = _one_above_many(m, group, d, n, n - m if late else 0, "fp32")
+    O = f64(sa.longformer_attn_paged_fwd(*dev(Q, K, V, table, ints([n])), 4 * n))
+    ref, A, S = oracle_paged(f64(Q), *values, table.numpy(), [n], None, 4 * n)
+    lim = bound4(ref, A, S, "fp32", n, d, 2.0 ** -7 * np.nanmax(np.abs(values[1])))  # that much finer than 2^-32
+    assert (np.abs(O - ref) <= lim).all()
+
+
 @pytest.mark.parametrize("m,group,d,n", [(100, 1, 64, 9000), (50, 2, 128, 9000), (200, 1, 64, 6000), (200, 1, 128, 6000),
                                          (20, 1, 64, 9000), (4, 4, 128, 9000)])
 def test_parts_that_are_taken_again_join_those_that_are_not(m, group, d, n):
