@@ -21,9 +21,9 @@ constexpr int kRowsBf16 = 1, kRowsFp32 = 8, kFewRows = 24;
 // Chunks over 4-bit pages may turn them into bf16 ones first (paged_unpack): what a step of
 // 256 rows and 64 keys then takes less, in ns (d = 64, 128), and what a 64-key block of a key
 // head, read and written, and the launch cost; and the most scratch that is asked for. 4096
-// tokens over 16384 keys, 32 query and 4 key heads, take 841 us with and 1038 without
-// (d = 128: 840 and 1382), with a window of 512 58 and 65 (67 and 77); 256 tokens of 4
-// sequences, 8 heads, 126 and 106 (169 and 128).
+// tokens over 16384 keys, 32 query and 4 key heads, take 831 us with and 1044 without
+// (d = 128: 831 and 1345), with a window of 512 56 and 63 (65 and 77); 256 tokens of 4
+// sequences, 8 heads, 122 and 104 (171 and 130). profiles/paged_unpack_rule.md has 288 sizes.
 constexpr int kUnpackStep[2] = {260, 700}, kUnpackBlock[2] = {2, 5}, kUnpackLaunch = 2000;
 constexpr size_t kUnpackBytes = 1ull << 30;
 
@@ -125,7 +125,8 @@ PagedKernel paged_shape(PagedProblem &p, sa_dtype dtype, bool force_simt, int nu
         longest = band < longest ? band : longest;
     }
     p.unpack = 0;
-    if (p.packed && kind == kPagedTc && 2 * paged_unpack_pool_bytes(p) <= kUnpackBytes && (long long)p.B * p.max_pages * p.Hkv <= 0x7fffffffll) {
+    if (p.packed && kind == kPagedTc && 2 * paged_unpack_pool_bytes(p) <= kUnpackBytes &&
+        (long long)p.B * p.max_pages * p.Hkv <= 0x7fffffffll) {
         // Dilations, which are the device's to know, make walks and reach longer alike.
         const long long band = ((long long)p.half + p.tpt + 63) >> 6, near = ((long long)p.half + p.m + 63) >> 6;
         const double steps = (double)tiles * (double)(band < row ? band : row) / num_sms;
@@ -291,7 +292,8 @@ sa_status longformer_attn_paged_fwd(const void *Q, const void *K_pages, const vo
 
 size_t sa_longformer_paged_workspace_bytes_ex(int B, int Hq, int Hkv, int m, int d, int page, int max_pages, int window,
                                               int dilated, int n_global, sa_dtype dtype, sa_pool pool) {
-    if ((dtype != SA_BF16 && dtype != SA_FP32) || (pool != SA_POOL_PLAIN && pool != SA_POOL_4BIT) || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
+    if ((dtype != SA_BF16 && dtype != SA_FP32) || (pool != SA_POOL_PLAIN && pool != SA_POOL_4BIT)) return 0;
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
         Hq / Hkv > sa::kPagedMaxGroup || Hkv > sa::kPagedMaxHeads || n_global < 0 || n_global > sa::kPagedMaxGlobal ||
         window < 0 || sizes_ok(B, Hkv, m, d, page, 1, max_pages) != SA_OK)
         return 0;

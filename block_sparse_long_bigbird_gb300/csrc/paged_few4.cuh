@@ -509,12 +509,17 @@ __global__ void __launch_bounds__(W * 32, Few4<T, D, NT, W>::ctas) paged_few4(co
                                     // keys were 75 u off (u = 2^-24; 12 u so, at 4% of the time, 14% for 16 rows at d =
                                     // 128, which spill). So they sum 16 keys, and those sums are added as floats are.
                                     float t[4];
-                                    mma16816_0(t, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j], wt[u][nt][0][0], wt[u][nt][0][1]);
-                                    mma16816(t, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j], wt[u][nt][1][0], wt[u][nt][1][1]);
-                                    ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(to[0], to[1]), ptx::f2_pack(t[0], t[1])), to[0], to[1]);
-                                    ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(to[2], to[3]), ptx::f2_pack(t[2], t[3])), to[2], to[3]);
+                                    mma16816_0(t, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j],
+                                               wt[u][nt][0][0], wt[u][nt][0][1]);
+                                    mma16816(t, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j],
+                                             wt[u][nt][1][0], wt[u][nt][1][1]);
+#pragma unroll
+                                    for (int i = 0; i < 4; i += 2)
+                                        ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(to[i], to[i + 1]), ptx::f2_pack(t[i], t[i + 1])),
+                                                       to[i], to[i + 1]);
                                 } else {
-                                    mma16816(to, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j], wt[u][nt][0][0], wt[u][nt][0][1]);
+                                    mma16816(to, a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j],
+                                             wt[u][nt][0][0], wt[u][nt][0][1]);
                                 }
                             }
                     }

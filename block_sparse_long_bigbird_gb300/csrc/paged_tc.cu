@@ -36,14 +36,14 @@
 // clocks, twice as long as they need alone, as little of their latency is hidden (one
 // such warp per scheduler; registers are out). Where a CTA takes many such steps the pages are
 // converted first instead (paged_unpack; kUnpackStep holds the rule): 4096 tokens over 32768
-// keys as below take 838 us, 1332 with converters. Those stay for few tiles and short windows (2048
+// keys as below take 822 us, 1332 with converters. Those stay for few tiles and short windows (2048
 // tokens of 4 sequences, window 512, 8 heads of 64: 55 us, 66 with the pages converted
 // first, 50 over bf16 pages) and where the scratch would be too large.
 // Roles' waits are bounded; on expiry the CTA latches SA_ERR_TIMEOUT, drains
 // its copies and MMAs, frees TMEM and exits.
 //
 // Measured: 4096 tokens at the end of 32768 keys, 16 query and 4 key heads, d =
-// 128: 826 us, 1250 TFLOP/s (0.63 of the measured bf16 rate); with as many key as
+// 128: 810 us, 1273 TFLOP/s (0.66 of the measured bf16 rate); with as many key as
 // query heads, 2 x 2048 tokens over 16384 keys: d = 128 444 us, 1160 TFLOP/s, d = 64
 // 423 us, 610 TFLOP/s. A 64-key block of two tiles takes 1.0 us whatever d is: the
 // softmax bounds it (16384 exponentials per block, one thread per row), not the
@@ -113,7 +113,9 @@ struct TcCfg {
     static constexpr int BAR_OFF = ST_OFF + NST * TILE;
     static constexpr int B_KF = 0, B_KE = B_KF + NST, B_IF = B_KE + NST, B_IE = B_IF + kSI, B_QF = B_IE + kSI,
                          B_QE = B_QF + 1, B_SF = B_QE + 1, B_PF = B_SF + 4, B_PD = B_PF + 4, B_OF = B_PD + 2, B_OE = B_OF + 2,
-                         B_MF = B_OE + 2, B_ME = B_MF + 1, B_UF = B_ME + 1, B_UE = B_UF + kNU, B_DRAIN = B_UE + kNU, B_RF = B_DRAIN + 2, B_RE = B_RF + (P4 ? kPR : 0), B_QR = B_RE + (P4 ? kPR : 0), B_COUNT = B_QR + (P4 ? 2 : 0);
+                         B_MF = B_OE + 2, B_ME = B_MF + 1, B_UF = B_ME + 1, B_UE = B_UF + kNU, B_DRAIN = B_UE + kNU,
+                         B_RF = B_DRAIN + 2, B_RE = B_RF + (P4 ? kPR : 0), B_QR = B_RE + (P4 ? kPR : 0),
+                         B_COUNT = B_QR + (P4 ? 2 : 0);
     static constexpr int REC_OFF = (BAR_OFF + B_COUNT * 8 + 15) & ~15;
     static constexpr int UNIT_OFF = REC_OFF + kSI * (int)sizeof(StepRec);
     static constexpr int MISC_OFF = UNIT_OFF + kNU * (int)sizeof(UnitRec);

@@ -135,7 +135,8 @@ def longformer_attn_paged_fwd(Q, K_pages, V_pages, block_table, seq_lens, window
     packed = kind is torch.uint8
     if not (len(shape) == len(pool) == 4 and V_pages.shape == pool and dtype in _DTYPE and V_pages.dtype is kind
             and (shape[3] == pool[3] and kind is dtype if not packed else _HEAD_4BIT.get(pool[3]) == shape[3])
-            and block_table.dtype is _INT and seq_lens.dtype is _INT and K_pages.device == dev and V_pages.device == dev and block_table.device == dev and seq_lens.device == dev
+            and block_table.dtype is _INT and seq_lens.dtype is _INT and K_pages.device == dev and V_pages.device == dev
+            and block_table.device == dev and seq_lens.device == dev
             and Q.is_cuda and Q.is_contiguous() and K_pages.is_contiguous() and V_pages.is_contiguous()
             and block_table.is_contiguous() and seq_lens.is_contiguous()
             and len(table) == 2 and table[0] == shape[0] and seq_lens.shape == shape[:1]):
@@ -288,7 +289,8 @@ def cache_read(K_pages, V_pages, block_table, seq_lens, m, q_lens=None, dtype=No
     """
     pool, table, kind, dev = K_pages.shape, block_table.shape, K_pages.dtype, K_pages.device
     packed = kind is torch.uint8
-    if not (len(pool) == 4 and V_pages.shape == pool and V_pages.dtype is kind and (kind in _DTYPE or packed and pool[3] in _HEAD_4BIT)
+    if not (len(pool) == 4 and V_pages.shape == pool and V_pages.dtype is kind
+            and (kind in _DTYPE or packed and pool[3] in _HEAD_4BIT)
             and V_pages.device == dev and block_table.device == dev and seq_lens.device == dev and block_table.dtype is _INT
             and seq_lens.dtype is _INT and K_pages.is_cuda and K_pages.is_contiguous() and V_pages.is_contiguous()
             and block_table.is_contiguous() and seq_lens.is_contiguous() and len(table) == 2 and seq_lens.shape == table[:1]):

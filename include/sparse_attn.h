@@ -492,8 +492,8 @@ sa_status bigbird_attn_fwd_noalloc(const void *Q, const void *K, const void *V, 
  * A code is a sign (its highest bit) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6; a scale
  * is the bits 7 to 14 of a half-precision number, at most 10240 (226), or 255: the
  * group's elements are NaN. (227 to 254 are not written and not to be used.)
- * An element is code x scale: 6 significant bits, exact in bf16 and fp32. The calls that move pages take such pools with
- * page_bytes = Hkv * page * 9 * d / 16.
+ * An element is code x scale: 6 significant bits, exact in bf16 and fp32. The
+ * calls that move pages take such pools with page_bytes = Hkv * page * 9 * d / 16.
  */
 typedef enum { SA_POOL_PLAIN = 0, SA_POOL_4BIT = 1 } sa_pool;
 
@@ -552,15 +552,23 @@ size_t sa_longformer_paged_workspace_bytes(int B, int Hq, int Hkv, int m, int d,
 
 /* longformer_attn_paged_fwd_ex - the same over either kind of pool. Of a 4-bit
  * pool every key and value counts as the number it stands for; Q and O are of
- * `dtype`. Numerics: scores, softmax and sums in fp32. In bf16 the weights are
- * rounded to halves (relative 2^-11, no finer than 2^-32 of the largest), in chunks
- * that turn the pages into bf16 ones first to bf16 (2^-8). In fp32 queries and
- * weights are the sums of two halves each (relative 2^-22) with up to 24 query heads
- * per key head (d = 128: 16), and fp32 throughout with more.
+ * `dtype`. Numerics: scores, softmax and sums in fp32.
+ *   bf16: the weights are rounded to halves: relative 2^-11, no finer than 2^-32 of
+ *     the largest. So are the queries, exact down to 2^-28 of their row's largest
+ *     element and no finer than 2^-38 of it. Some calls with more than 24 rows per
+ *     key head turn the pages into bf16 ones first: queries as they are, weights
+ *     rounded to bf16 (2^-8). Which ones goes by the sizes, the window and the
+ *     table's width (the scratch below), so such a call may answer in other bits
+ *     with a wider table.
+ *   fp32: with up to 24 query heads per key head (d = 128: 16) queries and weights
+ *     are the sums of two halves each: relative 2^-22, queries no finer than 2^-38
+ *     of their row's largest element, weights no finer than 2^-39 of the largest.
+ *     With more, fp32 throughout.
+ *   SA_OPT_FORCE_SIMT: fp32 throughout.
  * Scratch: sa_longformer_paged_workspace_bytes_ex, for this window, n_global
  * and whether there are dilations (of a plain pool what the call without _ex asks
- * for). Long chunks over a 4-bit pool ask for room for the pages as bf16 ones too,
- * up to 1 GiB; where that would not do they go without. */
+ * for). Chunks that turn their pages into bf16 ones first ask for room for all that
+ * the table has places for, up to 1 GiB; where that would not do they go without. */
 sa_status longformer_attn_paged_fwd_ex(const void *Q, const void *K_pages, const void *V_pages, void *O,
                                        int B, int Hq, int Hkv, int m, int d,
                                        int page, int num_pages, int max_pages,
@@ -597,7 +605,8 @@ sa_status sa_cache_append(const void *K_new, const void *V_new, void *K_pages, v
  *   and s = rope_sin[p][i]; elements from rot on stay. Pair i is elements (i, i + rot / 2),
  *   or (2 i, 2 i + 1) with interleaved = 1. The keys are rotated, and queries
  *   Q_new [B][Hq][m][d] into Q_out, which may be Q_new; rows t >= q_lens[b] of Q_out are
- *   zeros. Hq = 0: no queries (with rot = 0 there are none). Values stay.
+ *   zeros. Hq = 0: no queries (with rot = 0 there are none). Values stay. In plain
+ *   pools and Q_out all that is not rotated keeps its bits.
  *   rope_cos, rope_sin: DEVICE fp32 [rope_len][rot / 2], 16-byte aligned. A token
  *   at a position past rope_len is dropped, its query row zeros, and latches
  *   SA_ERR_BAD_INDEX. Before it is rounded to dtype the result is off by 2^-23 of
@@ -607,8 +616,9 @@ sa_status sa_cache_append(const void *K_new, const void *V_new, void *K_pages, v
  *   number with 4 significant bits (or the nearest multiple of 2^-17), at most
  *   10240, a code the nearest to element / scale; halfway cases to the even
  *   code. Magnitudes past 61440 become that; a group that holds an infinity or
- *   NaN reads as NaN. K_new as rounded to dtype is what codes are chosen for, so a
- *   4-bit pool holds the 4-bit form of what a plain pool would.
+ *   NaN reads as NaN. Codes are chosen for the elements as rounded to dtype, rotated
+ *   ones rounded once. (A plain pool's rotated bf16 elements, rounded by way of fp32,
+ *   are the neighbouring number in some 2 of 100000.)
  * No two of K_new, V_new, Q_out, K_pages, V_pages may be the same.
  * Errors: as for sa_cache_append.
  */
